@@ -37,6 +37,19 @@ MXG_FLAG_C_MMAJOR = 128
 MXG_FLAG_A_MMAJOR = 256
 MXG_FLAG_B_NMAJOR = 512
 
+MXG_DT_F32 = 0
+MXG_DT_BF16 = 1
+MXG_DT_F16 = 2
+MXG_QUANT_SQUARE = 1
+MXG_QUANT_POW2 = 2
+MXG_B128_B_ROWS = 1
+MXG_B128_ACCUMULATE = 2
+MXG_ROPE_HALF = 0
+MXG_ROPE_INTERLEAVED = 1
+MXG_ROPE_INTERLEAVED_TO_HALF = 2
+MXG_ROPE_TRANSPOSE = 1
+MXG_ROPE_POS64 = 2
+
 MXG_OK = 0
 MXG_ERR_NULL = -1
 MXG_ERR_SHAPE = -2
@@ -53,7 +66,9 @@ EXPORTED = ("mxgemm_amax", "mxgemm_amax_ex", "mxgemm_amax_reset", "mxgemm_check_
             "mxgemm_sf_bytes", "mxgemm_launch_config", "mxgemm_strerror", "mxgemm_mx_quantize",
             "mxgemm_sf_rowwise_to_atoms", "mxgemm_plan_init", "mxgemm_plan_execute", "mxgemm_codes_to_kmajor",
             "mxgemm_proj_rope_mxfp8", "mxgemm_gemm_rope_mxfp8", "mxgemm_projection_workspace_bytes",
-            "mxgemm_projection_mxfp8", "mxgemm_projection_mxfp8_noalloc")
+            "mxgemm_projection_mxfp8", "mxgemm_projection_mxfp8_noalloc", "mxgemm_block128_quantize", "mxgemm_block128",
+            "mxgemm_block128_workspace_bytes", "mxgemm_rope", "mxgemm_qk_norm_rope", "mxgemm_qk_norm_rope_backward",
+            "mxgemm_qk_norm_rope_backward_workspace_bytes")
 
 
 class MxgemmError(Exception):
@@ -113,6 +128,21 @@ def _load():
     lib.mxgemm_projection_mxfp8.restype = ci
     lib.mxgemm_projection_mxfp8_noalloc.argtypes = [vp] * 10 + [i64] * 5 + [vp]
     lib.mxgemm_projection_mxfp8_noalloc.restype = ci
+    cz, cf, strides = ctypes.c_size_t, ctypes.c_float, ctypes.POINTER(i64)
+    lib.mxgemm_block128_quantize.argtypes = [vp, i64, vp, vp, vp, vp, i64, i64, i64, ci, ci, cu, vp]
+    lib.mxgemm_block128_quantize.restype = ci
+    lib.mxgemm_block128.argtypes = [vp] * 5 + [i64] * 5 + [ci, ci, ci, cu, vp, cz, vp]
+    lib.mxgemm_block128.restype = ci
+    lib.mxgemm_block128_workspace_bytes.argtypes = [i64] * 4 + [ci]
+    lib.mxgemm_block128_workspace_bytes.restype = cz
+    lib.mxgemm_rope.argtypes = [vp] * 5 + [strides] + [i64] * 6 + [ci, ci, cu, vp]
+    lib.mxgemm_rope.restype = ci
+    lib.mxgemm_qk_norm_rope.argtypes = [vp] * 9 + [strides] + [i64] * 7 + [cf, ci, ci, ci, cu, vp]
+    lib.mxgemm_qk_norm_rope.restype = ci
+    lib.mxgemm_qk_norm_rope_backward.argtypes = [vp] * 13 + [strides] + [i64] * 7 + [cf, ci, ci, ci, cu, vp, cz, vp]
+    lib.mxgemm_qk_norm_rope_backward.restype = ci
+    lib.mxgemm_qk_norm_rope_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.mxgemm_qk_norm_rope_backward_workspace_bytes.restype = cz
     return lib
 
 
@@ -456,6 +486,357 @@ def mx_quantize(x, sf_vec_size=32, fmt=MXG_FMT_E4M3, q=None, sf=None, stream=Non
     return q, sf
 
 
+# --- block-128 quantisation and product, rotary positions, per-head norm -----------
+
+_ROPE_LAYOUTS = {"half": MXG_ROPE_HALF, "interleaved": MXG_ROPE_INTERLEAVED,
+                 "interleaved_to_half": MXG_ROPE_INTERLEAVED_TO_HALF}
+_dtypes = {}  # torch dtype -> MXG_DT_* or MXG_FMT_*, filled on first use
+
+
+def _dtype_tables():
+    import torch
+    _dtypes["dt"] = {torch.float32: MXG_DT_F32, torch.bfloat16: MXG_DT_BF16, torch.float16: MXG_DT_F16}
+    _dtypes["fmt"] = {torch.float8_e4m3fn: MXG_FMT_E4M3, torch.float8_e5m2: MXG_FMT_E5M2}
+    _dtypes["code"] = {MXG_FMT_E4M3: torch.float8_e4m3fn, MXG_FMT_E5M2: torch.float8_e5m2}
+    _dtypes["empty"] = torch.empty
+
+
+def _dt(t, name):
+    """MXG_DT_* of a tensor or dtype."""
+    if not _dtypes:
+        _dtype_tables()
+    d = _dtypes["dt"].get(getattr(t, "dtype", t))
+    if d is None:
+        raise MxgemmValueError(MXG_ERR_FMT, f"{name} must be float32, bfloat16 or float16")
+    return d
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a kernel on `stream`: its memory is not handed out again before that stream is done with it."""
+    t = _dtypes["empty"](shape, dtype=dtype, device=device)
+    if stream is not None:
+        import torch
+        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        if s != torch.cuda.current_stream(t.device):
+            t.record_stream(s)
+    return t
+
+
+def _same(t, like, shape, dtype, name):
+    """Checks of an output or operand given by the caller."""
+    if tuple(t.shape) != tuple(shape):
+        raise MxgemmValueError(MXG_ERR_SHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise MxgemmValueError(MXG_ERR_FMT, f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise MxgemmValueError(MXG_ERR_DEVICE, f"{name} must be on {like.device}")
+
+
+def _contiguous(t, name):
+    if not t.is_contiguous():
+        raise MxgemmValueError(MXG_ERR_ALIGN, f"{name} must be contiguous")
+
+
+def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, pow2=False, out=None, stream=None):
+    """C-ABI mxgemm_block128_quantize: 8-bit codes of x with one float32 scale per block of 128.
+
+    x is (M, K) or (L, M, K) float32, bfloat16 or float16, K contiguous (rows may be further apart).  Returns
+    (q, s, qt, st), None for what is not asked for, with a leading L where x has one:
+
+    rows: q (M, K16) codes in blocks of 1 x 128, K16 = K rounded up to 16 (codes past K zero), s (ceil(K/128), M);
+    cols: qt (K, M16) codes of the transpose in blocks of 128 along M, st (ceil(M/128), K): the operand of a
+    product over M (a weight gradient);
+    square: blocks of 128 x 128, s (ceil(M/128), ceil(K/128)) and st its transpose (a weight, for the forward
+    product and the input gradient).
+
+    pow2: scales are powers of two.  out: those four tensors preallocated (None where not wanted)."""
+    import torch
+    dt = _dt(x, "x")
+    if x.dim() not in (2, 3):
+        raise MxgemmValueError(MXG_ERR_SHAPE, "x must be (M, K) or (L, M, K)")
+    if fmt not in _dtypes["code"]:
+        raise MxgemmValueError(MXG_ERR_FMT, "fmt must be MXG_FMT_E4M3 or MXG_FMT_E5M2")
+    if not rows and not cols:
+        raise MxgemmValueError(MXG_ERR_NULL, "neither rows nor cols asked for")
+    lead = tuple(x.shape[:-2])
+    l, (m, k) = lead[0] if lead else 1, x.shape[-2:]
+    ldx = x.stride(-2) if m > 1 else (x.stride(0) if lead and l > 1 else k)
+    if (k > 1 and x.stride(-1) != 1) or ldx < k or (l > 1 and m * k > 0 and x.stride(0) != m * ldx):
+        raise MxgemmValueError(MXG_ERR_ALIGN, "x must have contiguous rows, evenly spaced over rows and batches")
+    kb, mb = -(-k // 128), -(-m // 128)
+    f8 = _dtypes["code"][fmt]
+    shapes = ((lead + (m, -(-k // 16) * 16), f8), (lead + ((mb, kb) if square else (kb, m)), torch.float32),
+              (lead + (k, -(-m // 16) * 16), f8), (lead + ((kb, mb) if square else (mb, k)), torch.float32))
+    want = (rows, rows, cols, cols)
+    if out is None:
+        out = tuple(_empty(sh, d, x.device, stream) if w else None for (sh, d), w in zip(shapes, want))
+    else:
+        for t, (sh, d), w, name in zip(out, shapes, want, ("q", "s", "qt", "st")):
+            if (t is not None) != bool(w):
+                raise MxgemmValueError(MXG_ERR_NULL, f"{name} given but not asked for, or the reverse")
+            if w:
+                _same(t, x, sh, d, name)
+                _contiguous(t, name)
+    q, s, qt, st = out
+    status = _lib.mxgemm_block128_quantize(_ptr(x), ldx, _ptr(q), _ptr(s), _ptr(qt), _ptr(st), m, k, l, dt, fmt,
+                                           (MXG_QUANT_SQUARE if square else 0) | (MXG_QUANT_POW2 if pow2 else 0),
+                                           _stream(stream))
+    if status != MXG_OK:
+        _raise(status)
+    return out
+
+
+def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=False, workspace=None, stream=None):
+    """C-ABI mxgemm_block128: c (M, N) = a b^T of block-128 quantised operands, as block128_quantize makes them.
+
+    a (M, K) codes with sa (ceil(K/128), M), b (N, K) codes with sb (ceil(N/128), ceil(K/128)) for b_block=128 or
+    (ceil(K/128), N) for b_block=1; K a multiple of 16; all with a leading L or none; E4M3 or E5M2 each.  c_dtype:
+    float32, bfloat16 (the default) or float16.  c: the output, whose rows may be further apart than N; accumulate
+    adds to a float32 c."""
+    import torch
+    if not _dtypes:
+        _dtype_tables()
+    fa, fb = _dtypes["fmt"].get(a.dtype), _dtypes["fmt"].get(b.dtype)
+    if fa is None or fb is None:
+        raise MxgemmValueError(MXG_ERR_FMT, "a and b must be float8_e4m3fn or float8_e5m2")
+    if a.dim() not in (2, 3) or b.dim() != a.dim() or a.shape[-1] != b.shape[-1] or a.shape[:-2] != b.shape[:-2]:
+        raise MxgemmValueError(MXG_ERR_SHAPE, "a and b must be (M, K) and (N, K), or (L, M, K) and (L, N, K)")
+    if b_block not in (1, 128):
+        raise MxgemmValueError(MXG_ERR_SHAPE, "b_block must be 1 or 128")
+    lead = tuple(a.shape[:-2])
+    l, m, n, k = lead[0] if lead else 1, a.shape[-2], b.shape[-2], a.shape[-1]
+    kb = -(-k // 128)
+    _same(sa, a, lead + (kb, m), torch.float32, "sa")
+    _same(sb, a, lead + ((kb, n) if b_block == 1 else (-(-n // 128), kb)), torch.float32, "sb")
+    for t, name in ((a, "a"), (sa, "sa"), (b, "b"), (sb, "sb")):
+        _contiguous(t, name)
+    if c is None:
+        if accumulate:
+            raise MxgemmValueError(MXG_ERR_NULL, "accumulate needs c")
+        ct, ldc = _dt(c_dtype or torch.bfloat16, "c_dtype"), n
+        c = _empty(lead + (m, n), c_dtype or torch.bfloat16, a.device, stream)
+    else:
+        ct = _dt(c, "c")
+        _same(c, a, lead + (m, n), c_dtype or c.dtype, "c")
+        ldc = c.stride(-2) if m > 1 else (c.stride(0) if lead and l > 1 else n)
+        if (n > 1 and c.stride(-1) != 1) or ldc < n or (l > 1 and m * n > 0 and c.stride(0) != m * ldc):
+            raise MxgemmValueError(MXG_ERR_ALIGN, "c must have contiguous rows, evenly spaced over rows and batches")
+    need = _lib.mxgemm_block128_workspace_bytes(m, n, k, l, ct)
+    if need and workspace is None:
+        workspace = _empty((need,), torch.uint8, a.device, stream)
+    st = _lib.mxgemm_block128(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(c), ldc, m, n, k, l, fa, fb, ct,
+                              (MXG_B128_B_ROWS if b_block == 1 else 0) | (MXG_B128_ACCUMULATE if accumulate else 0),
+                              _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                              _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    return c
+
+
+def rope_table(length, rot, base=10000.0, scaling="none", factor=1.0, original_length=4096, beta_fast=32.0,
+               beta_slow=1.0, device="cuda"):
+    """(cos, sin) float32 tables (length, rot/2) for rope and qk_norm_rope, computed on the host in float64.
+
+    Pair i turns by position * base^(-2i/rot).  scaling stretches that for contexts `factor` times longer than the
+    original_length the weights were trained on:
+
+    "linear": every frequency divided by factor;
+    "ntk": base raised so that the slowest pair is stretched by factor and the fastest kept;
+    "yarn": pairs that turn more than beta_fast times within original_length are kept, those below beta_slow
+    turns are divided by factor, a linear ramp over the pair index in between, and cos and sin are multiplied by
+    0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models", 2023)."""
+    import numpy as np
+    import torch
+    if length < 0 or rot < 0 or rot % 2:
+        raise MxgemmValueError(MXG_ERR_SHAPE, "length must not be negative and rot must be even")
+    if scaling not in ("none", "linear", "ntk", "yarn") or factor <= 0:
+        raise MxgemmValueError(MXG_ERR_FMT, "scaling must be none, linear, ntk or yarn, and factor positive")
+    i = np.arange(rot // 2, dtype=np.float64)
+    m = 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2.0))
+    freq = base ** (-2.0 * i / max(rot, 1))
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        # the (fractional) pair that turns a number of times within the original length
+        def pair(turns):
+            return rot * np.log(original_length / (turns * 2 * np.pi)) / (2 * np.log(base))
+        lo, hi = max(np.floor(pair(beta_fast)), 0.0), min(np.ceil(pair(beta_slow)), rot // 2 - 1.0)
+        ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+        freq = freq * (1 - ramp) + freq / factor * ramp
+        m = 0.1 * np.log(factor) + 1.0 if factor > 1 else 1.0
+    angle = np.arange(length, dtype=np.float64)[:, None] * freq[None, :]
+    return (torch.from_numpy((m * np.cos(angle)).astype(np.float32)).to(device),
+            torch.from_numpy((m * np.sin(angle)).astype(np.float32)).to(device))
+
+
+def _rotary(cos, sin, positions, tokens, layout, x):
+    """(rot, table rows, layout number, flags) of the rotary arguments, checked against x."""
+    import torch
+    lay = _ROPE_LAYOUTS.get(layout)
+    if lay is None:
+        raise MxgemmValueError(MXG_ERR_FMT, f"layout must be one of {sorted(_ROPE_LAYOUTS)}")
+    flags = 0
+    if cos is None or sin is None:
+        if cos is not None or sin is not None or positions is not None:
+            raise MxgemmValueError(MXG_ERR_NULL, "cos and sin come together, and positions with them")
+        return 0, 0, lay, 0
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise MxgemmValueError(MXG_ERR_SHAPE, "cos and sin must be (table rows, rot / 2)")
+    for t, name in ((cos, "cos"), (sin, "sin")):
+        if t.dtype != torch.float32:
+            raise MxgemmValueError(MXG_ERR_FMT, f"{name} must be float32")
+        _contiguous(t, name)
+    if positions is not None:
+        if tuple(positions.shape) != (tokens,):
+            raise MxgemmValueError(MXG_ERR_SHAPE, "positions must have one entry per token")
+        if positions.dtype == torch.int64:
+            flags = MXG_ROPE_POS64
+        elif positions.dtype != torch.int32:
+            raise MxgemmValueError(MXG_ERR_FMT, "positions must be int32 or int64")
+        _contiguous(positions, "positions")
+    return 2 * cos.shape[1], cos.shape[0], lay, flags
+
+
+def _heads_of(x, name, like=None):
+    """Checks of a (T, heads, D) tensor with contiguous features; `like`: T, D, dtype and device to share."""
+    if x.dim() != 3:
+        raise MxgemmValueError(MXG_ERR_SHAPE, f"{name} must be (tokens, heads, features)")
+    if x.shape[2] > 1 and x.stride(2) != 1:
+        raise MxgemmValueError(MXG_ERR_ALIGN, f"{name} must have contiguous features")
+    if like is not None:
+        _same(x, like, (like.shape[0], x.shape[1], like.shape[2]), like.dtype, name)
+
+
+def _new_heads(x, stream):
+    return _empty(tuple(x.shape), x.dtype, x.device, stream)
+
+
+def _strides(*tensors):
+    flat = []
+    for t in tensors:
+        if t is None:
+            flat += (0, 0)
+        else:
+            st = t.stride()
+            flat += (st[0], st[1])
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=False, out=None, stream=None):
+    """C-ABI mxgemm_rope: rotary positions on the heads of x (T, H, D), features contiguous (a view of a wider
+    projection output will do), float32, bfloat16 or float16.
+
+    cos, sin: float32 tables (rows, rot / 2) (see rope_table); the features [rot_offset, rot_offset + rot) of every
+    head rotate and the others are copied.  positions: (T) int32 or int64 table rows, None for 0, 1, ...; a token
+    whose position lies outside the tables gets NaN there.  layout: "half" (pairs i, i + rot/2), "interleaved"
+    (pairs 2i, 2i + 1) or "interleaved_to_half" (the latter in, the former out).  transpose: the transposed map, which takes
+    the output's gradient to the input's.  out: the result, which may be x; a new tensor by default."""
+    dt = _dt(x, "x")
+    _heads_of(x, "x")
+    t, h, d = x.shape
+    rot, rows, lay, flags = _rotary(cos, sin, positions, t, layout, x)
+    if out is None:
+        out = _new_heads(x, stream)
+    else:
+        _heads_of(out, "out", x)
+        _same(out, x, x.shape, x.dtype, "out")
+    st = _lib.mxgemm_rope(_ptr(x), _ptr(out), _ptr(cos), _ptr(sin), _ptr(positions), _strides(x, out), t, h, d, rot,
+                          rot_offset, rows, lay, dt, flags | (MXG_ROPE_TRANSPOSE if transpose else 0), _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    return out
+
+
+def _weights(q_weight, k_weight, q, k):
+    import torch
+    for w, x, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
+        if x is None:
+            continue
+        _same(w, x, (x.shape[2],), w.dtype, name)
+        _contiguous(w, name)
+    w_dtype = q_weight.dtype
+    if w_dtype not in (q.dtype, torch.float32) or (k is not None and k_weight.dtype != w_dtype):
+        raise MxgemmValueError(MXG_ERR_FMT, "weights must both be float32 or of the dtype of q and k")
+    return _dt(w_dtype, "q_weight")
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, eps=1e-6, layout="half", rot_offset=0,
+                 out=None, stream=None):
+    """C-ABI mxgemm_qk_norm_rope: each head of q (T, Hq, D) and k (T, Hk, D) divided by its root mean square,
+    multiplied with its weight (D) and rotated, in one launch.  Returns (q_out, k_out); out: that pair, which may be
+    (q, k).  k and k_weight may be None.  cos, sin None: no rotation.  The other arguments are rope's."""
+    dt = _dt(q, "q")
+    _heads_of(q, "q")
+    if k is not None:
+        _heads_of(k, "k", q)
+    wdt = _weights(q_weight, k_weight, q, k)
+    t, hq, d = q.shape
+    hk = 0 if k is None else k.shape[1]
+    rot, rows, lay, flags = _rotary(cos, sin, positions, t, layout, q)
+    if out is None:
+        yq, yk = _new_heads(q, stream), None if k is None else _new_heads(k, stream)
+    else:
+        yq, yk = out
+        for y, x, name in ((yq, q, "q_out"), (yk, k, "k_out")):
+            if (y is None) != (x is None):
+                raise MxgemmValueError(MXG_ERR_NULL, f"{name} must be given with its input")
+            if y is not None:
+                _heads_of(y, name, q)
+                _same(y, x, x.shape, x.dtype, name)
+    st = _lib.mxgemm_qk_norm_rope(_ptr(q), _ptr(k), _ptr(yq), _ptr(yk), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+                                  _ptr(sin), _ptr(positions), _strides(q, k, yq, yk), t, hq, hk, d, rot, rot_offset,
+                                  rows, eps, lay, dt, wdt, flags, _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    return yq, yk
+
+
+def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, positions=None, eps=1e-6,
+                          layout="half", rot_offset=0, out=None, workspace=None, stream=None):
+    """C-ABI mxgemm_qk_norm_rope_backward: from the gradients dq, dk of qk_norm_rope's outputs and its inputs,
+    (dq_in, dk_in, dq_weight, dk_weight), the weight gradients float32 (None for a missing k).  out: the first two,
+    which may be (dq, dk) or (q, k)."""
+    import torch
+    dt = _dt(q, "q")
+    _heads_of(q, "q")
+    _heads_of(dq, "dq", q)
+    _same(dq, q, q.shape, q.dtype, "dq")
+    if (dk is None) != (k is None):
+        raise MxgemmValueError(MXG_ERR_NULL, "dk must be given with k")
+    if k is not None:
+        _heads_of(k, "k", q)
+        _heads_of(dk, "dk", q)
+        _same(dk, k, k.shape, k.dtype, "dk")
+    wdt = _weights(q_weight, k_weight, q, k)
+    t, hq, d = q.shape
+    hk = 0 if k is None else k.shape[1]
+    rot, rows, lay, flags = _rotary(cos, sin, positions, t, layout, q)
+    if out is None:
+        xq, xk = _new_heads(q, stream), None if k is None else _new_heads(k, stream)
+    else:
+        xq, xk = out
+        for y, x, name in ((xq, q, "dq_in"), (xk, k, "dk_in")):
+            if (y is None) != (x is None):
+                raise MxgemmValueError(MXG_ERR_NULL, f"{name} must be given with its input")
+            if y is not None:
+                _heads_of(y, name, q)
+                _same(y, x, x.shape, x.dtype, name)
+    dwq = _empty((d,), torch.float32, q.device, stream)
+    dwk = None if k is None else _empty((d,), torch.float32, q.device, stream)
+    if workspace is None:
+        need = _lib.mxgemm_qk_norm_rope_backward_workspace_bytes(t, d)
+        workspace = _empty((need,), torch.uint8, q.device, stream)
+    st = _lib.mxgemm_qk_norm_rope_backward(
+        _ptr(dq), _ptr(dk), _ptr(q), _ptr(k), _ptr(xq), _ptr(xk), _ptr(dwq), _ptr(dwk), _ptr(q_weight), _ptr(k_weight),
+        _ptr(cos), _ptr(sin), _ptr(positions), _strides(dq, dk, q, k, xq, xk), t, hq, hk, d, rot, rot_offset, rows,
+        eps, lay, dt, wdt, flags, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    return xq, xk, dwq, dwk
+
+
 __all__ = [
     "mxgemm_amax", "mxgemm_amax_ex", "mxgemm_amax_reset", "mxgemm_check_support", "mxgemm_sf_bytes",
     "mxgemm_launch_config", "mxgemm_strerror", "gemm_amax", "LIB_PATH", "EXPORTED",
@@ -466,4 +847,8 @@ __all__ = [
     "proj_rope_mxfp8", "gemm_rope_mxfp8", "projection_mxfp8", "projection_mxfp8_noalloc", "MxgemmError",
     "MxgemmValueError",
     "MxgemmRuntimeError",
+    "block128_quantize", "block128_gemm", "rope_table", "rope", "qk_norm_rope", "qk_norm_rope_backward",
+    "MXG_DT_F32", "MXG_DT_BF16", "MXG_DT_F16", "MXG_QUANT_SQUARE", "MXG_QUANT_POW2", "MXG_B128_B_ROWS",
+    "MXG_B128_ACCUMULATE", "MXG_ROPE_HALF", "MXG_ROPE_INTERLEAVED", "MXG_ROPE_INTERLEAVED_TO_HALF",
+    "MXG_ROPE_TRANSPOSE", "MXG_ROPE_POS64",
 ]

@@ -1,0 +1,186 @@
+// C-ABI entry points of the block-128 quantiser and product (include/mxgemm.h).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "../../include/mxgemm.h"
+#include "block128_gemm.hpp"
+#include "block128_quantize.hpp"
+#include "host_checks.hpp"
+
+namespace {
+
+using namespace mxg::host;
+using mxg::b128::GemmParams;
+using mxg::b128::QuantParams;
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// --- quantiser --------------------------------------------------------------------
+
+int check_quantize(int64_t ldx, int64_t M, int64_t K, int64_t L, int dt, int fmt, unsigned flags) {
+  if (M < 0 || K < 0 || L < 0 || ldx < K) return MXG_ERR_SHAPE;
+  if (dt < MXG_DT_F32 || dt > MXG_DT_F16 || (fmt != MXG_FMT_E4M3 && fmt != MXG_FMT_E5M2)) return MXG_ERR_FMT;
+  if (flags & ~(unsigned)(MXG_QUANT_SQUARE | MXG_QUANT_POW2)) return MXG_ERR_FLAGS;
+  // sizes are 32-bit in the kernels, offsets 64-bit
+  const int64_t top = 0x7FFFFF00LL;
+  if (M > top || K > top || L > top || ldx > (1LL << 40)) return MXG_ERR_SHAPE;
+  if (M && L && ldx && (ldx > (1LL << 58) / M || M * ldx > (1LL << 58) / L)) return MXG_ERR_SHAPE;
+  if (M && L && K && M * K > (1LL << 58) / L) return MXG_ERR_SHAPE;
+  if (M && K && L && cdiv(M, 16) * cdiv(K, 128) > 0x7FFFFFFFLL / L) return MXG_ERR_SHAPE;
+  return MXG_OK;
+}
+
+template <int DT, int FMT, int RT, bool VEC>
+void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, int64_t grid, hipStream_t s) {
+  using namespace mxg::b128;
+  const dim3 g((unsigned)grid), b(kQThreads);
+  if constexpr (RT == 8) {
+    if (square && rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, true, true>), g, b, 0, s, p);
+    else if (square && rows) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, false, true>), g, b, 0, s, p);
+    else if (square) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, false, true, true>), g, b, 0, s, p);
+    else if (rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, true, false>), g, b, 0, s, p);
+    else if (cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, false, true, false>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, false, false>), g, b, 0, s, p);
+  } else {
+    hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, false, false>), g, b, 0, s, p);
+  }
+}
+
+template <int DT>
+void launch_quantize(const QuantParams& p, int fmt, bool vec, bool rows, bool cols, bool square, int64_t grid, hipStream_t s) {
+  if (fmt == MXG_FMT_E4M3) {
+    if (vec) launch_quantize<DT, 0, 8, true>(p, rows, cols, square, grid, s);
+    else launch_quantize<DT, 0, 8, false>(p, rows, cols, square, grid, s);
+  } else {
+    if (vec) launch_quantize<DT, 1, 8, true>(p, rows, cols, square, grid, s);
+    else launch_quantize<DT, 1, 8, false>(p, rows, cols, square, grid, s);
+  }
+}
+
+// --- product ----------------------------------------------------------------------
+
+int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, int fb, int ct, unsigned flags) {
+  if (M < 0 || N < 0 || K < 0 || L < 0 || ldc < N) return MXG_ERR_SHAPE;
+  for (int f : {fa, fb})
+    if (f != MXG_FMT_E4M3 && f != MXG_FMT_E5M2) return MXG_ERR_FMT;
+  if (ct < MXG_DT_F32 || ct > MXG_DT_F16) return MXG_ERR_FMT;
+  if (flags & ~(unsigned)(MXG_B128_B_ROWS | MXG_B128_ACCUMULATE)) return MXG_ERR_FLAGS;
+  if ((flags & MXG_B128_ACCUMULATE) && ct != MXG_DT_F32) return MXG_ERR_FLAGS;
+  const int64_t top = 0x7FFFFF00LL;
+  // a tile's 256 rows of A, B or C are addressed with 32-bit byte offsets
+  if (M > top || N > top || L > top || K > (1LL << 23) - 16 || ldc > (1LL << 21)) return MXG_ERR_SHAPE;
+  if (L * cdiv(M, 32) > 0x7FFFFFFFLL / std::max<int64_t>(1, cdiv(N, 32))) return MXG_ERR_SHAPE;
+  if (K % 16 != 0) return MXG_ERR_ALIGN;
+  return MXG_OK;
+}
+
+template <int FA, int FB>
+void launch_plain(const GemmParams& p, int ct, hipStream_t s) {
+  const dim3 g((unsigned)(p.L * cdiv(p.M, 32) * cdiv(p.N, 32))), b(64);
+  if (ct == MXG_DT_F32) hipLaunchKernelGGL((mxg::b128::block128_plain_kernel<FA, FB, 0>), g, b, 0, s, p);
+  else if (ct == MXG_DT_BF16) hipLaunchKernelGGL((mxg::b128::block128_plain_kernel<FA, FB, 1>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((mxg::b128::block128_plain_kernel<FA, FB, 2>), g, b, 0, s, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void* QT, float* ST, int64_t M, int64_t K,
+                             int64_t L, int x_dtype, int fmt, unsigned flags, void* stream) {
+  int st = check_quantize(ldx, M, K, L, x_dtype, fmt, flags);
+  if (st != MXG_OK) return st;
+  if (M == 0 || K == 0 || L == 0) return MXG_OK;
+  const bool rows = Q != nullptr, cols = QT != nullptr, square = (flags & MXG_QUANT_SQUARE) != 0;
+  if (!X || (!rows && !cols) || rows != (S != nullptr) || cols != (ST != nullptr)) return MXG_ERR_NULL;
+  const size_t e = mxg::elem_bytes(x_dtype);
+  if (!aligned_to(X, e) || !aligned16(Q) || !aligned16(QT) || !aligned_to(S, 4) || !aligned_to(ST, 4))
+    return MXG_ERR_ALIGN;
+  int dev = 0, cus = 0;
+  st = device_check(&dev, &cus);
+  if (st != MXG_OK) return st;
+  if (!on_device(X, dev) || (rows && (!on_device(Q, dev) || !on_device(S, dev))) ||
+      (cols && (!on_device(QT, dev) || !on_device(ST, dev))))
+    return MXG_ERR_DEVICE;
+  QuantParams p{};
+  p.X = X;
+  p.Q = static_cast<uint8_t*>(Q);
+  p.S = S;
+  p.QT = static_cast<uint8_t*>(QT);
+  p.ST = ST;
+  p.ldx = ldx;
+  p.M = (int)M;
+  p.K = (int)K;
+  p.L = (int)L;
+  p.K16 = (int)up16(K);
+  p.M16 = (int)up16(M);
+  p.Mb = (int)cdiv(M, 128);
+  p.Kb = (int)cdiv(K, 128);
+  p.pow2 = (flags & MXG_QUANT_POW2) != 0;
+  // whole 8-element chunks at 16-byte addresses
+  const bool vec = aligned16(X) && K % 8 == 0 && ldx % 8 == 0;
+  p.tiles_m = p.Mb;
+  const int64_t grid = L * p.tiles_m * p.Kb;
+  hipStream_t s = (hipStream_t)stream;
+  if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, vec, rows, cols, square, grid, s);
+  else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, vec, rows, cols, square, grid, s);
+  else launch_quantize<2>(p, fmt, vec, rows, cols, square, grid, s);
+  return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
+}
+
+size_t mxgemm_block128_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int c_dtype) {
+  (void)M, (void)N, (void)K, (void)L, (void)c_dtype;
+  return 0;
+}
+
+int mxgemm_block128(const void* A, const float* SA, const void* B, const float* SB, void* C, int64_t ldc, int64_t M,
+                    int64_t N, int64_t K, int64_t L, int a_fmt, int b_fmt, int c_dtype, unsigned flags, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int st = check_gemm(ldc, M, N, K, L, a_fmt, b_fmt, c_dtype, flags);
+  if (st != MXG_OK) return st;
+  if (M == 0 || N == 0 || L == 0) return MXG_OK;
+  if (!C || (K > 0 && (!A || !B || !SA || !SB))) return MXG_ERR_NULL;
+  const size_t need = mxgemm_block128_workspace_bytes(M, N, K, L, c_dtype);
+  if (need > 0 && !workspace) return MXG_ERR_NULL;
+  if (need > workspace_bytes) return MXG_ERR_SHAPE;
+  if (!aligned16(A) || !aligned16(B) || !aligned_to(SA, 4) || !aligned_to(SB, 4) ||
+      !aligned_to(C, mxg::elem_bytes(c_dtype)) || (need > 0 && !aligned16(workspace)))
+    return MXG_ERR_ALIGN;
+  int dev = 0, cus = 0;
+  st = device_check(&dev, &cus);
+  if (st != MXG_OK) return st;
+  if (!on_device(C, dev) || (K > 0 && (!on_device(A, dev) || !on_device(B, dev) || !on_device(SA, dev) ||
+                                       !on_device(SB, dev))) ||
+      (need > 0 && !on_device(workspace, dev)))
+    return MXG_ERR_DEVICE;
+  GemmParams p{};
+  p.A = static_cast<const uint8_t*>(A);
+  p.B = static_cast<const uint8_t*>(B);
+  p.SA = SA;
+  p.SB = SB;
+  p.C = C;
+  p.ldc = ldc;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.L = (int)L;
+  p.Kb = (int)cdiv(K, 128);
+  p.Nb = (int)cdiv(N, 128);
+  p.b_rows = (flags & MXG_B128_B_ROWS) != 0;
+  p.accumulate = (flags & MXG_B128_ACCUMULATE) != 0;
+  hipStream_t s = (hipStream_t)stream;
+  if (a_fmt == MXG_FMT_E4M3) {
+    if (b_fmt == MXG_FMT_E4M3) launch_plain<0, 0>(p, c_dtype, s);
+    else launch_plain<0, 1>(p, c_dtype, s);
+  } else {
+    if (b_fmt == MXG_FMT_E4M3) launch_plain<1, 0>(p, c_dtype, s);
+    else launch_plain<1, 1>(p, c_dtype, s);
+  }
+  return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,259 @@
+// Quantisation to 8-bit codes with one float32 scale per block of 128, on
+// gfx950: rows (blocks of 1 x 128 along K), columns (blocks of 128 x 1, stored
+// transposed) or both from one read of X, or 128 x 128 blocks.
+//
+//   a = max |x| over the block, at least 448 * 2^-100;  scale = a / FMAX,
+//   code = rne(x * (FMAX / a));  power-of-two scales: 2^e, e the smallest
+//   integer with FMAX * 2^e >= a.
+//
+// A workgroup takes a tile of 16 RT rows x 128 columns: thread (g, c) holds
+// rows RT g .. RT g + RT - 1 of columns 8c .. 8c + 7 in registers, RT chunks of
+// 8 elements as loaded.  Row maxima finish across the 16 lanes of a row; column
+// maxima across the 16 threads of a chunk, in LDS.  Magnitudes are compared as
+// the integers of their bits without the sign, which orders NaN above infinity
+// above the finite, so a block that holds either gets a scale that is neither
+// lost nor finite.  The transposed codes are converted along the thread's 8
+// rows, gathered in LDS as (column, row) bytes and stored as whole 128-byte
+// rows.
+#pragma once
+
+#include "dtypes.hpp"
+#include "mx_quantize.hpp"
+
+namespace mxg {
+namespace b128 {
+
+constexpr int kQThreads = 256;
+
+struct QuantParams {
+  const void* X;
+  uint8_t* Q;
+  float* S;
+  uint8_t* QT;
+  float* ST;
+  int64_t ldx;
+  int M, K, L;
+  int K16, M16;      // row lengths of Q and QT
+  int Mb, Kb;        // ceil(M / 128), ceil(K / 128)
+  int tiles_m;       // row tiles per batch
+  bool pow2;
+};
+
+constexpr unsigned kTinyBits = 0x11E00000u;  // 448 * 2^-100 = 1.75 * 2^-92
+
+struct Scale {
+  float scale, inv;
+};
+// Scale and multiplier of a block from the bits of its largest magnitude (float32).
+template <int FMT>
+__device__ __forceinline__ Scale block_scale(unsigned bits, bool pow2) {
+  constexpr float kMax = FMT == 0 ? 448.f : 57344.f;
+  const float a = __uint_as_float(bits > kTinyBits ? bits : kTinyBits);
+  if (pow2 && bits < 0x7F800000u) {
+    const int e = quant::block_exponent<FMT>(a);
+    return {__uint_as_float((unsigned)(127 + e) << 23), __uint_as_float((unsigned)(127 - e) << 23)};
+  }
+  return {a / kMax, kMax / a};  // correctly rounded; inf or NaN stay so
+}
+
+// Bits of the magnitudes of 8 elements, as loaded: two 16-bit ones to a dword.
+template <int DT>
+struct Mag8 {
+  unsigned w[DT == 0 ? 8 : 4];
+};
+template <int DT>
+__device__ __forceinline__ Mag8<DT> magnitudes(const Raw8<DT>& r) {
+  Mag8<DT> m;
+  if constexpr (DT == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m.w[i] = r.w[i >> 2][i & 3] & 0x7FFFFFFFu;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m.w[i] = r.w[0][i] & 0x7FFF7FFFu;
+  }
+  return m;
+}
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ unsigned mag_max(unsigned a, unsigned b) {
+  if constexpr (DT == 0) return max(a, b);
+  else return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(v2us, a), __builtin_bit_cast(v2us, b)));
+}
+// float32 bits of the larger half of a dword of two 16-bit magnitudes (or of a float32 magnitude).
+template <int DT>
+__device__ __forceinline__ unsigned half_bits(unsigned h) {
+  if constexpr (DT == 1) return h << 16;
+  else return __float_as_uint((float)__builtin_bit_cast(_Float16, (unsigned short)h));
+}
+template <int DT>
+__device__ __forceinline__ unsigned mag_bits(unsigned m) {
+  if constexpr (DT == 0) return m;
+  else return half_bits<DT>(max(m & 0xFFFFu, m >> 16));
+}
+
+// 8 elements at p, those at or past `valid` read as zero.
+template <int DT, bool VEC>
+__device__ __forceinline__ Raw8<DT> load_chunk(const elem_t<DT>* p, int valid) {
+  Raw8<DT> r;
+  if constexpr (VEC) {
+    if (valid > 0) return load8<DT>(p);
+#pragma unroll
+    for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) r.w[i] = (v4u){0, 0, 0, 0};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (DT == 0) {
+        r.w[i >> 2][i & 3] = i < valid ? __float_as_uint(p[i]) : 0u;
+      } else {
+        const unsigned short h = i < valid ? __builtin_bit_cast(unsigned short, p[i]) : (unsigned short)0;
+        if (i & 1) r.w[0][i >> 1] |= (unsigned)h << 16;
+        else r.w[0][i >> 1] = h;
+      }
+    }
+  }
+  return r;
+}
+
+// VEC: 16-byte loads (X, ldx and K in multiples of 8 elements, base aligned).
+template <int DT, int FMT, int RT, bool VEC, bool ROWS, bool COLS, bool SQUARE>
+__global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParams p) {
+  static_assert(RT == 8 || (!COLS && !SQUARE), "columns and squares need the 128 rows of a block");
+  constexpr int kRows = 16 * RT, kPitch = 132;  // LDS bytes between columns of the transposed codes
+  __shared__ __attribute__((aligned(16))) uint8_t tile[COLS ? 128 * kPitch : 16];
+  __shared__ unsigned colmax[COLS && !SQUARE ? 4 : 1][COLS && !SQUARE ? 128 : 4];
+  __shared__ float rowscale[ROWS && !SQUARE ? kRows : 1];
+
+  const int tid = threadIdx.x, c = tid & 15, g = tid >> 4, wave = tid >> 6;
+  int b = blockIdx.x;
+  const int kb = b % p.Kb;
+  b /= p.Kb;
+  const int tm = b % p.tiles_m, l = b / p.tiles_m;
+  const int m0 = tm * kRows, k0 = kb * 128, k = k0 + 8 * c;
+  const elem_t<DT>* x = static_cast<const elem_t<DT>*>(p.X) + ((int64_t)l * p.M + m0) * p.ldx + k;
+
+  Raw8<DT> v[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int m = RT * g + i;
+    v[i] = load_chunk<DT, VEC>(x + (int64_t)m * p.ldx, m0 + m < p.M ? p.K - k : 0);
+  }
+
+  // largest magnitudes: of the thread's rows, and of its columns
+  constexpr int kW = DT == 0 ? 8 : 4;
+  unsigned rmax[RT];
+  Mag8<DT> cmax;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const Mag8<DT> m = magnitudes<DT>(v[i]);
+    unsigned r = m.w[0];
+#pragma unroll
+    for (int j = 1; j < kW; ++j) r = mag_max<DT>(r, m.w[j]);
+    rmax[i] = mag_bits<DT>(r);
+    if constexpr (COLS && !SQUARE) {
+#pragma unroll
+      for (int j = 0; j < kW; ++j) cmax.w[j] = i == 0 ? m.w[j] : mag_max<DT>(cmax.w[j], m.w[j]);
+    }
+  }
+
+  Scale row[RT], col[8];
+  if constexpr (SQUARE) {
+    unsigned t = rmax[0];
+#pragma unroll
+    for (int i = 1; i < RT; ++i) t = max(t, rmax[i]);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) t = max(t, (unsigned)__shfl_xor((int)t, s));
+    if ((tid & 63) == 0) colmax[0][wave] = t;
+    __syncthreads();
+    t = max(max(colmax[0][0], colmax[0][1]), max(colmax[0][2], colmax[0][3]));
+    const Scale s = block_scale<FMT>(t, p.pow2);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) row[i] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) col[i] = s;
+    if (tid == 0) {
+      if constexpr (ROWS) p.S[((int64_t)l * p.Mb + tm) * p.Kb + kb] = s.scale;
+      if constexpr (COLS) p.ST[((int64_t)l * p.Kb + kb) * p.Mb + tm] = s.scale;
+    }
+  } else {
+    if constexpr (ROWS) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        unsigned t = rmax[i];
+#pragma unroll
+        for (int s = 1; s < 16; s <<= 1) t = max(t, (unsigned)__shfl_xor((int)t, s));
+        row[i] = block_scale<FMT>(t, p.pow2);
+        if (c == 0) rowscale[RT * g + i] = row[i].scale;
+      }
+    }
+    if constexpr (COLS) {
+      // across the wave's four rows of threads, then across the waves
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        unsigned t = cmax.w[j];
+        t = mag_max<DT>(t, (unsigned)__shfl_xor((int)t, 16));
+        t = mag_max<DT>(t, (unsigned)__shfl_xor((int)t, 32));
+        if ((tid & 48) == 0) {
+          if constexpr (DT == 0) {
+            colmax[wave][8 * c + j] = t;
+          } else {
+            colmax[wave][8 * c + 2 * j] = half_bits<DT>(t & 0xFFFFu);
+            colmax[wave][8 * c + 2 * j + 1] = half_bits<DT>(t >> 16);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if constexpr (COLS) {
+      // each column's scale once, left in place of its maximum: thread j < 128 makes column j's
+      if (tid < 128) {
+        const unsigned t = max(max(colmax[0][tid], colmax[1][tid]), max(colmax[2][tid], colmax[3][tid]));
+        const Scale s = block_scale<FMT>(t, p.pow2);
+        if (k0 + tid < p.K) p.ST[((int64_t)l * p.Mb + tm) * p.K + k0 + tid] = s.scale;
+        colmax[0][tid] = __float_as_uint(s.inv);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) col[j].inv = __uint_as_float(colmax[0][8 * c + j]);
+    }
+    if constexpr (ROWS) {
+      if (tid < kRows && m0 + tid < p.M) p.S[((int64_t)l * p.Kb + kb) * p.M + m0 + tid] = rowscale[tid];
+    }
+  }
+
+  if constexpr (ROWS) {
+    uint8_t* q = p.Q + ((int64_t)l * p.M + m0) * p.K16 + k;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int m = RT * g + i;
+      const v8f f = widen8<DT>(v[i]) * row[i].inv;
+      const uint2 u = make_uint2(quant::codes4<FMT>(f[0], f[1], f[2], f[3]), quant::codes4<FMT>(f[4], f[5], f[6], f[7]));
+      if (m0 + m < p.M && k < p.K16) *reinterpret_cast<uint2*>(q + (int64_t)m * p.K16) = u;
+    }
+  }
+  if constexpr (COLS) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const v8f f0 = widen8<DT>(v[4 * h]), f1 = widen8<DT>(v[4 * h + 1]), f2 = widen8<DT>(v[4 * h + 2]),
+                f3 = widen8<DT>(v[4 * h + 3]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = col[j].inv;
+        *reinterpret_cast<unsigned*>(tile + (8 * c + j) * kPitch + 8 * g + 4 * h) =
+            quant::codes4<FMT>(f0[j] * s, f1[j] * s, f2[j] * s, f3[j] * s);
+      }
+    }
+    __syncthreads();
+    uint8_t* q = p.QT + ((int64_t)l * p.K + k0) * p.M16 + m0;
+    const int at = 16 * (tid & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (tid >> 3) + 32 * i;
+      const unsigned* t = reinterpret_cast<const unsigned*>(tile + r * kPitch + at);
+      const v4u u = {t[0], t[1], t[2], t[3]};
+      if (k0 + r < p.K && m0 + at < p.M16) *reinterpret_cast<v4u*>(q + (int64_t)r * p.M16 + at) = u;
+    }
+  }
+}
+
+}  // namespace b128
+}  // namespace mxg

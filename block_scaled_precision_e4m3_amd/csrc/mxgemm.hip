@@ -17,6 +17,7 @@
 #include "codes_transpose.hpp"
 #include "proj_rope.hpp"
 #include "gemm_launch.hpp"
+#include "host_checks.hpp"
 
 namespace mxg {
 
@@ -42,20 +43,7 @@ __global__ void c_zero_kernel(uint2* c, int64_t n8) {
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
-
-struct DeviceInfo {
-  int checked = 0;   // 0 unknown, 1 gfx950, -1 other
-  int cus = 0;
-};
-
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mutex;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool fits_i32(int64_t v) { return v >= 0 && v <= 0x7FFFFFFFLL; }
+using namespace mxg::host;
 
 // Pure size/format validation shared by every entry point.
 int check_sizes(int64_t M, int64_t N, int64_t K, int64_t L, int sf, int a_fmt, int b_fmt) {
@@ -82,28 +70,6 @@ int check_sizes(int64_t M, int64_t N, int64_t K, int64_t L, int sf, int a_fmt, i
   return MXG_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Current device must be gfx950; returns its CU count through *cus.
-int device_check(int* dev_out, int* cus) {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return MXG_ERR_DEVICE;
-  DeviceInfo& d = g_dev[dev];
-  if (d.checked == 0) {
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
-    if (d.checked == 0) {
-      hipDeviceProp_t prop;
-      if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MXG_ERR_DEVICE;
-      d.cus = prop.multiProcessorCount;
-      d.checked = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : -1;
-    }
-  }
-  if (d.checked != 1) return MXG_ERR_DEVICE;
-  *dev_out = dev;
-  *cus = d.cus;
-  return MXG_OK;
-}
-
 // Device address of `scratch` on device `dev` (current), looked up on the
 // first call on that device and kept; nullptr if HIP cannot give it.
 void* g_scratch_ptr[kMaxDevices];
@@ -120,17 +86,6 @@ void* scratch_address(int dev) {
     g_scratch_ptr[dev] = ptr;
   }
   return g_scratch_ptr[dev];
-}
-
-// Device memory of `dev` (or managed memory) is accepted; host memory is not.
-bool on_device(const void* p, int dev) {
-  hipPointerAttribute_t attr;
-  if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
-    (void)hipGetLastError();
-    return false;
-  }
-  if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged) return false;
-  return attr.device == dev;
 }
 
 // Tile shapes, one workgroup per CU either way (mxgemm_big.hpp): 256x256 (4

@@ -1,0 +1,309 @@
+"""The block-128 quantiser (bit-exact against the oracle) and product (against float64) on the GPU.
+
+Tolerances of the product, with S = sum |a||b| and u the rounding of C's type (2^-8, 2^-11, none for float32):
+float32 C: exact products, one rounded add per 16 K in a block (K/16), a rounded scale product, a rounded multiply
+and add per block: (K/16 + 4 K/128 + 4) 2^-24 S.  16-bit C: besides, what the 8-bit products may drop in a group of
+8 K elements, 8 terms each below 2^-13 of the largest: 2^-10 S."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block128 as B
+from oracle.codecs import decode
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+U = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import block_scaled_precision_e4m3_amd as lib
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return lib
+
+
+def values(shape, seed, dtype):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal(shape) * np.exp2(rng.integers(-4, 5, shape))
+    x.reshape(-1)[:: 7] = 0
+    return torch.from_numpy(x.astype(np.float32)).to(dtype)
+
+
+def guarded(shape, dtype, fill=0xA5, guard=512):
+    n = int(np.prod(shape)) * dtype.itemsize
+    buf = torch.full((n + guard,), fill, dtype=torch.uint8, device="cuda")
+    return buf, buf[:n].view(dtype).view(shape), n
+
+
+def check_quantize(lib, x, fmt, rows, cols, square, pow2):
+    """One call with guard bands, against the oracle, every byte."""
+    m, k = x.shape
+    kb, mb, k16, m16 = -(-k // 128), -(-m // 128), -(-k // 16) * 16, -(-m // 16) * 16
+    f8 = torch.float8_e4m3fn if fmt == 0 else torch.float8_e5m2
+    shapes = (((m, k16), f8), ((mb, kb) if square else (kb, m), torch.float32), ((k, m16), f8),
+              ((kb, mb) if square else (mb, k), torch.float32))
+    bufs = [guarded(*s) if w else None for s, w in zip(shapes, (rows, rows, cols, cols))]
+    lib.block128_quantize(x.cuda() if not x.is_cuda else x, fmt, rows, cols, square, pow2,
+                          out=tuple(b and b[1] for b in bufs))
+    torch.cuda.synchronize()
+    want = B.quantize(x.float().cpu().numpy(), fmt, rows, cols, square, pow2)
+    for name, b, w in zip(("q", "s", "qt", "st"), bufs, want):
+        if b is None:
+            continue
+        assert torch.all(b[0][b[2]:] == 0xA5).item(), f"write past {name}"
+        got = b[1].view(torch.uint8).cpu().numpy() if name[0] == "q" else b[1].cpu().numpy()
+        bad = np.argwhere(got != w)
+        assert got.shape == w.shape and len(bad) == 0, f"{name}: {len(bad)} differ, first {bad[:4].tolist()}"
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("m,k", [(1, 1), (1, 128), (3, 7168), (16, 24), (127, 129), (128, 128), (129, 500), (300, 264),
+                                 (17, 4096)])
+def test_quantize_bit_exact(lib, m, k, dtype):
+    print(f"quantise {m}x{k} {dtype}", flush=True)
+    x = values((m, k), m * 31 + k, DT[dtype])
+    for fmt in (0, 1):
+        for rows, cols, square in ((True, False, False), (False, True, False), (True, True, False), (True, True, True),
+                                   (True, False, True), (False, True, True)):
+            check_quantize(lib, x, fmt, rows, cols, square, fmt == 1 and rows)
+    check_quantize(lib, x, 0, True, True, False, True)
+    check_quantize(lib, x, 0, True, True, True, True)
+
+
+@pytest.mark.parametrize("m,k", [(5, 256), (140, 200), (2100, 136)])
+def test_quantize_strided_and_unaligned_rows(lib, m, k):
+    print(f"quantise strided {m}x{k}", flush=True)
+    for dtype in DT.values():
+        for pad, off in ((8, 0), (8, 8), (3, 0), (8, 1)):
+            wide = values((m, k + pad + off), m + pad, dtype).cuda()
+            check_quantize(lib, wide[:, off:off + k], 0, True, True, False, False)
+            check_quantize(lib, wide[:, off:off + k], 0, True, False, False, False)
+
+
+def test_quantize_batches_equal_single_calls(lib):
+    x = values((3, 70, 320), 5, torch.bfloat16).cuda()
+    for square in (False, True):
+        q, s, qt, st = lib.block128_quantize(x, 0, True, True, square)
+        for i in range(3):
+            one = lib.block128_quantize(x[i], 0, True, True, square)
+            for got, want in zip((q[i], s[i], qt[i], st[i]), one):
+                assert torch.equal(got.contiguous().view(torch.uint8), want.view(torch.uint8))
+    # batches of a wider buffer, rows evenly spaced over them
+    q2 = lib.block128_quantize(torch.nn.functional.pad(x, (0, 64))[:, :, :320])[0]
+    assert torch.equal(q2.view(torch.uint8), lib.block128_quantize(x)[0].view(torch.uint8))
+
+
+def test_quantize_extremes(lib):
+    """Zero blocks, the smallest and largest magnitudes, ties, maxima whose quotients round either way."""
+    rng = np.random.default_rng(9)
+    x = np.zeros((64, 128), np.float32)
+    x[1, 5] = 2.0 ** -149
+    x[2] = 3.0e38
+    x[3] = np.float32(448.0 * 2.0 ** -100)
+    x[4] = 1e-30 * rng.standard_normal(128)
+    x[5, ::2] = 448.0
+    x[5, 1::2] = rng.integers(-448, 449, 64)                       # ties of the grid at scale 1
+    x[6:] = rng.standard_normal((58, 128)) * np.exp2(rng.uniform(-20, 20, (58, 1)))
+    for pow2 in (False, True):
+        for fmt in (0, 1):
+            check_quantize(lib, torch.from_numpy(x.astype(np.float32)), fmt, True, True, False, pow2)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_quantize_non_finite_blocks_are_not_lost(lib, dtype, bad):
+    x = values((40, 256), 3, DT[dtype])
+    x[7, 130] = bad
+    for pow2 in (False, True):
+        q, s, qt, st = (t.cpu() for t in lib.block128_quantize(x.cuda(), 0, True, True, False, pow2))
+        hit = torch.zeros(2, 40, dtype=torch.bool)
+        hit[1, 7] = True
+        assert torch.equal(~torch.isfinite(s), hit)
+        assert torch.isfinite(st).sum() == 255 and not torch.isfinite(st[0, 130])
+        y = lib.block128_gemm(q.cuda(), s.cuda(), torch.ones(4, 256).cuda().to(torch.float8_e4m3fn),
+                              torch.ones(1, 2).cuda(), c_dtype=torch.float32).cpu()
+        assert torch.isnan(y[7]).all() and torch.isfinite(y[:7]).all() and torch.isfinite(y[8:]).all()
+
+
+# --- product --------------------------------------------------------------------------
+
+def operands(m, n, k, fa, fb, b_block, seed, heavy=False):
+    rng = np.random.default_rng(seed)
+    gen = (lambda *s: rng.standard_t(3, s)) if heavy else (lambda *s: rng.standard_normal(s))
+    a, sa, _, _ = B.quantize(gen(m, k).astype(np.float32), fa)
+    b, sb, _, _ = B.quantize(gen(n, k).astype(np.float32) / np.float32(np.sqrt(k)), fb, square=b_block == 128)
+    return a, np.ascontiguousarray(sa), b, np.ascontiguousarray(sb)
+
+
+def upload(a, sa, b, sb, fa, fb):
+    f8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+    up = lambda v: torch.from_numpy(np.ascontiguousarray(v)).cuda()  # noqa: E731
+    return up(a).view(f8[fa]), up(sa), up(b).view(f8[fb]), up(sb)
+
+
+def bound(s, ref, k, dtype):
+    b = (k / 16 + 4 * -(-k // 128) + 4) * 2.0 ** -24 * s
+    if dtype != torch.float32:
+        b = b + 2.0 ** -10 * s + U[dtype] * (np.abs(ref) + b + 2.0 ** -10 * s)
+        b = b + (2.0 ** -25 if dtype == torch.float16 else 0.0)    # float16 subnormals
+    return b
+
+
+def check_gemm(lib, m, n, k, fa=0, fb=0, b_block=128, dtype=torch.bfloat16, seed=0, heavy=False, ldc=None, c0=None):
+    host = operands(m, n, k, fa, fb, b_block, seed, heavy)
+    ref, s = B.gemm(*host, fa, fb, b_block)
+    ldc = ldc or n
+    buf, full, used = guarded((m, ldc), dtype)
+    c = full[:, :n]
+    if c0 is not None:
+        c.copy_(torch.from_numpy(c0))
+    before = full.view(torch.uint8).clone()
+    lib.block128_gemm(*upload(*host, fa, fb), b_block=b_block, c=c, accumulate=c0 is not None)
+    torch.cuda.synchronize()
+    assert torch.all(buf[used:] == 0xA5).item(), "write past C"
+    e = dtype.itemsize
+    assert torch.equal(full.view(torch.uint8)[:, n * e:], before[:, n * e:]), "write between the rows of C"
+    if c0 is not None:
+        ref, s = ref + c0, s + np.abs(c0)
+    got = c.double().cpu().numpy()
+    bad = ~(np.abs(got - ref) <= bound(s, ref, k, dtype))
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} outside, first {np.argwhere(bad)[:4].tolist()}"
+
+
+SIZES = [(1, 1, 16), (1, 7168, 2048), (2, 130, 144), (7, 96, 1040), (16, 256, 128), (17, 100, 256), (33, 72, 400),
+         (64, 512, 512), (65, 300, 640), (100, 1000, 272), (128, 128, 128), (129, 257, 384), (200, 700, 2064),
+         (256, 256, 256), (300, 520, 1024), (513, 1030, 528), (1000, 2056, 160)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_gemm_types(lib, m, n, k):
+    print(f"gemm {m}x{n}x{k}", flush=True)
+    for dtype in DT.values():
+        for b_block in (128, 1):
+            check_gemm(lib, m, n, k, 0, 0, b_block, dtype, seed=m + n + k)
+
+
+@pytest.mark.parametrize("fa,fb", [(0, 1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("m,n,k", [(3, 200, 272), (70, 136, 400), (300, 260, 528), (600, 900, 256)])
+def test_gemm_formats_and_heavy_tails(lib, m, n, k, fa, fb):
+    print(f"gemm {m}x{n}x{k} formats {fa} {fb}", flush=True)
+    for dtype in (torch.float32, torch.bfloat16):
+        check_gemm(lib, m, n, k, fa, fb, 128, dtype, seed=m, heavy=True)
+        check_gemm(lib, m, n, k, fa, fb, 1, dtype, seed=m, heavy=True)
+
+
+@pytest.mark.parametrize("m,n,k,ldc", [(5, 33, 144, 40), (66, 129, 256, 131), (300, 400, 256, 408), (257, 255, 384, 333)])
+def test_gemm_rows_of_a_wider_output(lib, m, n, k, ldc):
+    for dtype in DT.values():
+        check_gemm(lib, m, n, k, dtype=dtype, ldc=ldc, seed=2)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 40, 160), (64, 200, 2048), (300, 260, 512), (512, 512, 4096)])
+def test_gemm_accumulates(lib, m, n, k):
+    c0 = np.random.default_rng(1).standard_normal((m, n)).astype(np.float32).astype(np.float64)
+    check_gemm(lib, m, n, k, b_block=1, dtype=torch.float32, c0=c0, seed=4)
+    check_gemm(lib, m, n, k, b_block=128, dtype=torch.float32, c0=c0, seed=5, ldc=n + 3)
+
+
+def test_gemm_empty(lib):
+    f8 = torch.float8_e4m3fn
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    for dtype in DT.values():
+        c = lib.block128_gemm(z(5, 0).to(f8), z(0, 5), z(130, 0).to(f8), z(2, 0), c_dtype=dtype)
+        assert c.shape == (5, 130) and not c.any()
+        for m, n in ((0, 8), (8, 0)):
+            assert lib.block128_gemm(z(m, 32).to(f8), z(1, m), z(n, 32).to(f8), z(-(-n // 128), 1), c_dtype=dtype).shape == (m, n)
+    c = torch.ones(5, 130, device="cuda")
+    lib.block128_gemm(z(5, 0).to(f8), z(0, 5), z(130, 0).to(f8), z(2, 0), c=c, accumulate=True)
+    assert torch.equal(c, torch.ones_like(c))
+
+
+@pytest.mark.parametrize("m", [2, 40, 300])
+def test_gemm_batches_equal_single_calls(lib, m):
+    rng = np.random.default_rng(8)
+    x = torch.from_numpy(rng.standard_normal((3, m, 272)).astype(np.float32)).cuda()
+    w = torch.from_numpy(rng.standard_normal((3, 200, 272)).astype(np.float32)).cuda()
+    a, sa, _, _ = lib.block128_quantize(x)
+    for b_block in (1, 128):
+        b, sb, _, _ = lib.block128_quantize(w, square=b_block == 128)
+        for dtype in DT.values():
+            c = lib.block128_gemm(a, sa, b, sb, b_block=b_block, c_dtype=dtype)
+            for i in range(3):
+                one = lib.block128_gemm(a[i], sa[i].contiguous(), b[i], sb[i].contiguous(), b_block=b_block, c_dtype=dtype)
+                # sizes choose the kernel, so a batch may sum in another order than its parts
+                host = [t[i].float().cpu().numpy() for t in (a, sa, b, sb)]
+                da = host[0].astype(np.float64) * np.repeat(host[1].T, 128, 1)[:, :272]
+                sbx = host[3].T if b_block == 1 else np.repeat(host[3], 128, 0)[:200]
+                db = host[2].astype(np.float64) * np.repeat(sbx, 128, 1)[:, :272]
+                ref, s = da @ db.T, np.abs(da) @ np.abs(db).T
+                for got in (c[i], one):
+                    assert (np.abs(got.double().cpu().numpy() - ref) <= bound(s, ref, 272, dtype)).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 200, 512), (40, 300, 1024), (300, 300, 512), (700, 900, 1024)])
+def test_gemm_scales_and_codes_that_are_not_numbers(lib, m, n, k):
+    """A NaN or infinite scale, or a NaN code, reaches exactly the outputs of its row or column."""
+    a, sa, b, sb = upload(*operands(m, n, k, 0, 0, 1, 3), 0, 0)
+    for dtype in DT.values():
+        s2 = sa.clone()
+        s2[k // 128 - 1, m - 1] = float("nan")
+        c = lib.block128_gemm(a, s2, b, sb, b_block=1, c_dtype=dtype)
+        assert torch.isnan(c[m - 1]).all() and torch.isfinite(c[:m - 1]).all()
+        b2 = b.clone()
+        b2.view(torch.uint8)[n - 1, k - 1] = 0x7F
+        c = lib.block128_gemm(a, sa, b2, sb, b_block=1, c_dtype=dtype)
+        assert torch.isnan(c[:, n - 1]).all() and torch.isfinite(c[:, :n - 1]).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 500, 4096), (64, 512, 2048), (500, 520, 1024)])
+def test_gemm_repeats_bit_for_bit_and_in_a_graph(lib, m, n, k):
+    ops = upload(*operands(m, n, k, 0, 0, 128, 6), 0, 0)
+    for dtype in DT.values():
+        first = lib.block128_gemm(*ops, c_dtype=dtype)
+        out = torch.empty_like(first)
+        lib.block128_gemm(*ops, c=out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lib.block128_gemm(*ops, c=out)
+        for _ in range(3):
+            out.fill_(1)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, first)
+            assert torch.equal(lib.block128_gemm(*ops, c_dtype=dtype), first)
+
+
+def test_on_another_stream(lib):
+    s = torch.cuda.Stream()
+    x = values((300, 512), 1, torch.bfloat16).cuda()
+    w = values((400, 512), 2, torch.float32).cuda()
+    torch.cuda.synchronize()
+    q, sq, _, _ = lib.block128_quantize(x, stream=s)
+    wq, ws, _, _ = lib.block128_quantize(w, square=True, stream=s)
+    c = lib.block128_gemm(q, sq, wq, ws, c_dtype=torch.float32, stream=s)
+    s.synchronize()
+    here = lib.block128_gemm(*lib.block128_quantize(x)[:2], *lib.block128_quantize(w, square=True)[:2], c_dtype=torch.float32)
+    assert torch.equal(c, here)
+
+
+def test_training_products_of_a_layer(lib):
+    """y = x w^T, dx = dy w, dw = dy^T x from quantised operands, against float64 on the dequantised ones."""
+    T, N, K = 333, 272, 400
+    x, w, dy = values((T, K), 1, torch.bfloat16), values((N, K), 2, torch.float32), values((T, N), 3, torch.bfloat16)
+    xq, xs, xt, xts = lib.block128_quantize(x.cuda(), 0, True, True)
+    wq, ws, wt, wts = lib.block128_quantize(w.cuda(), 0, True, True, square=True)
+    gq, gs, gt, gts = lib.block128_quantize(dy.cuda(), 1, True, True)
+    y = lib.block128_gemm(xq, xs, wq, ws, c_dtype=torch.float32)
+    dx = lib.block128_gemm(gq, gs, wt, wts, c_dtype=torch.float32)
+    dw = lib.block128_gemm(gt, gts, xt, xts, b_block=1, c_dtype=torch.float32)
+    code = lambda t: t.view(torch.uint8).cpu().numpy()  # noqa: E731
+    deq = lambda q, s, f, sq: B.dequantize(code(q), s.cpu().numpy(), f, sq)  # noqa: E731
+    for got, a, b, k in ((y, deq(xq, xs, 0, False), deq(wq, ws, 0, True), K), (dx, deq(gq, gs, 1, False), deq(wt, wts, 0, True), N),
+                         (dw, deq(gt, gts, 1, False), deq(xt, xts, 0, False), T)):
+        ref, s = a @ b.T, np.abs(a) @ np.abs(b).T
+        assert (np.abs(got.double().cpu().numpy() - ref) <= bound(s, ref, k + 16, torch.float32)).all()
+    assert np.array_equal(code(wt)[:, :N], code(wq)[:, :K].T)
+    assert decode(code(xq), 0).shape == (T, K)
