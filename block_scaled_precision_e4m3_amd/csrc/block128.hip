@@ -5,7 +5,7 @@
 #include <initializer_list>
 
 #include "../../include/mxgemm.h"
-#include "block128_gemm.hpp"
+#include "block128_launch.hpp"
 #include "block128_quantize.hpp"
 #include "host_checks.hpp"
 
@@ -74,16 +74,32 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
   // a tile's 256 rows of A, B or C are addressed with 32-bit byte offsets
   if (M > top || N > top || L > top || K > (1LL << 23) - 16 || ldc > (1LL << 21)) return MXG_ERR_SHAPE;
   if (L * cdiv(M, 32) > 0x7FFFFFFFLL / std::max<int64_t>(1, cdiv(N, 32))) return MXG_ERR_SHAPE;
+  // K steps of all tiles are counted in 32 bits
+  if (L * cdiv(M, 32) * cdiv(N, 32) > 0x7FFFFFFFLL / (cdiv(K, 128) + 1) * 16) return MXG_ERR_SHAPE;
   if (K % 16 != 0) return MXG_ERR_ALIGN;
   return MXG_OK;
 }
 
-template <int FA, int FB>
-void launch_plain(const GemmParams& p, int ct, hipStream_t s) {
-  const dim3 g((unsigned)(p.L * cdiv(p.M, 32) * cdiv(p.N, 32))), b(64);
-  if (ct == MXG_DT_F32) hipLaunchKernelGGL((mxg::b128::block128_plain_kernel<FA, FB, 0>), g, b, 0, s, p);
-  else if (ct == MXG_DT_BF16) hipLaunchKernelGGL((mxg::b128::block128_plain_kernel<FA, FB, 1>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((mxg::b128::block128_plain_kernel<FA, FB, 2>), g, b, 0, s, p);
+// Which kernel and tile.  kind 0: rows of A straight from memory; 1: tiles of bm x bn.
+struct Choice {
+  int kind, bm, bn, mt, nt;
+  int64_t grid;
+};
+
+Choice choose(int64_t M, int64_t N, int64_t L, bool exact, int cus) {
+  if (M <= 64) {
+    const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4, nt = mt == 1 || L * cdiv(N, 32) < 2 * cus ? 1 : 2;
+    return {0, 16 * mt, 16 * nt, mt, nt, L * cdiv(N, 16 * nt)};
+  }
+  if (exact) {
+    const int64_t t = L * cdiv(M, 256) * cdiv(N, 128);
+    if (t >= cus) return {1, 256, 128, 0, 0, std::min<int64_t>(t, cus)};
+    return {1, 128, 128, 0, 0, std::min<int64_t>(L * cdiv(M, 128) * cdiv(N, 128), 2 * cus)};
+  }
+  const int64_t t = L * cdiv(M, 256) * cdiv(N, 256), t128 = L * cdiv(M, 128) * cdiv(N, 128);
+  if (t >= cus) return {1, 256, 256, 0, 0, std::min<int64_t>(t, cus)};
+  if (t128 >= cus) return {1, 128, 128, 0, 0, std::min<int64_t>(t128, 2 * cus)};
+  return {1, 64, 64, 0, 0, std::min<int64_t>(L * cdiv(M, 64) * cdiv(N, 64), 2 * cus)};
 }
 
 }  // namespace
@@ -173,14 +189,29 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
   p.b_rows = (flags & MXG_B128_B_ROWS) != 0;
   p.accumulate = (flags & MXG_B128_ACCUMULATE) != 0;
   hipStream_t s = (hipStream_t)stream;
-  if (a_fmt == MXG_FMT_E4M3) {
-    if (b_fmt == MXG_FMT_E4M3) launch_plain<0, 0>(p, c_dtype, s);
-    else launch_plain<0, 1>(p, c_dtype, s);
-  } else {
-    if (b_fmt == MXG_FMT_E4M3) launch_plain<1, 0>(p, c_dtype, s);
-    else launch_plain<1, 1>(p, c_dtype, s);
+  if (K == 0) {
+    if (p.accumulate) return MXG_OK;
+    const dim3 g((unsigned)std::min<int64_t>(cdiv(L * M * N, 256), 16LL * cus)), b(256);
+    if (c_dtype == MXG_DT_F32) hipLaunchKernelGGL((mxg::b128::block128_zero_kernel<0>), g, b, 0, s, p);
+    else if (c_dtype == MXG_DT_BF16) hipLaunchKernelGGL((mxg::b128::block128_zero_kernel<1>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((mxg::b128::block128_zero_kernel<2>), g, b, 0, s, p);
+    return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
   }
-  return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
+  const bool exact = c_dtype == MXG_DT_F32;
+  const int per16 = exact ? 4 : 8;
+  p.c_vec = aligned16(C) && ldc % per16 == 0 && N % per16 == 0;
+  const Choice ch = choose(M, N, L, exact, cus);
+  p.tilesM = (int)cdiv(M, ch.bm);
+  p.tilesN = (int)cdiv(N, ch.bn);
+  p.num_tiles = (int)(L * p.tilesM * p.tilesN);
+  p.xcd_remap = ch.grid % 8 == 0;
+  hipError_t e;
+  if (ch.kind == 0) e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.mt, ch.nt, ch.grid, s);
+  else if (exact) e = (ch.bm == 256 ? mxg::b128::launch_exact256 : mxg::b128::launch_exact128)(p, a_fmt, b_fmt, ch.grid, s);
+  else if (ch.bm == 256) e = mxg::b128::launch_tile256(p, a_fmt, b_fmt, c_dtype, ch.grid, s);
+  else if (ch.bm == 128) e = mxg::b128::launch_tile128(p, a_fmt, b_fmt, c_dtype, ch.grid, s);
+  else e = mxg::b128::launch_tile64(p, a_fmt, b_fmt, c_dtype, ch.grid, s);
+  return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 
 }  // extern "C"
