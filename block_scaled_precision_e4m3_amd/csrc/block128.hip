@@ -80,27 +80,55 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
   return MXG_OK;
 }
 
-// Which kernel and tile.  kind 0: rows of A straight from memory; 1: tiles of bm x bn.
+// Which kernel, tile and division of K.  rows: a kernel for up to 16 rows of A.
+//
+// Tiles: the time in microseconds of a tile size is taken as
+//   rounds of work items over the compute units x (blocks of K x block + end)
+// and, where K is divided, the second kernel that adds the parts up.  block and
+// end were measured on MI355X, one size forced at a time: 16-bit C, tiles of 64
+// (300x2048x7168: 15.4 us), 128 (2048x2048x2048: 13.2 us, with 64 20.4 us and
+// with 256 30.8 us) and 256 (4096x4096x4096: 63 us, with 128 73 us); float32 C,
+// 64 (300x1024x4096: 15.3 us), 128 (2048x2048x2048: 22 us, with 64 30 us) and
+// 256 x 128 (4096x4096x4096: 129 us, with 128 135 us).  K is divided only where
+// tiles leave compute units idle: 64x1024x7168 in 4 parts 10.3 us, in one 14.8.
 struct Choice {
-  int kind, bm, bn, mt, nt;
-  int64_t grid;
+  int rows;                // columns per workgroup of the rows kernel, 0: tiles
+  int bm, bn, kb, splits;  // tile; blocks of K per step; parts of K
 };
 
-Choice choose(int64_t M, int64_t N, int64_t L, bool exact, int cus) {
-  if (M <= 64) {
-    const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4, nt = mt == 1 || L * cdiv(N, 32) < 2 * cus ? 1 : 2;
-    return {0, 16 * mt, 16 * nt, mt, nt, L * cdiv(N, 16 * nt)};
+constexpr int kUnits = 256;  // compute units: the choice, and with it the workspace, must not need a device
+
+Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
+  // a rows workgroup reads A once for its columns, so more columns are better as long as they leave enough
+  // workgroups (7168 columns: 32 at a time 4.9 us, 16 5.1 us; 4096: 7.3 and 5.8 us; K = 2048 and 4096)
+  if (M <= 16) return {L * cdiv(N, 32) >= kUnits * 3 / 4 ? 32 : 16, 16, 0, 1, 1};
+  struct Size {
+    int bm, bn, kb;
+    double block, end;
+  };
+  static constexpr Size kSizes[2][3] = {{{64, 64, 2, 0.24, 0.5}, {128, 128, 2, 0.6, 1.0}, {256, 256, 1, 1.95, 3.0}},
+                                        {{64, 64, 2, 0.40, 0.7}, {128, 128, 2, 1.05, 1.5}, {256, 128, 1, 1.9, 2.0}}};
+  const int64_t blocks = cdiv(K, 128);
+  Choice best{};
+  double best_time = 0;
+  for (const Size& t : kSizes[exact]) {
+    const int64_t tiles = L * cdiv(M, t.bm) * cdiv(N, t.bn), steps = cdiv(blocks, t.kb);
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (t.bm == 256 || splits > steps || tiles * (splits - 1) >= kUnits)) break;
+      const int64_t per = cdiv(steps, splits), parts = cdiv(steps, per);
+      double time = (double)cdiv(tiles * parts, kUnits) * (per * t.kb * t.block + t.end);
+      if (parts > 1) time += 4.0 + parts * L * M * N * 8 / 3e6;  // written and read at 3 TB/s
+      if (best.bm == 0 || time < best_time) {
+        best = {0, t.bm, t.bn, t.kb, (int)parts};
+        best_time = time;
+      }
+    }
   }
-  if (exact) {
-    const int64_t t = L * cdiv(M, 256) * cdiv(N, 128);
-    if (t >= cus) return {1, 256, 128, 0, 0, std::min<int64_t>(t, cus)};
-    return {1, 128, 128, 0, 0, std::min<int64_t>(L * cdiv(M, 128) * cdiv(N, 128), 2 * cus)};
-  }
-  const int64_t t = L * cdiv(M, 256) * cdiv(N, 256), t128 = L * cdiv(M, 128) * cdiv(N, 128);
-  if (t >= cus) return {1, 256, 256, 0, 0, std::min<int64_t>(t, cus)};
-  if (t128 >= cus) return {1, 128, 128, 0, 0, std::min<int64_t>(t128, 2 * cus)};
-  return {1, 64, 64, 0, 0, std::min<int64_t>(L * cdiv(M, 64) * cdiv(N, 64), 2 * cus)};
+  return best;
 }
+
+// float32 columns of a row of the parts' sums
+int64_t sums_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
 }  // namespace
 
@@ -149,8 +177,10 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
 }
 
 size_t mxgemm_block128_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int c_dtype) {
-  (void)M, (void)N, (void)K, (void)L, (void)c_dtype;
-  return 0;
+  if (check_gemm(N, M, N, K, L, MXG_FMT_E4M3, MXG_FMT_E4M3, c_dtype, 0) != MXG_OK || M == 0 || N == 0 || K == 0 || L == 0)
+    return 0;
+  const Choice ch = choose(M, N, K, L, c_dtype == MXG_DT_F32);
+  return ch.splits > 1 ? (size_t)(ch.splits * L * M * sums_ld(N) * 4) : 0;
 }
 
 int mxgemm_block128(const void* A, const float* SA, const void* B, const float* SB, void* C, int64_t ldc, int64_t M,
@@ -200,17 +230,47 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
   const bool exact = c_dtype == MXG_DT_F32;
   const int per16 = exact ? 4 : 8;
   p.c_vec = aligned16(C) && ldc % per16 == 0 && N % per16 == 0;
-  const Choice ch = choose(M, N, L, exact, cus);
+  const Choice ch = choose(M, N, K, L, exact);
+  if (ch.rows) {
+    p.tilesN = (int)cdiv(N, ch.rows);
+    const hipError_t e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.rows, L * p.tilesN, s);
+    return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
+  }
   p.tilesM = (int)cdiv(M, ch.bm);
   p.tilesN = (int)cdiv(N, ch.bn);
   p.num_tiles = (int)(L * p.tilesM * p.tilesN);
-  p.xcd_remap = ch.grid % 8 == 0;
+  p.steps = (int)cdiv(p.Kb, ch.kb);
+  p.per = (int)cdiv(p.steps, ch.splits);
+  p.splits = ch.splits;
+  const int64_t grid = std::min<int64_t>((int64_t)p.num_tiles * p.splits, cus);
+  p.xcd_remap = grid % 8 == 0;
+  GemmParams last = p;  // what adds the parts up
+  if (p.splits > 1) {
+    p.sums = last.sums = static_cast<float*>(workspace);
+    p.ldw = last.ldw = (int)sums_ld(N);
+    if (exact) {
+      // a part's sums are a float32 C of their own
+      p.C = workspace;
+      p.ldc = p.ldw;
+      p.c_vec = N % 4 == 0;
+      p.accumulate = false;
+    }
+  }
   hipError_t e;
-  if (ch.kind == 0) e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.mt, ch.nt, ch.grid, s);
-  else if (exact) e = (ch.bm == 256 ? mxg::b128::launch_exact256 : mxg::b128::launch_exact128)(p, a_fmt, b_fmt, ch.grid, s);
-  else if (ch.bm == 256) e = mxg::b128::launch_tile256(p, a_fmt, b_fmt, c_dtype, ch.grid, s);
-  else if (ch.bm == 128) e = mxg::b128::launch_tile128(p, a_fmt, b_fmt, c_dtype, ch.grid, s);
-  else e = mxg::b128::launch_tile64(p, a_fmt, b_fmt, c_dtype, ch.grid, s);
+  if (exact) {
+    const auto f = ch.bm == 256 ? mxg::b128::launch_exact256 : ch.bm == 128 ? mxg::b128::launch_exact128 : mxg::b128::launch_exact64;
+    e = f(p, a_fmt, b_fmt, grid, s);
+  } else {
+    const auto f = ch.bm == 256 ? mxg::b128::launch_tile256 : ch.bm == 128 ? mxg::b128::launch_tile128 : mxg::b128::launch_tile64;
+    e = f(p, a_fmt, b_fmt, c_dtype, grid, s);
+  }
+  if (e == hipSuccess && p.splits > 1) {
+    const dim3 g((unsigned)std::min<int64_t>(cdiv(L * M * (last.ldw / 4), 256), 8LL * cus)), b(256);
+    if (exact) hipLaunchKernelGGL((mxg::b128::block128_sum_kernel<0>), g, b, 0, s, last, p.splits);
+    else if (c_dtype == MXG_DT_BF16) hipLaunchKernelGGL((mxg::b128::block128_sum_kernel<1>), g, b, 0, s, last, p.splits);
+    else hipLaunchKernelGGL((mxg::b128::block128_sum_kernel<2>), g, b, 0, s, last, p.splits);
+    e = hipGetLastError();
+  }
   return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 

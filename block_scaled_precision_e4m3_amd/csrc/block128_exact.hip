@@ -5,10 +5,15 @@ namespace mxg {
 namespace b128 {
 
 hipError_t launch_exact256(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s) {
-  return launch_exact<TileShape<256, 128, 4, 2, 2>>(p, fa, fb, grid, s);
+  return launch_exact<Exact256>(p, fa, fb, grid, s);
 }
+
 hipError_t launch_exact128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s) {
-  return launch_exact<TileShape<128, 128, 2, 2, 2>>(p, fa, fb, grid, s);
+  return launch_exact<Exact128>(p, fa, fb, grid, s);
+}
+
+hipError_t launch_exact64(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s) {
+  return launch_exact<Exact64>(p, fa, fb, grid, s);
 }
 
 }  // namespace b128

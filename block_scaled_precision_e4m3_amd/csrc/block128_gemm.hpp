@@ -27,23 +27,30 @@ struct GemmParams {
   int M, N, K, L;
   int Kb, Nb;        // ceil(K / 128), ceil(N / 128)
   int tilesM, tilesN, num_tiles, xcd_remap;
+  int steps, splits, per;  // steps of a tile's whole K; parts it is cut into, of `per` steps each (the last may be shorter)
+  float* sums;       // splits > 1: (splits, L, M, ldw) float32 partial sums in place of C
+  int ldw;
   bool b_rows, accumulate;
   bool c_vec;        // 16-byte stores of C: base, ldc and N in multiples of 16 bytes
 };
 
 constexpr unsigned kOob = 0x80000000u;  // an offset past every resource: reads as zero, is not stored
 
-// A tile of BM x BN outputs by WM x WN waves, operands in a ring of NST stages.
-template <int BM, int BN, int WM, int WN, int NST>
+// A tile of BM x BN outputs by WM x WN waves, operands in a ring of NST stages of KB blocks of K each, moved by the
+// same waves (NP = 0) or by NP more that do nothing else.
+template <int BM, int BN, int WM, int WN, int NST, int KB, int NP = 0>
 struct TileShape {
-  static constexpr int kBM = BM, kBN = BN, kWaves = WM * WN, kWn = WN, kStages = NST;
+  static constexpr int kBM = BM, kBN = BN, kWaves = WM * WN, kWn = WN, kStages = NST, kKB = KB;
+  static constexpr int kProducers = NP, kDmaWaves = NP ? NP : kWaves, kAllWaves = kWaves + NP;
   static constexpr int kTM = BM / WM, kTN = BN / WN;     // a wave's outputs
   static constexpr int kOffB = BM * 128, kOffSA = kOffB + BN * 128, kOffSB = kOffSA + BM * 4;
-  static constexpr int kStage = kOffSB + BN * 4;
-  static constexpr int kDa = BM / 8 / kWaves, kDb = BN / 8 / kWaves;  // operand DMA instructions per wave and step
-  static constexpr int kIssued = kDa + kDb + 1;                       // and the scales'
-  static_assert(kWaves % 4 == 0 && (BM / 8) % kWaves == 0 && (BN / 8) % kWaves == 0, "DMA shares");
-  static_assert(BM % 64 == 0 && BN % 64 == 0 && BM / 64 + BN / 64 <= kWaves, "one scale DMA per wave");
+  static constexpr int kBlock = kOffSB + BN * 4;         // LDS bytes of one block of K
+  static constexpr int kStage = KB * kBlock;
+  static constexpr int kDa = BM / 8 / kDmaWaves, kDb = BN / 8 / kDmaWaves;  // operand DMA instructions per wave and step
+  static constexpr int kPerBlock = kDa + kDb + 1;                     // and the scales', for one block
+  static constexpr int kIssued = KB * kPerBlock;
+  static_assert(kDmaWaves % 4 == 0 && (BM / 8) % kDmaWaves == 0 && (BN / 8) % kDmaWaves == 0, "DMA shares");
+  static_assert(BM % 64 == 0 && BN % 64 == 0 && BM / 64 + BN / 64 <= kDmaWaves, "one scale DMA per wave");
   static_assert(kTN % 32 == 0 && 128 % kTN == 0, "one 128-column block per wave");
   static constexpr int kLds = NST * kStage + 256;        // and where waves without scales to fetch write zeros
   static_assert(kLds <= 160 * 1024, "LDS");
@@ -62,8 +69,18 @@ __device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t rs, unsigned voff
 struct TileAt {
   int l, m0, n0;
 };
-// Tile t: batches, then groups of kGroupM tile rows walked column by column.
+struct Part {
+  int at, count;  // first step and number of steps
+};
+__device__ __forceinline__ Part part_of(const GemmParams& p, int item) {
+  if (p.splits == 1) return {0, p.steps};
+  const int at = __builtin_amdgcn_readfirstlane(item / p.num_tiles * p.per);
+  return {at, min(p.per, p.steps - at)};
+}
+// Tile t: batches, then groups of kGroupM tile rows walked column by column.  A work item is a tile and a part of
+// its K; items of one part follow each other.
 __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int bm, int bn) {
+  if (p.splits > 1) t %= p.num_tiles;
   const int per = p.tilesM * p.tilesN, l = t / per, r = t - l * per;
   const int group = kGroupM * p.tilesN, g = r / group, first = g * kGroupM;
   const int rows = min(p.tilesM - first, kGroupM), rg = r - g * group;
@@ -84,22 +101,23 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int bm, in
 template <class T, bool BROWS, int (*SwA)(int), int (*SwB)(int)>
 struct Stream {
   const GemmParams& p;
-  const int wave, G;
-  int tile, step = 0;       // of the next step to fetch
+  const int wave, G, items;
+  int item, left = 0;       // of the next step to fetch: its work item and the steps that are left of it
+  unsigned k;               // and its first K
   unsigned lds0, chunk_a, chunk_b, row_k, next_k;
   __amdgpu_buffer_rsrc_t ra, rb;
-  const char* sc_at;        // the step's scales: the first waves fetch A's, 64 rows each, the next ones B's
+  const char* sc_at;        // the block's scales: the first waves fetch A's, 64 rows each, the next ones B's
   unsigned sc_bytes, sc_voff, sc_inc;
-  unsigned base, va, vb;    // of the step being fetched
+  unsigned base, va[T::kKB], vb[T::kKB];  // of the step being fetched
 
-  __device__ __forceinline__ Stream(const GemmParams& p_, const uint8_t* lds, int lane, int wave_, int t0)
-      : p(p_), wave(wave_), G((int)gridDim.x), tile(t0) {
+  __device__ __forceinline__ Stream(const GemmParams& p_, const uint8_t* lds, int lane, int wave_, int first)
+      : p(p_), wave(wave_), G((int)gridDim.x), items(p_.num_tiles * p_.splits), item(first) {
     lds0 = lds_addr(lds);
     const int row = 8 * wave + (lane >> 3);
     chunk_a = (unsigned)((lane & 7) ^ SwA(row)) * 16;
     chunk_b = (unsigned)((lane & 7) ^ SwB(row)) * 16;
     row_k = (unsigned)row * (unsigned)p.K;
-    next_k = 8u * T::kWaves * (unsigned)p.K;
+    next_k = 8u * T::kDmaWaves * (unsigned)p.K;
     const unsigned mine = (unsigned)(wave < T::kBM / 64 ? wave : wave - T::kBM / 64) * 64 + lane;
     sc_voff = 4 * mine;
     if (!BROWS && wave >= T::kBM / 64)  // one scale per 128 columns: lane j takes block j of the tile
@@ -110,47 +128,59 @@ struct Stream {
   __device__ __forceinline__ void open() {
     TileAt f{0, 0, 0};
     unsigned mv = 0, nv = 0;
-    if (tile < p.num_tiles) {
-      f = tile_at(p, tile, T::kBM, T::kBN);
+    int at = 0;
+    left = 0x7FFFFFFF;
+    if (item < items) {
+      f = tile_at(p, item, T::kBM, T::kBN);
       mv = (unsigned)min(p.M - f.m0, T::kBM);
       nv = (unsigned)min(p.N - f.n0, T::kBN);
+      const Part part = part_of(p, item);
+      at = T::kKB * part.at;
+      left = part.count;
     }
+    k = 128u * (unsigned)at;
     ra = make_rsrc(p.A + ((int64_t)f.l * p.M + f.m0) * p.K, mv * (unsigned)p.K);
     rb = make_rsrc(p.B + ((int64_t)f.l * p.N + f.n0) * p.K, nv * (unsigned)p.K);
     if (wave < T::kBM / 64) {
-      sc_at = (const char*)(p.SA + (int64_t)f.l * p.Kb * p.M + f.m0);
+      sc_at = (const char*)(p.SA + ((int64_t)f.l * p.Kb + at) * p.M + f.m0);
       sc_bytes = 4 * mv;
     } else if constexpr (BROWS) {
-      sc_at = (const char*)(p.SB + (int64_t)f.l * p.Kb * p.N + f.n0);
+      sc_at = (const char*)(p.SB + ((int64_t)f.l * p.Kb + at) * p.N + f.n0);
       sc_bytes = 4 * nv;
     } else {
       const int nb = min(p.Nb - f.n0 / 128, (T::kBN + 127) / 128);
-      sc_at = (const char*)(p.SB + ((int64_t)f.l * p.Nb + f.n0 / 128) * p.Kb);
+      sc_at = (const char*)(p.SB + ((int64_t)f.l * p.Nb + f.n0 / 128) * p.Kb + at);
       sc_bytes = nv ? 4u * (unsigned)((nb - 1) * p.Kb + 1) : 0u;
     }
+    if (wave >= T::kBM / 64 + T::kBN / 64) sc_bytes = 0;
   }
   __device__ __forceinline__ void begin(int stage) {
     base = lds0 + (unsigned)(stage * T::kStage) + 1024 * (unsigned)wave;
-    const unsigned k0 = 128u * (unsigned)step;
-    va = k0 + chunk_a < (unsigned)p.K ? row_k + k0 + chunk_a : kOob;
-    vb = k0 + chunk_b < (unsigned)p.K ? row_k + k0 + chunk_b : kOob;
+#pragma unroll
+    for (int b = 0; b < T::kKB; ++b) {
+      va[b] = k + 128 * b + chunk_a < (unsigned)p.K ? row_k + k + 128 * b + chunk_a : kOob;
+      vb[b] = k + 128 * b + chunk_b < (unsigned)p.K ? row_k + k + 128 * b + chunk_b : kOob;
+    }
   }
   // One of the step's kIssued DMA instructions (every wave issues as many, some on an empty resource, so that
   // waits can count them).
-  __device__ __forceinline__ void one(int q) {
-    if (q < T::kDa) dma16_at(ra, va + q * next_k, base + 1024 * T::kWaves * q);
-    else if (q < T::kDa + T::kDb) dma16_at(rb, vb + (q - T::kDa) * next_k, base + T::kOffB + 1024 * T::kWaves * (q - T::kDa));
+  __device__ __forceinline__ void one(int i) {
+    const int b = i / T::kPerBlock, q = i % T::kPerBlock;
+    const unsigned to = base + b * T::kBlock;
+    if (q < T::kDa) dma16_at(ra, va[b] + q * next_k, to + 1024 * T::kDmaWaves * q);
+    else if (q < T::kDa + T::kDb) dma16_at(rb, vb[b] + (q - T::kDa) * next_k, to + T::kOffB + 1024 * T::kDmaWaves * (q - T::kDa));
     else {
       const bool any = wave < T::kBM / 64 + T::kBN / 64;
-      dma4_at(make_rsrc(sc_at, any ? sc_bytes : 0u), sc_voff,
-              any ? base + T::kOffSA - 768 * (unsigned)wave : lds0 + T::kStages * T::kStage);
+      const bool in = T::kKB == 1 || k + 128 * b < (unsigned)p.K;  // a step's last blocks may lie past K
+      dma4_at(make_rsrc(sc_at + (in ? b : 0) * sc_inc, in ? sc_bytes : 0u), sc_voff,
+              any ? to + T::kOffSA - 768 * (unsigned)wave : lds0 + T::kStages * T::kStage);
     }
   }
   __device__ __forceinline__ void end() {
-    sc_at += sc_inc;
-    if (++step == p.Kb) {
-      step = 0;
-      tile += G;
+    sc_at += T::kKB * sc_inc;
+    k += 128 * T::kKB;
+    if (--left == 0) {
+      item += G;
       open();
     }
   }
@@ -173,6 +203,23 @@ __device__ __forceinline__ void wait_step(bool stores_fixed, bool stores_behind)
   if (!stores_behind) wait_vm<kAhead>();
   else if (stores_fixed) wait_vm<kAhead + kStores>();
   else wait_vm<0>();
+}
+
+// A wave that only moves operands: it meets the computing waves at their barrier of every step, when its DMA of that
+// step has landed, and then refills the stage they have left.  A wave whose DMA instruction finds the queue full
+// issues nothing until it drains, which these waves can afford.
+template <class T, class S>
+__device__ __forceinline__ void produce(const GemmParams& p, S& in, int item, int items) {
+  for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
+  int stage = 0;
+  for (; item < items; item += (int)gridDim.x)
+    for (int n = part_of(p, item).count; n > 0; --n) {
+      wait_vm<(T::kStages - 2) * T::kIssued>();
+      barrier();
+      in.all(stage == 0 ? T::kStages - 1 : stage - 1);
+      stage = stage + 1 == T::kStages ? 0 : stage + 1;
+    }
+  wait_vm<0>();  // no DMA may land after the workgroup's LDS is handed on
 }
 
 __device__ __forceinline__ int first_tile_of(const GemmParams& p) {
@@ -198,20 +245,27 @@ __device__ __forceinline__ int swizzle_a16(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swizzle_b16(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 
 template <class T, int FA, int FB, int CT, bool BROWS>
-__global__ __launch_bounds__(64 * T::kWaves, 2) void block128_tile_kernel(GemmParams p) {
+__global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void block128_tile_kernel(GemmParams p) {
   static_assert(CT != 0, "16-bit C");
   constexpr int kMt = T::kTM / 16, kNt = T::kTN / 16, kPairs = kNt / 2;
   constexpr int kStores = kMt * kPairs;                     // C store instructions per lane and tile
-  constexpr int kPerMt = (T::kIssued + kMt - 2) / (kMt - 1);  // DMA instructions between two rows of MFMAs
+  constexpr int kRows = T::kKB * kMt;                        // rows of MFMAs in a step
+  constexpr int kPerRow = (T::kIssued + kRows - 2) / (kRows - 1);  // DMA instructions between two of them
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave / T::kWn, wn = wave % T::kWn;
   const int r = lane & 15, g = lane >> 4;
   const int G = (int)gridDim.x;
-  int tile = first_tile_of(p);
-  const int total = (tile < p.num_tiles ? (p.num_tiles - 1 - tile) / G + 1 : 0) * p.Kb;  // steps (the host bounds it)
-  Stream<T, BROWS, swizzle_a16, swizzle_b16> in(p, lds, lane, wave, tile);
+  int item = first_tile_of(p);
+  const int items = p.num_tiles * p.splits;
+  Stream<T, BROWS, swizzle_a16, swizzle_b16> in(p, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
+  if constexpr (T::kProducers > 0) {
+    if (wave >= T::kWaves) {
+      produce<T>(p, in, item, items);
+      return;
+    }
+  }
 
   const int a_row = T::kTM * wm + r, b_row = T::kTN * wn + 8 * (r >> 2) + (r & 3);
   const unsigned a_off = (unsigned)(a_row * 128 + 16 * (g ^ swizzle_a16(a_row)));
@@ -222,32 +276,43 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void block128_tile_kernel(GemmPa
     return (v8i){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
 
-  for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
-  int step = 0, stage = 0;
+  if constexpr (T::kProducers == 0)
+    for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
+  int step = 0, stage = 0, count = item < items ? part_of(p, item).count : 0;
   bool stored = false;
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
   v4f acc[kMt][kNt];
-  for (int i = 0; i < total; ++i) {
-    wait_step<T, kStores>(p.c_vec, stored && step < T::kStages - 1);
+  while (item < items) {
+    if constexpr (T::kProducers == 0) wait_step<T, kStores>(p.c_vec && p.splits == 1, stored && step < T::kStages - 1);
     barrier();
     const uint8_t* st = lds + stage * T::kStage;
     const uint8_t *a_lo = st + a_off, *a_hi = st + (a_off ^ 64), *b_lo = st + b_off, *b_hi = st + (b_off ^ 64);
     const float* ssa = reinterpret_cast<const float*>(st + T::kOffSA) + a_row;
     const float* ssb = reinterpret_cast<const float*>(st + T::kOffSB) + (BROWS ? T::kTN * wn + 8 * g : T::kTN * wn / 128);
-    v8i b[kNt], a[3];
-    a[0] = frag(a_lo, a_hi, 0);
+    // row t of MFMAs is row t % kMt of block t / kMt; A's fragments come three rows ahead of their use
+    auto a_frag = [&](int t) { return frag(a_lo, a_hi, t / kMt * T::kBlock + 2048 * (t % kMt)); };
+    v8i b[T::kKB][kNt], a[3];
+    a[0] = a_frag(0);
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) b[nt] = frag(b_lo, b_hi, 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
-    a[1] = frag(a_lo, a_hi, 2048);
-    float sa[kMt];
+    for (int nt = 0; nt < kNt; ++nt) b[0][nt] = frag(b_lo, b_hi, 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
+    a[1] = a_frag(1);
+    float sa[T::kKB][kMt];
+    v4f sb[T::kKB][BROWS ? kNt : 1];
 #pragma unroll
-    for (int mt = 0; mt < kMt; ++mt) sa[mt] = ssa[16 * mt];
-    v4f sb[BROWS ? kNt : 1];
-    if constexpr (BROWS) {
+    for (int kb = 0; kb < T::kKB; ++kb) {
+      if (kb > 0) {
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) sb[nt] = *reinterpret_cast<const v4f*>(ssb + 32 * (nt >> 1) + 4 * (nt & 1));
-    } else {
-      sb[0][0] = ssb[0];
+        for (int nt = 0; nt < kNt; ++nt) b[kb][nt] = frag(b_lo, b_hi, kb * T::kBlock + 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
+      }
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) sa[kb][mt] = ssa[kb * (T::kBlock / 4) + 16 * mt];
+      if constexpr (BROWS) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt)
+          sb[kb][nt] = *reinterpret_cast<const v4f*>(ssb + kb * (T::kBlock / 4) + 32 * (nt >> 1) + 4 * (nt & 1));
+      } else {
+        sb[kb][0][0] = ssb[kb * (T::kBlock / 4)];
+      }
     }
     if (step == 0) {
 #pragma unroll
@@ -256,42 +321,59 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void block128_tile_kernel(GemmPa
         for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] = zero;
     }
     v4f part[2][kNt];
-    auto fold = [&](int mt, const v4f* pt) {
-      const float s0 = BROWS ? sa[mt] : sa[mt] * sb[0][0];
+    auto fold = [&](int t) {
+      const int kb = t / kMt, mt = t % kMt;
+      const v4f* pt = part[t & 1];
+      const float s0 = BROWS ? sa[kb][mt] : sa[kb][mt] * sb[kb][0][0];
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[mt][nt][e] = __builtin_fmaf(pt[nt][e], BROWS ? s0 * sb[nt][e] : s0, acc[mt][nt][e]);
+          acc[mt][nt][e] = __builtin_fmaf(pt[nt][e], BROWS ? s0 * sb[kb][nt][e] : s0, acc[mt][nt][e]);
         // keeps the multiply-adds here: moved past the step's branches, all parts would have to be kept
         asm volatile("" : "+v"(acc[mt][nt]));
       }
     };
     // the stage the step before used takes the DMA that is furthest ahead, issued between the rows of MFMAs
-    in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
+    if constexpr (T::kProducers == 0) in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
 #pragma unroll
-    for (int mt = 0; mt < kMt; ++mt) {
+    for (int t = 0; t < kRows; ++t) {
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt)
-        part[mt & 1][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[nt], a[mt % 3], zero, FB, FA, 0, 0, 0, 0);
-      if (mt + 2 < kMt) a[(mt + 2) % 3] = frag(a_lo, a_hi, 2048 * (mt + 2));
-      if (mt > 0) fold(mt - 1, part[(mt - 1) & 1]);
+        part[t & 1][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[t / kMt][nt], a[t % 3], zero, FB, FA, 0, 0, 0, 0);
+      if (t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
+      if (t > 0) fold(t - 1);
 #pragma unroll
       for (int q = 0; q < T::kIssued; ++q)
-        if (q / kPerMt == mt) in.one(q);
+        if (T::kProducers == 0 && q / kPerRow == t) in.one(q);
       __builtin_amdgcn_sched_barrier(0);
     }
-    fold(kMt - 1, part[(kMt - 1) & 1]);
-    in.end();
+    fold(kRows - 1);
+    if constexpr (T::kProducers == 0) in.end();
     stage = stage + 1 == T::kStages ? 0 : stage + 1;
 
-    if (++step == p.Kb) {
+    if (++step == count) {
       step = 0;
       stored = true;
-      const TileAt at = tile_at(p, tile, T::kBM, T::kBN);
-      tile += G;
-      using E = elem_t<CT>;
+      const TileAt at = tile_at(p, item, T::kBM, T::kBN);
       const int rows = min(p.M - at.m0, T::kBM);
+      if (p.splits > 1) {
+        // a part's sums, four columns at a time (ldw is a multiple of 4)
+        float* w = p.sums + (((int64_t)(item / p.num_tiles) * p.L + at.l) * p.M + at.m0) * p.ldw + at.n0;
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) {
+            const int m = a_row + 16 * mt, n = T::kTN * wn + 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
+            if (m < rows && at.n0 + n < p.ldw) *reinterpret_cast<v4f*>(w + (int64_t)m * p.ldw + n) = acc[mt][nt];
+          }
+        item += G;
+        count = item < items ? part_of(p, item).count : 0;
+        continue;
+      }
+      item += G;
+      count = item < items ? part_of(p, item).count : 0;
+      using E = elem_t<CT>;
       E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
       if (p.c_vec) {
         // N and ldc are multiples of 8 here: a lane's 8 columns lie inside or outside N together
@@ -369,109 +451,125 @@ __device__ __forceinline__ int swizzle_a32(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swizzle_b32(int row) { return ((row >> 1) & 1) | ((row >> 3) & 2) | (row & 4); }
 
 template <class T, int FA, int FB, bool BROWS>
-__global__ __launch_bounds__(64 * T::kWaves, 2) void block128_exact_kernel(GemmParams p) {
-  static_assert(T::kTM == 64 && T::kTN == 64, "64 x 64 outputs per wave");
-  constexpr int kStores = 16;
+__global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void block128_exact_kernel(GemmParams p) {
+  constexpr int kMt = T::kTM / 32, kNt = T::kTN / 32;  // a wave's MFMA blocks
+  constexpr int kStores = 4 * kMt * kNt;               // C store instructions per lane and tile
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave / T::kWn, wn = wave % T::kWn;
   const int r = lane & 31, h = lane >> 5;
   const int G = (int)gridDim.x;
-  int tile = first_tile_of(p);
-  const int total = (tile < p.num_tiles ? (p.num_tiles - 1 - tile) / G + 1 : 0) * p.Kb;
-  Stream<T, BROWS, swizzle_a32, swizzle_b32> in(p, lds, lane, wave, tile);
+  int item = first_tile_of(p);
+  const int items = p.num_tiles * p.splits;
+  Stream<T, BROWS, swizzle_a32, swizzle_b32> in(p, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
+  if constexpr (T::kProducers > 0) {
+    if (wave >= T::kWaves) {
+      produce<T>(p, in, item, items);
+      return;
+    }
+  } else {
+    for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
+  }
 
-  const int a_row = 64 * wm + r, b_row = 64 * wn + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);
+  const int a_row = T::kTM * wm + r, b_row = T::kTN * wn + 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);
   // a lane's chunk c of K (c = 0..3) is 2c + h of the row: at 32 c ^ its offset
   const unsigned a_off = (unsigned)(a_row * 128 + 16 * (h ^ swizzle_a32(a_row)));
   const unsigned b_off = (unsigned)(T::kOffB + b_row * 128 + 16 * (h ^ swizzle_b32(b_row)));
 
-  for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
-  int step = 0, stage = 0;
+  int step = 0, stage = 0, count = item < items ? part_of(p, item).count : 0;
   bool stored = false;
-  v16f acc[2][2];
-  for (int i = 0; i < total; ++i) {
-    wait_step<T, kStores>(p.c_vec && !p.accumulate, stored && step < T::kStages - 1);
+  v16f acc[kMt][kNt];
+  while (item < items) {
+    if constexpr (T::kProducers == 0) {
+      wait_step<T, kStores>(p.c_vec && !p.accumulate, stored && step < T::kStages - 1);
+    }
     barrier();
+    if constexpr (T::kProducers == 0) in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
     const uint8_t* st = lds + stage * T::kStage;
-    in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
     if (step == 0) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < kMt * kNt; ++t)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[t >> 1][t & 1][e] = 0.f;
+        for (int e = 0; e < 16; ++e) acc[t / kNt][t % kNt][e] = 0.f;
     }
-    v4u ra[2][2], rb[2][2];  // raw chunks: this one's and the next one's
-    auto read = [&](int c) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        ra[c & 1][t] = *reinterpret_cast<const v4u*>(st + (a_off ^ (32 * c)) + 4096 * t);
-        rb[c & 1][t] = *reinterpret_cast<const v4u*>(st + (b_off ^ (32 * c)) + 4096 * t);
-      }
-    };
-    v16f part[2][2];
-    read(0);
+    for (int kb = 0; kb < T::kKB; ++kb) {
+      const uint8_t* sk = st + kb * T::kBlock;
+      v4u ra[2][kMt], rb[2][kNt];  // raw chunks: this one's and the next one's
+      auto read = [&](int c) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c < 3) read(c + 1);
+        for (int t = 0; t < kMt; ++t) ra[c & 1][t] = *reinterpret_cast<const v4u*>(sk + (a_off ^ (32 * c)) + 4096 * t);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        v8bf a[2], b[2];
+        for (int t = 0; t < kNt; ++t) rb[c & 1][t] = *reinterpret_cast<const v4u*>(sk + (b_off ^ (32 * c)) + 4096 * t);
+      };
+      v16f part[kMt][kNt];
+      read(0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          a[t] = cvt8<FA>(ra[c & 1][t][2 * s], ra[c & 1][t][2 * s + 1], 1.f);
-          b[t] = cvt8<FB>(rb[c & 1][t][2 * s], rb[c & 1][t][2 * s + 1], 1.f);
-        }
+      for (int c = 0; c < 4; ++c) {
+        if (c < 3) read(c + 1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          v16f from = part[t >> 1][t & 1];
-          if (c == 0 && s == 0) {
+        for (int s = 0; s < 2; ++s) {
+          v8bf a[kMt], b[kNt];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) from[e] = 0.f;
+          for (int t = 0; t < kMt; ++t) a[t] = cvt8<FA>(ra[c & 1][t][2 * s], ra[c & 1][t][2 * s + 1], 1.f);
+#pragma unroll
+          for (int t = 0; t < kNt; ++t) b[t] = cvt8<FB>(rb[c & 1][t][2 * s], rb[c & 1][t][2 * s + 1], 1.f);
+#pragma unroll
+          for (int t = 0; t < kMt * kNt; ++t) {
+            v16f from = part[t / kNt][t % kNt];
+            if (c == 0 && s == 0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) from[e] = 0.f;
+            }
+            part[t / kNt][t % kNt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[t % kNt], a[t / kNt], from, 0, 0, 0);
           }
-          part[t >> 1][t & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[t & 1], a[t >> 1], from, 0, 0, 0);
+        }
+        if constexpr (T::kProducers == 0) {
+#pragma unroll
+          for (int q = 0; q < T::kPerBlock; ++q)
+            if (q / ((T::kPerBlock + 2) / 3) == c) in.one(kb * T::kPerBlock + q);
         }
       }
+      const float* ssa = reinterpret_cast<const float*>(sk + T::kOffSA) + a_row;
+      const float* ssb = reinterpret_cast<const float*>(sk + T::kOffSB) + (BROWS ? T::kTN * wn + 16 * h : T::kTN * wn / 128);
 #pragma unroll
-      for (int q = 0; q < T::kIssued; ++q)
-        if (q / ((T::kIssued + 2) / 3) == c) in.one(q);
-    }
-    in.end();
-    const float* ssa = reinterpret_cast<const float*>(st + T::kOffSA) + a_row;
-    const float* ssb = reinterpret_cast<const float*>(st + T::kOffSB) + (BROWS ? 64 * wn + 16 * h : 64 * wn / 128);
+      for (int n = 0; n < kNt; ++n) {
+        v4f sb[4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      v4f sb[4];
+        for (int q = 0; q < (BROWS ? 4 : 1); ++q) {
+          if constexpr (BROWS) sb[q] = *reinterpret_cast<const v4f*>(ssb + 32 * n + 4 * q);
+          else sb[0][0] = ssb[0];
+        }
 #pragma unroll
-      for (int q = 0; q < (BROWS ? 4 : 1); ++q) {
-        if constexpr (BROWS) sb[q] = *reinterpret_cast<const v4f*>(ssb + 32 * n + 4 * q);
-        else sb[0][0] = ssb[0];
-      }
+        for (int m = 0; m < kMt; ++m) {
+          const float sa = ssa[32 * m];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float sa = ssa[32 * m];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[m][n][e] = __builtin_fmaf(part[m][n][e], sa * (BROWS ? sb[e >> 2][e & 3] : sb[0][0]), acc[m][n][e]);
+          for (int e = 0; e < 16; ++e)
+            acc[m][n][e] = __builtin_fmaf(part[m][n][e], sa * (BROWS ? sb[e >> 2][e & 3] : sb[0][0]), acc[m][n][e]);
+        }
       }
     }
+    if constexpr (T::kProducers == 0) in.end();
     stage = stage + 1 == T::kStages ? 0 : stage + 1;
 
-    if (++step == p.Kb) {
+    if (++step == count) {
       step = 0;
       stored = true;
-      const TileAt at = tile_at(p, tile, T::kBM, T::kBN);
-      tile += G;
+      const TileAt at = tile_at(p, item, T::kBM, T::kBN);
+      // a part's sums go to the workspace, which the host has described as C: (splits, L, M, ldc)
+      const int l = at.l + (p.splits > 1 ? item / p.num_tiles * p.L : 0);
+      item += G;
+      count = item < items ? part_of(p, item).count : 0;
       const int rows = min(p.M - at.m0, T::kBM);
-      float* c = static_cast<float*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
+      float* c = static_cast<float*>(p.C) + ((int64_t)l * p.M + at.m0) * p.ldc + at.n0;
       if (p.c_vec) {
         // N and ldc are multiples of 4 here
         const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 4u * (unsigned)((int64_t)(rows - 1) * p.ldc + min(p.N - at.n0, T::kBN)));
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < kMt; ++m)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < kNt; ++n) {
             // quad q of row r (r % 4 = j) goes to lane j' = q of the four, as its quad of row j: a 4 x 4
             // transposition in two exchanges, with lane ^ 1 and lane ^ 2
             float v[4][4];
@@ -485,33 +583,44 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void block128_exact_kernel(GemmP
                 if (q & s) continue;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                  const float give = up ? v[q][w] : v[q | s][w];
-                  const int bits = __builtin_bit_cast(int, give);
-                  const float got = __builtin_bit_cast(float, s == 1 ? __builtin_amdgcn_mov_dpp(bits, 0xB1, 0xF, 0xF, true)
-                                                                     : __builtin_amdgcn_mov_dpp(bits, 0x4E, 0xF, 0xF, true));
-                  if (up) v[q][w] = got;
-                  else v[q | s][w] = got;
+                  const float x = v[q][w], y = v[q | s][w];
+                  const int give = __builtin_bit_cast(int, up ? x : y);
+                  const float got = __builtin_bit_cast(float, s == 1 ? __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true)
+                                                                     : __builtin_amdgcn_mov_dpp(give, 0x4E, 0xF, 0xF, true));
+                  v[q][w] = up ? got : x;
+                  v[q | s][w] = up ? y : got;
                 }
               }
             }
+            unsigned off[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int mm = (a_row & ~3) + q + 32 * m, nn = 64 * wn + 32 * n + 16 * h + 4 * (r & 3);
-              const bool in_c = mm < rows && at.n0 + nn < p.N;
-              const unsigned off = in_c ? 4u * (unsigned)(mm * (int)p.ldc + nn) : kOob;
-              v4f out = {v[q][0], v[q][1], v[q][2], v[q][3]};
-              if (p.accumulate) out += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off, 0, 0));
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, out), rc, (int)off, 0, 2);
+              const int mm = (a_row & ~3) + q + 32 * m, nn = T::kTN * wn + 32 * n + 16 * h + 4 * (r & 3);
+              off[q] = mm < rows && at.n0 + nn < p.N ? 4u * (unsigned)(mm * (int)p.ldc + nn) : kOob;
+            }
+            if (p.accumulate) {
+              v4u old[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) old[q] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off[q], 0, 0);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[q][w] += __uint_as_float(old[q][w]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const v4u out = {__float_as_uint(v[q][0]), __float_as_uint(v[q][1]), __float_as_uint(v[q][2]), __float_as_uint(v[q][3])};
+              __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 2);
             }
           }
       } else {
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < kMt; ++m)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kNt; ++n)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int mm = a_row + 32 * m, nn = 64 * wn + 32 * n + 16 * h + e;
+              const int mm = a_row + 32 * m, nn = T::kTN * wn + 32 * n + 16 * h + e;
               if (mm >= rows || at.n0 + nn >= p.N) continue;
               float* to = c + (int64_t)mm * p.ldc + nn;
               *to = (p.accumulate ? *to : 0.f) + acc[m][n][e];
@@ -519,131 +628,147 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void block128_exact_kernel(GemmP
       }
     }
   }
-  wait_vm<0>();
+  if constexpr (T::kProducers == 0) wait_vm<0>();
 }
 
 // --- few rows of A -----------------------------------------------------------------
 //
-// B is read once, straight from memory into the MFMA's registers: a workgroup
-// takes 16 NT columns and all rows (16 MT at most), its waves every kWaves-th
-// block of K, and the waves' sums meet in LDS in a fixed order.  B's bytes bound
-// it, so the waves only have to keep enough of them on the way: each loads U
-// blocks before it uses them.  Rows and columns past the matrix repeat the last
-// one and are not stored.  Lane (r, g) owns row 16 mt + r and columns 4g .. 4g + 3
-// of 16; a 16-bit C takes the 8-bit matrix cores, a float32 C the widened codes,
-// as in the tile kernels.
+// Up to 16 rows.  B is read once, straight from memory into the MFMA's
+// registers: a workgroup takes COLS columns, its W waves every W-th block of K,
+// and the waves' sums meet in LDS in a fixed order.  B's bytes bound it, so a
+// wave asks for its next block before it uses this one.  Rows and columns past
+// the matrix repeat the last one and are not stored.  Lane (r, g) owns row r and
+// columns 4g .. 4g + 3 of 16; a 16-bit C takes the 8-bit matrix cores, a float32
+// C the widened codes, as in the tile kernels.
 constexpr int kRowWaves = 8;
 
-template <int FA, int FB, int CT, bool BROWS, int MT, int NT, int U>
+template <int FA, int FB, int CT, bool BROWS, int COLS>
 __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParams p) {
-  __shared__ float lds[kRowWaves][16 * MT][16 * NT + 4];
+  constexpr int W = kRowWaves;
+  constexpr int NT = COLS / 16;
+  __shared__ float lds[W][16][16 * NT + 4];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int l = (int)blockIdx.x / p.tilesN, n0 = ((int)blockIdx.x % p.tilesN) * 16 * NT;
-  const uint8_t *a[MT], *b[NT];
-  const float *sa[MT], *sb[NT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = min(16 * t + r, p.M - 1);
-    a[t] = p.A + ((int64_t)l * p.M + m) * p.K + 16 * g;
-    sa[t] = p.SA + (int64_t)l * p.Kb * p.M + m;
-  }
+  const int l = (int)blockIdx.x / p.tilesN, n0 = ((int)blockIdx.x % p.tilesN) * COLS;
+  const int m = min(r, p.M - 1);
+  const uint8_t* a = p.A + ((int64_t)l * p.M + m) * p.K + 16 * g;
+  const float* sa = p.SA + (int64_t)l * p.Kb * p.M + m;
+  const uint8_t* b[NT];
+  const float* sb[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     b[t] = p.B + ((int64_t)l * p.N + min(n0 + 16 * t + r, p.N - 1)) * p.K + 16 * g;
     sb[t] = BROWS ? p.SB + (int64_t)l * p.Kb * p.N : p.SB + ((int64_t)l * p.Nb + min(n0 + 16 * t, p.N - 1) / 128) * p.Kb;
   }
-  const v4f zero = {0.f, 0.f, 0.f, 0.f};
-  v4f acc[MT][NT];
+  struct Block {
+    v4u a[2], b[NT][2];
+    float sa;
+    v4f sb[NT];
+  };
+  auto load = [&](Block& k, int j) {
+    // chunks g and g + 4 of the block; those past K repeat the row's last and are zeroed before use
+    const int64_t lo = (int64_t)min(128 * j, p.K - 16 - 16 * g), hi = (int64_t)min(128 * j + 64, p.K - 16 - 16 * g);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int t = 0; t < NT; ++t) {
+      k.b[t][0] = *reinterpret_cast<const v4u*>(b[t] + lo);
+      k.b[t][1] = *reinterpret_cast<const v4u*>(b[t] + hi);
+    }
+    k.a[0] = *reinterpret_cast<const v4u*>(a + lo);
+    k.a[1] = *reinterpret_cast<const v4u*>(a + hi);
+    k.sa = sa[(int64_t)j * p.M];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = zero;
-
-  for (int j0 = wave; j0 < p.Kb; j0 += kRowWaves * U) {
-    v4u ra[U][MT][2], rb[U][NT][2];
-    float va[U][MT];
-    v4f vb[U][NT];
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (BROWS) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = min(j0 + u * kRowWaves, p.Kb - 1);
-      // chunks g and g + 4 of the block; those past K repeat the row's last and are zeroed below
-      const int64_t lo = (int64_t)min(128 * j, p.K - 16 - 16 * g), hi = (int64_t)min(128 * j + 64, p.K - 16 - 16 * g);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        rb[u][t][0] = *reinterpret_cast<const v4u*>(b[t] + lo);
-        rb[u][t][1] = *reinterpret_cast<const v4u*>(b[t] + hi);
-        if constexpr (BROWS) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) vb[u][t][e] = sb[t][(int64_t)j * p.N + min(n0 + 16 * t + 4 * g + e, p.N - 1)];
-        } else {
-          vb[u][t][0] = sb[t][j];
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        ra[u][t][0] = *reinterpret_cast<const v4u*>(a[t] + lo);
-        ra[u][t][1] = *reinterpret_cast<const v4u*>(a[t] + hi);
-        va[u][t] = sa[t][(int64_t)j * p.M];
+        for (int e = 0; e < 4; ++e) k.sb[t][e] = sb[t][(int64_t)j * p.N + min(n0 + 16 * t + 4 * g + e, p.N - 1)];
+      } else {
+        k.sb[t][0] = sb[t][j];
       }
     }
+  };
+  const v4f zero = {0.f, 0.f, 0.f, 0.f};
+  v4f acc[NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * kRowWaves;
-      if (j >= p.Kb) break;
-      if (128 * j + 128 > p.K) {
-        const v4u none = {0, 0, 0, 0};
-        const bool lo_in = 128 * j + 16 * g < p.K, hi_in = 128 * j + 64 + 16 * g < p.K;
+  for (int t = 0; t < NT; ++t) acc[t] = zero;
+  auto multiply = [&](Block& k, int j) {
+    if (128 * j + 128 > p.K) {
+      const v4u none = {0, 0, 0, 0};
+      const bool lo_in = 128 * j + 16 * g < p.K, hi_in = 128 * j + 64 + 16 * g < p.K;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          rb[u][t][0] = lo_in ? rb[u][t][0] : none;
-          rb[u][t][1] = hi_in ? rb[u][t][1] : none;
-        }
+      for (int t = 0; t < NT; ++t) {
+        k.b[t][0] = lo_in ? k.b[t][0] : none;
+        k.b[t][1] = hi_in ? k.b[t][1] : none;
+      }
+      k.a[0] = lo_in ? k.a[0] : none;
+      k.a[1] = hi_in ? k.a[1] : none;
+    }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          ra[u][t][0] = lo_in ? ra[u][t][0] : none;
-          ra[u][t][1] = hi_in ? ra[u][t][1] : none;
-        }
+    for (int t = 0; t < NT; ++t) {
+      v4f part = zero;
+      if constexpr (CT != 0) {
+        struct Bytes32 { v4u lo, hi; };
+        part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(v8i, (Bytes32{k.b[t][0], k.b[t][1]})),
+                                                                __builtin_bit_cast(v8i, (Bytes32{k.a[0], k.a[1]})), zero,
+                                                                FB, FA, 0, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cvt8<FB>(k.b[t][q >> 1][2 * (q & 1)], k.b[t][q >> 1][2 * (q & 1) + 1], 1.f),
+                                                         cvt8<FA>(k.a[q >> 1][2 * (q & 1)], k.a[q >> 1][2 * (q & 1) + 1], 1.f),
+                                                         part, 0, 0, 0);
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          v4f part = zero;
-          if constexpr (CT != 0) {
-            struct Pair16 { v4u lo, hi; };
-            part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                __builtin_bit_cast(v8i, (Pair16{rb[u][n][0], rb[u][n][1]})),
-                __builtin_bit_cast(v8i, (Pair16{ra[u][m][0], ra[u][m][1]})), zero, FB, FA, 0, 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  cvt8<FB>(rb[u][n][q >> 1][2 * (q & 1)], rb[u][n][q >> 1][2 * (q & 1) + 1], 1.f),
-                  cvt8<FA>(ra[u][m][q >> 1][2 * (q & 1)], ra[u][m][q >> 1][2 * (q & 1) + 1], 1.f), part, 0, 0, 0);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[m][n][e] = __builtin_fmaf(part[e], va[u][m] * (BROWS ? vb[u][n][e] : vb[u][n][0]), acc[m][n][e]);
-        }
+      for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(part[e], k.sa * k.sb[t][BROWS ? e : 0], acc[t][e]);
+    }
+  };
+  if (wave < p.Kb) {
+    Block k0, k1;
+    load(k0, wave);
+    for (int j = wave;;) {
+      const bool more = j + W < p.Kb;
+      if (more) load(k1, j + W);
+      multiply(k0, j);
+      if (!more) break;
+      j += W;
+      const bool again = j + W < p.Kb;
+      if (again) load(k0, j + W);
+      multiply(k1, j);
+      if (!again) break;
+      j += W;
     }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) *reinterpret_cast<v4f*>(&lds[wave][16 * m + r][16 * n + 4 * g]) = acc[m][n];
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&lds[wave][r][16 * t + 4 * g]) = acc[t];
   __syncthreads();
   elem_t<CT>* c = static_cast<elem_t<CT>*>(p.C) + (int64_t)l * p.M * p.ldc + n0;
-  for (int i = threadIdx.x; i < p.M * 16 * NT; i += 64 * kRowWaves) {
-    const int m = i / (16 * NT), n = i % (16 * NT);
+  for (int i = threadIdx.x; i < p.M * COLS; i += 64 * W) {
+    const int row = i / COLS, n = i % COLS;
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) sum += lds[w][m][n];
+    for (int w = 0; w < W; ++w) sum += lds[w][row][n];
     if (n0 + n < p.N) {
-      elem_t<CT>* to = c + (int64_t)m * p.ldc + n;
+      elem_t<CT>* to = c + (int64_t)row * p.ldc + n;
       if (CT == 0 && p.accumulate) sum += (float)*to;
       *to = (elem_t<CT>)sum;
     }
+  }
+}
+
+// C from the parts' sums, four columns to a thread, parts added in order.
+template <int CT>
+__global__ __launch_bounds__(256) void block128_sum_kernel(GemmParams p, int splits) {
+  const int quads = p.ldw / 4;
+  const int64_t rows = (int64_t)p.L * p.M, all = rows * quads, stride = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
+    const int64_t row = i / quads;
+    const int n = 4 * (int)(i - row * quads);
+    const float* w = p.sums + row * p.ldw + n;
+    v4f sum = *reinterpret_cast<const v4f*>(w);
+    for (int s = 1; s < splits; ++s) sum += *reinterpret_cast<const v4f*>(w + s * rows * p.ldw);
+    elem_t<CT>* c = static_cast<elem_t<CT>*>(p.C) + row * p.ldc + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) c[e] = (elem_t<CT>)(CT == 0 && p.accumulate ? (float)c[e] + sum[e] : sum[e]);
   }
 }
 

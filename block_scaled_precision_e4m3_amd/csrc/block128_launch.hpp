@@ -8,15 +8,24 @@
 namespace mxg {
 namespace b128 {
 
-// 16-bit C (ct MXG_DT_BF16 or MXG_DT_F16) in tiles of 256 x 256, 128 x 128 or 64 x 64.
+// The tile shapes.  16-bit C: the eight waves of a 256 x 256 tile hold all registers and move the operands
+// themselves; the smaller tiles, whose steps are short, leave that to four more waves.  float32 C: the accumulators
+// and the block's sums together allow 64 x 64 outputs per wave.
+using Tile256 = TileShape<256, 256, 2, 4, 2, 1>;
+using Tile128 = TileShape<128, 128, 2, 2, 2, 2, 4>;
+using Tile64 = TileShape<64, 64, 2, 2, 4, 2, 4>;
+using Exact256 = TileShape<256, 128, 4, 2, 2, 1>;
+using Exact128 = Tile128;
+using Exact64 = Tile64;
+
 hipError_t launch_tile256(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile64(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
-// float32 C in tiles of 256 x 128 or 128 x 128.
 hipError_t launch_exact256(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 hipError_t launch_exact128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
-// up to 64 rows; p.tilesN counts groups of 16 * nt columns, mt rows of 16
-hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int mt, int nt, int64_t grid, hipStream_t s);
+hipError_t launch_exact64(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
+// up to 16 rows; p.tilesN counts groups of `cols` (16 or 32) columns
+hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int cols, int64_t grid, hipStream_t s);
 
 // f<FA, FB>(...) for the formats of A and B.
 template <class F>
@@ -28,7 +37,7 @@ hipError_t by_format(int fa, int fb, F f) {
 
 template <class T>
 hipError_t launch_tile(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s) {
-  const dim3 g((unsigned)grid), b(64 * T::kWaves);
+  const dim3 g((unsigned)grid), b(64 * T::kAllWaves);
   return by_format(fa, fb, [&](auto a, auto c) {
     constexpr int FA = decltype(a)::value, FB = decltype(c)::value;
     if (ct == 1) {
@@ -44,7 +53,7 @@ hipError_t launch_tile(const GemmParams& p, int fa, int fb, int ct, int64_t grid
 
 template <class T>
 hipError_t launch_exact(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s) {
-  const dim3 g((unsigned)grid), b(64 * T::kWaves);
+  const dim3 g((unsigned)grid), b(64 * T::kAllWaves);
   return by_format(fa, fb, [&](auto a, auto c) {
     constexpr int FA = decltype(a)::value, FB = decltype(c)::value;
     if (p.b_rows) hipLaunchKernelGGL((block128_exact_kernel<T, FA, FB, true>), g, b, 0, s, p);

@@ -5,7 +5,7 @@ namespace mxg {
 namespace b128 {
 
 hipError_t launch_tile128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s) {
-  return launch_tile<TileShape<128, 128, 2, 2, 2>>(p, fa, fb, ct, grid, s);
+  return launch_tile<Tile128>(p, fa, fb, ct, grid, s);
 }
 
 }  // namespace b128

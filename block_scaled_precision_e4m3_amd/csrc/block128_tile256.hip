@@ -5,7 +5,7 @@ namespace mxg {
 namespace b128 {
 
 hipError_t launch_tile256(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s) {
-  return launch_tile<TileShape<256, 256, 2, 4, 2>>(p, fa, fb, ct, grid, s);
+  return launch_tile<Tile256>(p, fa, fb, ct, grid, s);
 }
 
 }  // namespace b128

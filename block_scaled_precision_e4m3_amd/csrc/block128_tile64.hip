@@ -5,7 +5,7 @@ namespace mxg {
 namespace b128 {
 
 hipError_t launch_tile64(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s) {
-  return launch_tile<TileShape<64, 64, 2, 2, 4>>(p, fa, fb, ct, grid, s);
+  return launch_tile<Tile64>(p, fa, fb, ct, grid, s);
 }
 
 }  // namespace b128

@@ -185,6 +185,37 @@ def test_gemm_types(lib, m, n, k):
             check_gemm(lib, m, n, k, 0, 0, b_block, dtype, seed=m + n + k)
 
 
+# one or more work items per compute unit of every tile size, ragged in both directions, K divided or not, an odd
+# number of blocks, and rows that do or do not allow 16-byte stores
+LARGE = [(1030, 16400, 144), (1290, 9001, 272), (2050, 2056, 400), (700, 4104, 912), (65, 1000, 7168), (40, 130, 4112),
+         (300, 2050, 2064), (20, 24577, 128), (17, 64, 16), (4097, 264, 656)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_gemm_tiles_and_parts(lib, m, n, k):
+    print(f"gemm {m}x{n}x{k}", flush=True)
+    for dtype in DT.values():
+        check_gemm(lib, m, n, k, 1, 0, 128, dtype, seed=m + n)
+        check_gemm(lib, m, n, k, 0, 0, 1, dtype, seed=k)
+    c0 = np.random.default_rng(1).standard_normal((m, n)).astype(np.float32).astype(np.float64)
+    check_gemm(lib, m, n, k, 0, 1, 1, torch.float32, c0=c0, seed=4)
+
+
+def test_gemm_workspace(lib):
+    """K is divided for few tiles and a long K; a short or missing workspace is refused."""
+    need = lib._lib.mxgemm_block128_workspace_bytes(64, 512, 7168, 1, lib.MXG_DT_BF16)
+    assert need > 0 and need % (64 * 512 * 4) == 0
+    assert lib._lib.mxgemm_block128_workspace_bytes(8192, 8192, 7168, 1, lib.MXG_DT_BF16) == 0
+    ops = upload(*operands(64, 512, 7168, 0, 0, 128, 3), 0, 0)
+    ws = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    with pytest.raises(lib.MxgemmValueError):
+        lib.block128_gemm(*ops, workspace=ws[:need - 16])
+    c = lib.block128_gemm(*ops, workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert torch.all(ws[need:] == 0xA5).item()
+    assert torch.equal(c, lib.block128_gemm(*ops))
+
+
 @pytest.mark.parametrize("fa,fb", [(0, 1), (1, 0), (1, 1)])
 @pytest.mark.parametrize("m,n,k", [(3, 200, 272), (70, 136, 400), (300, 260, 528), (600, 900, 256)])
 def test_gemm_formats_and_heavy_tails(lib, m, n, k, fa, fb):
