@@ -41,6 +41,7 @@ constexpr unsigned kOob = 0x80000000u;  // an offset past every resource: reads 
 template <int BM, int BN, int WM, int WN, int NST, int KB, int NP = 0>
 struct TileShape {
   static constexpr int kBM = BM, kBN = BN, kWaves = WM * WN, kWn = WN, kStages = NST, kKB = KB;
+  static constexpr bool kParts = NP > 0;                 // K may be divided (the host's rule)
   static constexpr int kProducers = NP, kDmaWaves = NP ? NP : kWaves, kAllWaves = kWaves + NP;
   static constexpr int kTM = BM / WM, kTN = BN / WN;     // a wave's outputs
   static constexpr int kOffB = BM * 128, kOffSA = kOffB + BN * 128, kOffSB = kOffSA + BM * 4;
@@ -72,15 +73,18 @@ struct TileAt {
 struct Part {
   int at, count;  // first step and number of steps
 };
+template <class T>
 __device__ __forceinline__ Part part_of(const GemmParams& p, int item) {
-  if (p.splits == 1) return {0, p.steps};
+  if (!T::kParts || p.splits == 1) return {0, p.steps};
   const int at = __builtin_amdgcn_readfirstlane(item / p.num_tiles * p.per);
   return {at, min(p.per, p.steps - at)};
 }
 // Tile t: batches, then groups of kGroupM tile rows walked column by column.  A work item is a tile and a part of
 // its K; items of one part follow each other.
-__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t, int bm, int bn) {
-  if (p.splits > 1) t %= p.num_tiles;
+template <class T>
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
+  constexpr int bm = T::kBM, bn = T::kBN;
+  if (T::kParts && p.splits > 1) t %= p.num_tiles;
   const int per = p.tilesM * p.tilesN, l = t / per, r = t - l * per;
   const int group = kGroupM * p.tilesN, g = r / group, first = g * kGroupM;
   const int rows = min(p.tilesM - first, kGroupM), rg = r - g * group;
@@ -111,7 +115,7 @@ struct Stream {
   unsigned base, va[T::kKB], vb[T::kKB];  // of the step being fetched
 
   __device__ __forceinline__ Stream(const GemmParams& p_, const uint8_t* lds, int lane, int wave_, int first)
-      : p(p_), wave(wave_), G((int)gridDim.x), items(p_.num_tiles * p_.splits), item(first) {
+      : p(p_), wave(wave_), G((int)gridDim.x), items(T::kParts ? p_.num_tiles * p_.splits : p_.num_tiles), item(first) {
     lds0 = lds_addr(lds);
     const int row = 8 * wave + (lane >> 3);
     chunk_a = (unsigned)((lane & 7) ^ SwA(row)) * 16;
@@ -131,10 +135,10 @@ struct Stream {
     int at = 0;
     left = 0x7FFFFFFF;
     if (item < items) {
-      f = tile_at(p, item, T::kBM, T::kBN);
+      f = tile_at<T>(p, item);
       mv = (unsigned)min(p.M - f.m0, T::kBM);
       nv = (unsigned)min(p.N - f.n0, T::kBN);
-      const Part part = part_of(p, item);
+      const Part part = part_of<T>(p, item);
       at = T::kKB * part.at;
       left = part.count;
     }
@@ -213,7 +217,7 @@ __device__ __forceinline__ void produce(const GemmParams& p, S& in, int item, in
   for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
   int stage = 0;
   for (; item < items; item += (int)gridDim.x)
-    for (int n = part_of(p, item).count; n > 0; --n) {
+    for (int n = part_of<T>(p, item).count; n > 0; --n) {
       wait_vm<(T::kStages - 2) * T::kIssued>();
       barrier();
       in.all(stage == 0 ? T::kStages - 1 : stage - 1);
@@ -258,7 +262,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
   const int r = lane & 15, g = lane >> 4;
   const int G = (int)gridDim.x;
   int item = first_tile_of(p);
-  const int items = p.num_tiles * p.splits;
+  const int items = T::kParts ? p.num_tiles * p.splits : p.num_tiles;
   Stream<T, BROWS, swizzle_a16, swizzle_b16> in(p, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
   if constexpr (T::kProducers > 0) {
     if (wave >= T::kWaves) {
@@ -278,12 +282,12 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 
   if constexpr (T::kProducers == 0)
     for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
-  int step = 0, stage = 0, count = item < items ? part_of(p, item).count : 0;
+  int step = 0, stage = 0, count = item < items ? part_of<T>(p, item).count : 0;
   bool stored = false;
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
   v4f acc[kMt][kNt];
   while (item < items) {
-    if constexpr (T::kProducers == 0) wait_step<T, kStores>(p.c_vec && p.splits == 1, stored && step < T::kStages - 1);
+    if constexpr (T::kProducers == 0) wait_step<T, kStores>(p.c_vec, stored && step < T::kStages - 1);
     barrier();
     const uint8_t* st = lds + stage * T::kStage;
     const uint8_t *a_lo = st + a_off, *a_hi = st + (a_off ^ 64), *b_lo = st + b_off, *b_hi = st + (b_off ^ 64);
@@ -355,9 +359,9 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
     if (++step == count) {
       step = 0;
       stored = true;
-      const TileAt at = tile_at(p, item, T::kBM, T::kBN);
+      const TileAt at = tile_at<T>(p, item);
       const int rows = min(p.M - at.m0, T::kBM);
-      if (p.splits > 1) {
+      if (T::kParts && p.splits > 1) {
         // a part's sums, four columns at a time (ldw is a multiple of 4)
         float* w = p.sums + (((int64_t)(item / p.num_tiles) * p.L + at.l) * p.M + at.m0) * p.ldw + at.n0;
 #pragma unroll
@@ -368,11 +372,11 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
             if (m < rows && at.n0 + n < p.ldw) *reinterpret_cast<v4f*>(w + (int64_t)m * p.ldw + n) = acc[mt][nt];
           }
         item += G;
-        count = item < items ? part_of(p, item).count : 0;
+        count = item < items ? part_of<T>(p, item).count : 0;
         continue;
       }
       item += G;
-      count = item < items ? part_of(p, item).count : 0;
+      count = item < items ? part_of<T>(p, item).count : 0;
       using E = elem_t<CT>;
       E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
       if (p.c_vec) {
@@ -461,7 +465,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
   const int r = lane & 31, h = lane >> 5;
   const int G = (int)gridDim.x;
   int item = first_tile_of(p);
-  const int items = p.num_tiles * p.splits;
+  const int items = T::kParts ? p.num_tiles * p.splits : p.num_tiles;
   Stream<T, BROWS, swizzle_a32, swizzle_b32> in(p, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
   if constexpr (T::kProducers > 0) {
     if (wave >= T::kWaves) {
@@ -477,7 +481,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
   const unsigned a_off = (unsigned)(a_row * 128 + 16 * (h ^ swizzle_a32(a_row)));
   const unsigned b_off = (unsigned)(T::kOffB + b_row * 128 + 16 * (h ^ swizzle_b32(b_row)));
 
-  int step = 0, stage = 0, count = item < items ? part_of(p, item).count : 0;
+  int step = 0, stage = 0, count = item < items ? part_of<T>(p, item).count : 0;
   bool stored = false;
   v16f acc[kMt][kNt];
   while (item < items) {
@@ -556,11 +560,11 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
     if (++step == count) {
       step = 0;
       stored = true;
-      const TileAt at = tile_at(p, item, T::kBM, T::kBN);
+      const TileAt at = tile_at<T>(p, item);
       // a part's sums go to the workspace, which the host has described as C: (splits, L, M, ldc)
-      const int l = at.l + (p.splits > 1 ? item / p.num_tiles * p.L : 0);
+      const int l = at.l + (T::kParts && p.splits > 1 ? item / p.num_tiles * p.L : 0);
       item += G;
-      count = item < items ? part_of(p, item).count : 0;
+      count = item < items ? part_of<T>(p, item).count : 0;
       const int rows = min(p.M - at.m0, T::kBM);
       float* c = static_cast<float*>(p.C) + ((int64_t)l * p.M + at.m0) * p.ldc + at.n0;
       if (p.c_vec) {
