@@ -52,16 +52,69 @@ void launch_rows(const Params& p, int dtype, int64_t grid, hipStream_t s) {
   else hipLaunchKernelGGL((mxg::heads::rows_kernel<2, MODE>), g, b, 0, s, p);
 }
 
-// Workgroups of the backward pass: a row of its workspace each.
-int64_t backward_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(T, mxg::heads::kMaxParts)); }
+// Workgroups of the backward pass, each with a row of its workspace.
+int64_t backward_parts(int64_t T) {
+  return std::max<int64_t>(1, std::min<int64_t>(cdiv(T, mxg::heads::kWaves), mxg::heads::kMaxParts));
+}
 
+// Whether every access of the vector kernels is a whole 16-byte one: 8-feature chunks of the head, of its rotary part
+// and of what lies before it, at aligned addresses.
+bool whole_chunks(const Params& p, int dtype, const Tensor* tensors[], int count) {
+  const int e = mxg::elem_bytes(dtype);
+  if (p.D % 16 != 0 || p.rot % 16 != 0 || p.off % 8 != 0) return false;
+  for (int i = 0; i < count; ++i) {
+    const Tensor& x = *tensors[i];
+    if (!aligned16(x.p) || x.ts * e % 16 != 0 || x.hs * e % 16 != 0) return false;
+  }
+  return aligned16(p.cos) && aligned16(p.sin) && aligned16(p.w[0]) && aligned16(p.w[1]);
+}
+
+template <int DT, int MODE, bool IN, bool OUT>
+void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
+  const dim3 g((unsigned)grid), b(mxg::heads::kThreads);
+  if constexpr (MODE == mxg::heads::kBackward) hipLaunchKernelGGL((mxg::heads::heads_backward_kernel<DT, IN, OUT>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((mxg::heads::heads_kernel<DT, MODE, IN, OUT>), g, b, 0, s, p);
+}
+
+template <int DT, int MODE>
+void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
+  if (p.halves_in && p.halves_out) launch_heads<DT, MODE, true, true>(p, grid, s);
+  else if (p.halves_out) launch_heads<DT, MODE, false, true>(p, grid, s);
+  else if (!p.halves_in) launch_heads<DT, MODE, false, false>(p, grid, s);
+  else if constexpr (MODE == mxg::heads::kRope) launch_heads<DT, MODE, true, false>(p, grid, s);  // a transposed map only
+}
+
+// Launches the pass; returns its workgroups.
 template <int MODE>
 int launch(Params& p, int dtype, int cus, hipStream_t s) {
-  const int64_t rows = p.T * (p.H[0] + p.H[1]);
-  int64_t grid = cdiv(rows, mxg::heads::kWaves);
-  if (MODE == mxg::heads::kBackward) grid = std::min(grid, backward_parts(p.T));
-  grid = std::min<int64_t>(grid, 64LL * cus);
-  launch_rows<MODE>(p, dtype, grid, s);
+  const Tensor* tensors[6];
+  int count = 0;
+  for (int k = 0; k < 2; ++k)
+    if (p.H[k] > 0) {
+      tensors[count++] = &p.x[k];
+      tensors[count++] = &p.y[k];
+      if (MODE == mxg::heads::kBackward) tensors[count++] = &p.g[k];
+    }
+  int64_t grid;
+  if (whole_chunks(p, dtype, tensors, count)) {
+    p.lpr = 1;
+    while (16 * p.lpr < p.D) p.lpr *= 2;
+    p.rpw = 64 / p.lpr;
+    for (int k = 0; k < 2; ++k) p.groups[k] = (int)cdiv(p.H[k], p.rpw);
+    const int64_t groups = p.groups[0] + p.groups[1];
+    // up to 8 groups of heads to a wave share the token's angles; fewer while that leaves less than 16 waves per
+    // compute unit
+    p.gpw = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 8, p.T * groups / (16LL * cus)}));
+    grid = MODE == mxg::heads::kBackward ? backward_parts(p.T) : cdiv(p.T * cdiv(groups, p.gpw), mxg::heads::kWaves);
+    if (dtype == MXG_DT_F32) launch_heads<0, MODE>(p, grid, s);
+    else if (dtype == MXG_DT_BF16) launch_heads<1, MODE>(p, grid, s);
+    else launch_heads<2, MODE>(p, grid, s);
+  } else {
+    const int64_t rows = p.T * (p.H[0] + p.H[1]);
+    grid = std::min<int64_t>(cdiv(rows, mxg::heads::kWaves), 64LL * cus);
+    if (MODE == mxg::heads::kBackward) grid = std::min(grid, backward_parts(p.T));
+    launch_rows<MODE>(p, dtype, grid, s);
+  }
   return (int)grid;
 }
 

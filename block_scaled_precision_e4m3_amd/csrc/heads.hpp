@@ -191,6 +191,289 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(Params p) {
   }
 }
 
+// --- 16-byte accesses ------------------------------------------------------------
+//
+// A head is D / 8 chunks of 8 features; a lane owns two of them, so that it has
+// both members of its 8 pairs and no lane needs another's features: the chunks
+// at off + 8p and off + rot/2 + 8p where the pairs lie in halves, 16
+// consecutive features from off + 16p where they are interleaved (the first
+// members are then the even ones), and any two of the remaining chunks for
+// features that are only copied or normed.  D / 16 lanes, rounded up to a power
+// of two (lpr), share a head; a wave works on 64 / lpr heads of one token at a
+// time, and keeps that token's cos and sin (and the weights) in registers over
+// the heads it does.  The bound is memory: every feature is read once and
+// written once, cos and sin once per wave and token.
+
+// A lane's share of a head, as feature offsets: first and second chunk as read and as written.
+struct Lane {
+  int in0, in1, out0, out1;
+  bool rot;          // its pairs turn
+  int pair;          // index of its first pair
+};
+__device__ __forceinline__ Lane lane_of(const Params& p, int q, bool halves_in, bool halves_out) {
+  Lane l;
+  const int half = p.rot >> 1;
+  l.rot = q < (p.rot >> 4);
+  l.pair = 8 * q;
+  if (l.rot) {
+    l.in0 = p.off + (halves_in ? 8 * q : 16 * q);
+    l.in1 = l.in0 + (halves_in ? half : 8);
+    l.out0 = p.off + (halves_out ? 8 * q : 16 * q);
+    l.out1 = l.out0 + (halves_out ? half : 8);
+  } else {
+    // the chunks outside the rotary part, two at a time
+    const int c = 16 * (q - (p.rot >> 4));
+    l.in0 = l.out0 = c < p.off ? c : c + p.rot;
+    l.in1 = l.out1 = c + 8 < p.off ? c + 8 : c + 8 + p.rot;
+  }
+  return l;
+}
+
+struct Two {
+  v8f a, b;
+};
+// Two chunks as first and second members of 8 pairs, and back.
+template <bool HALVES>
+__device__ __forceinline__ Two split(const v8f& x, const v8f& y) {
+  if constexpr (HALVES) return {x, y};
+  return {__builtin_shufflevector(x, y, 0, 2, 4, 6, 8, 10, 12, 14), __builtin_shufflevector(x, y, 1, 3, 5, 7, 9, 11, 13, 15)};
+}
+template <bool HALVES>
+__device__ __forceinline__ Two join(const Two& t) {
+  if constexpr (HALVES) return t;
+  return {__builtin_shufflevector(t.a, t.b, 0, 8, 1, 9, 2, 10, 3, 11), __builtin_shufflevector(t.a, t.b, 4, 12, 5, 13, 6, 14, 7, 15)};
+}
+// The rotation between layouts; a lane whose pairs do not turn has its chunks back in the order they came.
+template <bool IN, bool OUT>
+__device__ __forceinline__ Two turn(const Two& t, const v8f& c, const v8f& s, bool rot) {
+  Two r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = t.a[i] * c[i] - t.b[i] * s[i], b = t.b[i] * c[i] + t.a[i] * s[i];
+    r.a[i] = rot ? a : t.a[i];
+    r.b[i] = rot ? b : t.b[i];
+  }
+  if constexpr (IN == OUT) return join<OUT>(r);
+  const Two x = join<OUT>(r), y = join<IN>(r);
+  Two z;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    z.a[i] = rot ? x.a[i] : y.a[i];
+    z.b[i] = rot ? x.b[i] : y.b[i];
+  }
+  return z;
+}
+
+struct Angles {
+  v8f c, s;
+};
+__device__ __forceinline__ Angles angles_of(const Params& p, int64_t t, const Lane& l, float sign) {
+  Angles a;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a.c[i] = a.s[i] = 0.f;
+  if (l.rot) {
+    const int64_t row = table_row(p, t);
+    if (row >= 0) {
+      const int64_t at = row * (p.rot >> 1) + l.pair;
+      a.c = widen8<0>(load8<0>(p.cos + at));
+      a.s = widen8<0>(load8<0>(p.sin + at)) * sign;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a.c[i] = a.s[i] = __builtin_nanf("");
+    }
+  }
+  return a;
+}
+
+// Sum over the lanes of a head, the same bits in each: pairs, quads, then the mirrored half and row (whose quads hold
+// equal sums) through the lane crossbar of the VALU, wider exchanges through LDS.
+template <int CTRL>
+__device__ __forceinline__ float add_across(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float head_sum(float v, int lpr) {
+  if (lpr > 1) v = add_across<0xB1>(v);    // quad_perm 1 0 3 2
+  if (lpr > 2) v = add_across<0x4E>(v);    // quad_perm 2 3 0 1
+  if (lpr > 4) v = add_across<0x141>(v);   // row_half_mirror
+  if (lpr > 8) v = add_across<0x140>(v);   // row_mirror
+  if (lpr > 16) v += __shfl_xor(v, 16);
+  if (lpr > 32) v += __shfl_xor(v, 32);
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ v8f weights8(const Params& p, int which, int i) {
+  if (p.w_f32) return widen8<0>(load8<0>(static_cast<const float*>(p.w[which]) + i));
+  return widen8<DT>(load8<DT>(static_cast<const elem_t<DT>*>(p.w[which]) + i));
+}
+
+// IN, OUT: the pairs lie in halves on the way in, and on the way out.
+template <int DT, int MODE, bool IN, bool OUT>
+__global__ __launch_bounds__(kThreads) void heads_kernel(Params p) {
+  using E = elem_t<DT>;
+  constexpr int U = 4;  // groups of heads whose loads are in flight together
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int all = p.groups[0] + p.groups[1], parts = (all + p.gpw - 1) / p.gpw;
+  const int64_t item = (int64_t)blockIdx.x * kWaves + wave;
+  const int64_t t = item / parts;
+  if (t >= p.T) return;
+  const int first = (int)(item - t * parts) * p.gpw, last = min(first + p.gpw, all);
+  const int q = lane & (p.lpr - 1), sub = lane / p.lpr;
+  const bool mine = 16 * q < p.D;
+  const Lane l = lane_of(p, q, IN, OUT);
+  const Angles ang = angles_of(p, t, l, p.sign);
+  Two w[2];
+  if constexpr (MODE == kNorm) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (mine && p.groups[k] > 0) w[k] = split<IN>(weights8<DT>(p, k, l.in0), weights8<DT>(p, k, l.in1));
+  }
+  for (int g0 = first; g0 < last; g0 += U) {
+    Raw8<DT> x[U][2];
+    bool live[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = g0 + u, k = g < p.groups[0] ? 0 : 1;
+      const int h = (k ? g - p.groups[0] : g) * p.rpw + sub;
+      live[u] = mine && g < last && h < p.H[k];
+      if (live[u]) {
+        const E* at = static_cast<const E*>(p.x[k].p) + t * p.x[k].ts + h * p.x[k].hs;
+        x[u][0] = load8<DT>(at + l.in0);
+        x[u][1] = load8<DT>(at + l.in1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (g0 + u >= last) break;
+      const int g = g0 + u, k = g < p.groups[0] ? 0 : 1;
+      const int h = (k ? g - p.groups[0] : g) * p.rpw + sub;
+      Two v = split<IN>(widen8<DT>(x[u][0]), widen8<DT>(x[u][1]));
+      if constexpr (MODE == kNorm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += v.a[i] * v.a[i] + v.b[i] * v.b[i];
+        ss = head_sum(live[u] ? ss : 0.f, p.lpr);
+        const float r = 1.f / sqrtf(ss * p.inv_d + p.eps);
+        v.a = v.a * r * (k ? w[1].a : w[0].a);
+        v.b = v.b * r * (k ? w[1].b : w[0].b);
+      }
+      const Two y = turn<IN, OUT>(v, ang.c, ang.s, l.rot);
+      if (live[u]) {
+        E* at = static_cast<E*>(p.y[k].p) + t * p.y[k].ts + h * p.y[k].hs;
+        store8<DT>(at + l.out0, y.a);
+        store8<DT>(at + l.out1, y.b);
+      }
+    }
+  }
+}
+
+// Backward: a wave takes every (workgroups x kWaves)-th token with all its heads, queries then keys, and keeps the
+// weight gradients of its lanes' features in registers to the end.
+template <int DT, bool IN, bool OUT>
+__global__ __launch_bounds__(kThreads) void heads_backward_kernel(Params p) {
+  using E = elem_t<DT>;
+  constexpr int U = 2;
+  __shared__ float lds[kWaves][2][kMaxD];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int q = lane & (p.lpr - 1), sub = lane / p.lpr;
+  const bool mine = 16 * q < p.D;
+  const Lane l = lane_of(p, q, IN, OUT);
+  Two w[2], dw[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k].a[i] = dw[k].b[i] = w[k].a[i] = w[k].b[i] = 0.f;
+    if (mine && p.groups[k] > 0) w[k] = split<IN>(weights8<DT>(p, k, l.in0), weights8<DT>(p, k, l.in1));
+  }
+  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < p.T; t += (int64_t)gridDim.x * kWaves) {
+    const Angles ang = angles_of(p, t, l, -1.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      for (int g0 = 0; g0 < p.groups[k]; g0 += U) {
+        Raw8<DT> x[U][2], g[U][2];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int h = (g0 + u) * p.rpw + sub;
+          live[u] = mine && h < p.H[k];
+          if (live[u]) {
+            const E* xa = static_cast<const E*>(p.x[k].p) + t * p.x[k].ts + h * p.x[k].hs;
+            const E* ga = static_cast<const E*>(p.g[k].p) + t * p.g[k].ts + h * p.g[k].hs;
+            x[u][0] = load8<DT>(xa + l.in0);
+            x[u][1] = load8<DT>(xa + l.in1);
+            g[u][0] = load8<DT>(ga + l.out0);
+            g[u][1] = load8<DT>(ga + l.out1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (g0 + u >= p.groups[k]) break;
+          const Two v = split<IN>(widen8<DT>(x[u][0]), widen8<DT>(x[u][1]));
+          // the transposed rotation: from where y's pairs lie to where x's lie, as chunks and then as pairs again
+          Two d = turn<OUT, IN>(split<OUT>(widen8<DT>(g[u][0]), widen8<DT>(g[u][1])), ang.c, ang.s, l.rot);
+          d = split<IN>(d.a, d.b);
+          float ss = 0.f, dot = 0.f;
+          Two dn;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss += v.a[i] * v.a[i] + v.b[i] * v.b[i];
+          dn.a = d.a * w[k].a;
+          dn.b = d.b * w[k].b;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot += dn.a[i] * v.a[i] + dn.b[i] * v.b[i];
+          ss = head_sum(live[u] ? ss : 0.f, p.lpr);
+          dot = head_sum(live[u] ? dot : 0.f, p.lpr);
+          const float r = 1.f / sqrtf(ss * p.inv_d + p.eps);
+          const Two n = {v.a * r, v.b * r};
+          const float m = dot * r * p.inv_d;
+          Two dx;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dx.a[i] = r * (dn.a[i] - n.a[i] * m);
+            dx.b[i] = r * (dn.b[i] - n.b[i] * m);
+          }
+          if (live[u]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              dw[k].a[i] += d.a[i] * n.a[i];
+              dw[k].b[i] += d.b[i] * n.b[i];
+            }
+            const Two out = join<IN>(dx);
+            const int h = (g0 + u) * p.rpw + sub;
+            E* at = static_cast<E*>(p.y[k].p) + t * p.y[k].ts + h * p.y[k].hs;
+            store8<DT>(at + l.in0, out.a);
+            store8<DT>(at + l.in1, out.b);
+          }
+        }
+      }
+    }
+  }
+  // the workgroup's sums: lanes that own the same features, then waves, in order
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a = dw[k].a[i], b = dw[k].b[i];
+      for (int s = p.lpr; s < 64; s <<= 1) {
+        a += __shfl_xor(a, s);
+        b += __shfl_xor(b, s);
+      }
+      if (mine && sub == 0) {
+        lds[wave][k][IN ? l.in0 + i : (i < 4 ? l.in0 + 2 * i : l.in1 + 2 * (i - 4))] = a;
+        lds[wave][k][IN ? l.in1 + i : (i < 4 ? l.in0 + 2 * i + 1 : l.in1 + 2 * (i - 4) + 1)] = b;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
+    const int k = i >= p.D ? 1 : 0, f = i - k * p.D;
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) sum += lds[v][k][f];
+    p.parts[((int64_t)blockIdx.x * 2 + k) * p.D + f] = sum;
+  }
+}
+
 // dW: the sums of `parts` workgroups, 16 columns and 16 groups of rows to a
 // workgroup, added in a fixed order.
 __global__ __launch_bounds__(256) void weight_sum_kernel(const float* parts, float* dwq, float* dwk, int count, int D) {
