@@ -51,12 +51,17 @@ void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, in
 }
 
 template <int DT>
-void launch_quantize(const QuantParams& p, int fmt, bool vec, bool rows, bool cols, bool square, int64_t grid, hipStream_t s) {
+void launch_quantize(const QuantParams& p, int fmt, bool vec, bool few, bool rows, bool cols, bool square, int64_t grid,
+                     hipStream_t s) {
   if (fmt == MXG_FMT_E4M3) {
-    if (vec) launch_quantize<DT, 0, 8, true>(p, rows, cols, square, grid, s);
+    if (few && vec) launch_quantize<DT, 0, 1, true>(p, rows, cols, square, grid, s);
+    else if (few) launch_quantize<DT, 0, 1, false>(p, rows, cols, square, grid, s);
+    else if (vec) launch_quantize<DT, 0, 8, true>(p, rows, cols, square, grid, s);
     else launch_quantize<DT, 0, 8, false>(p, rows, cols, square, grid, s);
   } else {
-    if (vec) launch_quantize<DT, 1, 8, true>(p, rows, cols, square, grid, s);
+    if (few && vec) launch_quantize<DT, 1, 1, true>(p, rows, cols, square, grid, s);
+    else if (few) launch_quantize<DT, 1, 1, false>(p, rows, cols, square, grid, s);
+    else if (vec) launch_quantize<DT, 1, 8, true>(p, rows, cols, square, grid, s);
     else launch_quantize<DT, 1, 8, false>(p, rows, cols, square, grid, s);
   }
 }
@@ -167,12 +172,14 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
   p.pow2 = (flags & MXG_QUANT_POW2) != 0;
   // whole 8-element chunks at 16-byte addresses
   const bool vec = aligned16(X) && K % 8 == 0 && ldx % 8 == 0;
-  p.tiles_m = p.Mb;
+  // rows alone, and too few of them for 128-row tiles to fill the chip: 16 rows to a workgroup
+  const bool few = rows && !cols && !square && L * p.Mb * p.Kb < 4LL * cus;
+  p.tiles_m = few ? (int)cdiv(M, 16) : p.Mb;
   const int64_t grid = L * p.tiles_m * p.Kb;
   hipStream_t s = (hipStream_t)stream;
-  if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, vec, rows, cols, square, grid, s);
-  else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, vec, rows, cols, square, grid, s);
-  else launch_quantize<2>(p, fmt, vec, rows, cols, square, grid, s);
+  if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, vec, few, rows, cols, square, grid, s);
+  else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, vec, few, rows, cols, square, grid, s);
+  else launch_quantize<2>(p, fmt, vec, few, rows, cols, square, grid, s);
   return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 

@@ -54,7 +54,7 @@ void launch_rows(const Params& p, int dtype, int64_t grid, hipStream_t s) {
 
 // Workgroups of the backward pass, each with a row of its workspace.
 int64_t backward_parts(int64_t T) {
-  return std::max<int64_t>(1, std::min<int64_t>(cdiv(T, mxg::heads::kWaves), mxg::heads::kMaxParts));
+  return std::max<int64_t>(2, std::min<int64_t>(cdiv(T, mxg::heads::kWaves), mxg::heads::kMaxParts));
 }
 
 // Whether every access of the vector kernels is a whole 16-byte one: 8-feature chunks of the head, of its rotary part
@@ -102,9 +102,16 @@ int launch(Params& p, int dtype, int cus, hipStream_t s) {
     p.rpw = 64 / p.lpr;
     for (int k = 0; k < 2; ++k) p.groups[k] = (int)cdiv(p.H[k], p.rpw);
     const int64_t groups = p.groups[0] + p.groups[1];
-    // up to 8 groups of heads to a wave share the token's angles; fewer while that leaves less than 16 waves per
-    // compute unit
-    p.gpw = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 8, p.T * groups / (16LL * cus)}));
+    // Groups of heads to a wave, which share the token's angles and weights: 2 (rope, 8192 tokens of 128 heads of 192:
+    // 1 174 us, 2 146 us, 8 159 us) or 8 (norm, 8192 tokens of 32 + 8 heads of 128: 1 56 us, 2 50 us, 5 and 8 41 us);
+    // fewer while that leaves less than 16 waves per compute unit.
+    p.gpw = (int)std::max<int64_t>(1, std::min<int64_t>({groups, MODE == mxg::heads::kRope ? 2 : 8, p.T * groups / (16LL * cus)}));
+    if (MODE == mxg::heads::kBackward) {
+      // workgroups in proportion to the groups of queries and keys, at least one of each that there is
+      const int64_t parts = backward_parts(p.T);
+      const int64_t q = p.groups[1] == 0 ? parts : std::min(parts - 1, std::max<int64_t>(1, cdiv(parts * p.groups[0], groups)));
+      p.parts_q = p.groups[0] == 0 ? 0 : (int)q;
+    }
     grid = MODE == mxg::heads::kBackward ? backward_parts(p.T) : cdiv(p.T * cdiv(groups, p.gpw), mxg::heads::kWaves);
     if (dtype == MXG_DT_F32) launch_heads<0, MODE>(p, grid, s);
     else if (dtype == MXG_DT_BF16) launch_heads<1, MODE>(p, grid, s);
@@ -281,8 +288,13 @@ int mxgemm_qk_norm_rope_backward(const void* GQ, const void* GK, const void* Q, 
     parts = launch<mxg::heads::kBackward>(p, dtype, cus, (hipStream_t)stream);
     if (hipGetLastError() != hipSuccess) return MXG_ERR_LAUNCH;
   }
-  hipLaunchKernelGGL(mxg::heads::weight_sum_kernel, dim3((unsigned)cdiv(2 * D, 16)), dim3(256), 0, (hipStream_t)stream,
-                     p.parts, DWQ, DWK, parts, (int)D);
+  // the wave-per-row kernel leaves queries' and keys' sums side by side, the vector kernel in rows of their own
+  const bool rows = p.lpr == 0;
+  const int64_t row = rows ? 2 * D : D;
+  const int parts_q = rows ? parts : p.parts_q, parts_k = rows ? parts : parts - p.parts_q;
+  const float* sums_k = rows ? p.parts + D : p.parts + p.parts_q * row;
+  hipLaunchKernelGGL(mxg::heads::weight_sum_kernel, dim3((unsigned)cdiv(D, 16), DWK ? 2 : 1), dim3(1024), 0,
+                     (hipStream_t)stream, p.parts, parts_q, sums_k, parts_k, row, DWQ, DWK, (int)D);
   return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 

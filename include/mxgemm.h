@@ -460,10 +460,11 @@ enum {
  * 128, the operands of mxgemm_block128.  For every block with largest
  * magnitude a (taken as 448 * 2^-100 if it is smaller):
  *
- *   scale = a / FMAX,  code = rne(x * (FMAX / a))         FMAX 448 or 57344
+ *   scale = a / FMAX,  code = rne(x FMAX / a)             FMAX 448 or 57344
  *
- * with both quotients rounded to float32, or, with MXG_QUANT_POW2, scale = 2^e
- * with e the smallest integer giving FMAX * 2^e >= a and code = rne(x * 2^-e).
+ * with both quotients rounded to float32 (the second before it is rounded to a
+ * code), or, with MXG_QUANT_POW2, scale = 2^e with e the smallest integer giving
+ * FMAX * 2^e >= a and code = rne(x * 2^-e).
  *
  *   X  : (L, M, K) of x_dtype, K contiguous, rows ldx >= K elements apart,
  *        batches M * ldx apart.

@@ -2,9 +2,9 @@
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
 
-``quantize`` follows the rule in numpy float32 (IEEE quotients and products, so the GPU must give the same bits): for
-a block with largest magnitude a, at least 448 * 2^-100, scale = a / FMAX and code = nearest(x * (FMAX / a)), or with
-powers of two scale = 2^e with the smallest e that has FMAX * 2^e >= a.  ``gemm`` dequantises to float64 and
+``quantize``: for a block with largest magnitude a, at least 448 * 2^-100, scale = float32(a / FMAX) and code =
+nearest(float32(x FMAX / a)), or with powers of two scale = 2^e with the smallest e that has FMAX * 2^e >= a and code =
+nearest(x 2^-e); the GPU must give the same bits.  ``gemm`` dequantises to float64 and
 contracts; it also returns S = sum |a||b|, which the tolerances scale with.
 
 Pins (``tests/test_oracle_block128.py``): the scale rule against exact fractions, codes against a brute-force nearest
@@ -34,9 +34,14 @@ def block_scales(amax, fmt, pow2):
     return scale, inv
 
 
-def _codes(v, fmt):
-    """uint8 codes of finite float32 values; the products of a block's values stay within one rounding of FMAX."""
-    return encode_rne(np.clip(v, -FMAX[fmt], FMAX[fmt]), fmt)
+def _codes(x, amax, fmt, pow2):
+    """uint8 codes of finite float32 x in blocks with largest magnitudes amax (broadcast against x)."""
+    a = np.maximum(np.asarray(amax, np.float32), TINY).astype(np.float64)
+    if pow2:
+        q = x.astype(np.float64) * block_scales(amax, fmt, True)[1].astype(np.float64)
+    else:
+        q = (x.astype(np.float64) * float(FMAX[fmt]) / a).astype(np.float32)
+    return encode_rne(q, fmt)
 
 
 def _pad(x, axis, m):
@@ -56,20 +61,23 @@ def quantize(x, fmt=0, rows=True, cols=False, square=False, pow2=False):
     t = full.reshape(mb, 128, kb, 128)
     q = s = qt = st = None
     if square:
-        scale, inv = block_scales(np.abs(t).max(axis=(1, 3)), fmt, pow2)
-        codes = _codes(t * inv[:, None, :, None], fmt).reshape(full.shape)
+        amax = np.abs(t).max(axis=(1, 3))
+        scale = block_scales(amax, fmt, pow2)[0]
+        codes = _codes(t, amax[:, None, :, None], fmt, pow2).reshape(full.shape)
         if rows:
             q, s = codes[:M, :k16], scale
         if cols:
             qt, st = codes[:m16, :K].T, scale.T
         return q, s, qt, st
     if rows:
-        scale, inv = block_scales(np.abs(t).max(axis=3), fmt, pow2)            # (mb, 128, kb)
-        codes = _codes(t * inv[..., None], fmt).reshape(full.shape)
+        amax = np.abs(t).max(axis=3)                                            # (mb, 128, kb)
+        scale = block_scales(amax, fmt, pow2)[0]
+        codes = _codes(t, amax[..., None], fmt, pow2).reshape(full.shape)
         q, s = codes[:M, :k16], scale.reshape(mb * 128, kb)[:M].T
     if cols:
-        scale, inv = block_scales(np.abs(t).max(axis=1), fmt, pow2)            # (mb, kb, 128)
-        codes = _codes(t * inv[:, None], fmt).reshape(full.shape)
+        amax = np.abs(t).max(axis=1)                                            # (mb, kb, 128)
+        scale = block_scales(amax, fmt, pow2)[0]
+        codes = _codes(t, amax[:, None], fmt, pow2).reshape(full.shape)
         qt, st = codes[:m16, :K].T, scale.reshape(mb, kb * 128)[:, :K]
     return q, s, qt, st
 

@@ -62,7 +62,7 @@ def test_codes_are_nearest_and_blocks_are_where_they_should_be(fmt, square):
             a1, a2 = np.abs(x[m, cols]).max(), np.abs(x[rows, k]).max()
             assert s[kb, m] == a1 / B.FMAX[fmt] and st[mb, k] == a2 / B.FMAX[fmt]
         for code, a in ((q[m, k], a1), (qt[k, m], a2)):
-            v = float(np.float32(x[m, k] * (B.FMAX[fmt] / a)))
+            v = float(np.float32(float(x[m, k]) * float(B.FMAX[fmt]) / float(a)))
             assert abs(decode(np.array([code]), fmt)[0] - v) == np.abs(vals - v).min()
 
 
