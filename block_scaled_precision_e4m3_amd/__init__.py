@@ -49,6 +49,7 @@ MXG_ROPE_INTERLEAVED = 1
 MXG_ROPE_INTERLEAVED_TO_HALF = 2
 MXG_ROPE_TRANSPOSE = 1
 MXG_ROPE_POS64 = 2
+MXG_TRUSTED_POINTERS = 1073741824
 
 MXG_OK = 0
 MXG_ERR_NULL = -1
@@ -164,13 +165,29 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = _current_device = None  # the cheap current stream and device of torch, once its GPU side is up
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        handle = torch.cuda.current_stream().cuda_stream  # initialises the GPU, or says why it cannot
+        _bind_stream(torch)
+        return handle
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _bind_stream(torch):
+    """The cheap way to the current stream (0.1 us a call instead of 2.7) where this torch has it."""
+    global _raw_stream, _current_device
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+        _current_device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def mxgemm_strerror(status):
@@ -490,51 +507,92 @@ def mx_quantize(x, sf_vec_size=32, fmt=MXG_FMT_E4M3, q=None, sf=None, stream=Non
 
 _ROPE_LAYOUTS = {"half": MXG_ROPE_HALF, "interleaved": MXG_ROPE_INTERLEAVED,
                  "interleaved_to_half": MXG_ROPE_INTERLEAVED_TO_HALF}
-_dtypes = {}  # torch dtype -> MXG_DT_* or MXG_FMT_*, filled on first use
 
 
-def _dtype_tables():
-    import torch
-    _dtypes["dt"] = {torch.float32: MXG_DT_F32, torch.bfloat16: MXG_DT_BF16, torch.float16: MXG_DT_F16}
-    _dtypes["fmt"] = {torch.float8_e4m3fn: MXG_FMT_E4M3, torch.float8_e5m2: MXG_FMT_E5M2}
-    _dtypes["code"] = {MXG_FMT_E4M3: torch.float8_e4m3fn, MXG_FMT_E5M2: torch.float8_e5m2}
-    _dtypes["empty"] = torch.empty
+class _Torch:
+    """What the wrappers below need of torch, bound on first use."""
 
-
-def _dt(t, name):
-    """MXG_DT_* of a tensor or dtype."""
-    if not _dtypes:
-        _dtype_tables()
-    d = _dtypes["dt"].get(getattr(t, "dtype", t))
-    if d is None:
-        raise MxgemmValueError(MXG_ERR_FMT, f"{name} must be float32, bfloat16 or float16")
-    return d
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a kernel on `stream`: its memory is not handed out again before that stream is done with it."""
-    t = _dtypes["empty"](shape, dtype=dtype, device=device)
-    if stream is not None:
+    def __init__(self):
         import torch
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-        if s != torch.cuda.current_stream(t.device):
+        self.torch = torch
+        self.empty = torch.empty_strided
+        self.f32, self.bf16, self.u8 = torch.float32, torch.bfloat16, torch.uint8
+        self.i32, self.i64 = torch.int32, torch.int64
+        self.dt = {torch.float32: MXG_DT_F32, torch.bfloat16: MXG_DT_BF16, torch.float16: MXG_DT_F16}
+        self.fmt = {torch.float8_e4m3fn: MXG_FMT_E4M3, torch.float8_e5m2: MXG_FMT_E5M2}
+        self.code = {MXG_FMT_E4M3: torch.float8_e4m3fn, MXG_FMT_E5M2: torch.float8_e5m2}
+
+
+_env = None
+
+
+def _torch():
+    global _env
+    if _env is None:
+        _env = _Torch()
+    return _env
+
+
+def _refuse(status, msg):
+    raise MxgemmValueError(status, msg)
+
+
+def _here(dev, *tensors):
+    """The device check of the C entry points, for tensors that know their device: all on the current one, which
+    lets the call say MXG_TRUSTED_POINTERS."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _raise(MXG_ERR_DEVICE)
+    if dev < 0 or dev != (_current_device or _env.torch.cuda.current_device)():
+        _raise(MXG_ERR_DEVICE)
+
+
+def _empty(e, shape, dtype, device, stream):
+    """A new contiguous tensor for a kernel on `stream`: its memory is not handed out again before that stream is done
+    with it."""
+    n = len(shape)
+    if n == 2:
+        strides = (shape[1] or 1, 1)
+    elif n == 3:
+        b, c = shape[1] or 1, shape[2] or 1
+        strides = (b * c, c, 1)
+    else:
+        strides = (1,)
+    t = e.empty(shape, strides, dtype=dtype, device=device)
+    if stream is not None:
+        s = e.torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        if s != e.torch.cuda.current_stream(t.device):
             t.record_stream(s)
     return t
 
 
-def _same(t, like, shape, dtype, name):
-    """Checks of an output or operand given by the caller."""
-    if tuple(t.shape) != tuple(shape):
-        raise MxgemmValueError(MXG_ERR_SHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _expect(t, shape, dtype, name):
+    """Checks of a contiguous operand or output given by the caller."""
+    if t.shape != shape:
+        _refuse(MXG_ERR_SHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
-        raise MxgemmValueError(MXG_ERR_FMT, f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise MxgemmValueError(MXG_ERR_DEVICE, f"{name} must be on {like.device}")
-
-
-def _contiguous(t, name):
+        _refuse(MXG_ERR_FMT, f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
-        raise MxgemmValueError(MXG_ERR_ALIGN, f"{name} must be contiguous")
+        _refuse(MXG_ERR_ALIGN, f"{name} must be contiguous")
+
+
+def _matrix_rows(t, name):
+    """(leading dimensions, L, rows, columns, row stride) of a (rows, columns) or (L, rows, columns) tensor whose
+    columns are contiguous and whose rows are evenly spaced, over batches too."""
+    sh, st = t.shape, t.stride()
+    if len(sh) == 2:
+        m, k = sh
+        ld = st[0] if m > 1 else k
+        ok = True
+        l, lead = 1, ()
+    else:
+        l, m, k = sh
+        lead = (l,)
+        ld = st[1] if m > 1 else (st[0] if l > 1 else k)
+        ok = l <= 1 or m * k == 0 or st[0] == m * ld
+    if not ok or ld < k or (k > 1 and st[-1] != 1):
+        _refuse(MXG_ERR_ALIGN, f"{name} must have contiguous rows, evenly spaced over rows and batches")
+    return lead, l, m, k, ld
 
 
 def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, pow2=False, out=None, stream=None):
@@ -550,40 +608,47 @@ def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, 
     product and the input gradient).
 
     pow2: scales are powers of two.  out: those four tensors preallocated (None where not wanted)."""
-    import torch
-    dt = _dt(x, "x")
+    e = _env or _torch()
+    dt = e.dt.get(x.dtype)
+    if dt is None:
+        _refuse(MXG_ERR_FMT, "x must be float32, bfloat16 or float16")
     if x.dim() not in (2, 3):
-        raise MxgemmValueError(MXG_ERR_SHAPE, "x must be (M, K) or (L, M, K)")
-    if fmt not in _dtypes["code"]:
-        raise MxgemmValueError(MXG_ERR_FMT, "fmt must be MXG_FMT_E4M3 or MXG_FMT_E5M2")
+        _refuse(MXG_ERR_SHAPE, "x must be (M, K) or (L, M, K)")
+    f8 = e.code.get(fmt)
+    if f8 is None:
+        _refuse(MXG_ERR_FMT, "fmt must be MXG_FMT_E4M3 or MXG_FMT_E5M2")
     if not rows and not cols:
-        raise MxgemmValueError(MXG_ERR_NULL, "neither rows nor cols asked for")
-    lead = tuple(x.shape[:-2])
-    l, (m, k) = lead[0] if lead else 1, x.shape[-2:]
-    ldx = x.stride(-2) if m > 1 else (x.stride(0) if lead and l > 1 else k)
-    if (k > 1 and x.stride(-1) != 1) or ldx < k or (l > 1 and m * k > 0 and x.stride(0) != m * ldx):
-        raise MxgemmValueError(MXG_ERR_ALIGN, "x must have contiguous rows, evenly spaced over rows and batches")
+        _refuse(MXG_ERR_NULL, "neither rows nor cols asked for")
+    lead, l, m, k, ldx = _matrix_rows(x, "x")
     kb, mb = -(-k // 128), -(-m // 128)
-    f8 = _dtypes["code"][fmt]
-    shapes = ((lead + (m, -(-k // 16) * 16), f8), (lead + ((mb, kb) if square else (kb, m)), torch.float32),
-              (lead + (k, -(-m // 16) * 16), f8), (lead + ((kb, mb) if square else (mb, k)), torch.float32))
-    want = (rows, rows, cols, cols)
-    if out is None:
-        out = tuple(_empty(sh, d, x.device, stream) if w else None for (sh, d), w in zip(shapes, want))
-    else:
-        for t, (sh, d), w, name in zip(out, shapes, want, ("q", "s", "qt", "st")):
-            if (t is not None) != bool(w):
-                raise MxgemmValueError(MXG_ERR_NULL, f"{name} given but not asked for, or the reverse")
-            if w:
-                _same(t, x, sh, d, name)
-                _contiguous(t, name)
-    q, s, qt, st = out
+    q = s = qt = st = None
+    if out is not None:
+        q, s, qt, st = out
+        for t, want, name in ((q, rows, "q"), (s, rows, "s"), (qt, cols, "qt"), (st, cols, "st")):
+            if (t is not None) != bool(want):
+                _refuse(MXG_ERR_NULL, f"{name} given but not asked for, or the reverse")
+    dev = x.get_device()
+    _here(dev, q, s, qt, st) if out is not None or dev < 0 else _here(dev)
+    if rows:
+        qs, ss = lead + (m, -(-k // 16) * 16), lead + ((mb, kb) if square else (kb, m))
+        if q is None:
+            q, s = _empty(e, qs, f8, x.device, stream), _empty(e, ss, e.f32, x.device, stream)
+        else:
+            _expect(q, qs, f8, "q")
+            _expect(s, ss, e.f32, "s")
+    if cols:
+        qs, ss = lead + (k, -(-m // 16) * 16), lead + ((kb, mb) if square else (mb, k))
+        if qt is None:
+            qt, st = _empty(e, qs, f8, x.device, stream), _empty(e, ss, e.f32, x.device, stream)
+        else:
+            _expect(qt, qs, f8, "qt")
+            _expect(st, ss, e.f32, "st")
     status = _lib.mxgemm_block128_quantize(_ptr(x), ldx, _ptr(q), _ptr(s), _ptr(qt), _ptr(st), m, k, l, dt, fmt,
-                                           (MXG_QUANT_SQUARE if square else 0) | (MXG_QUANT_POW2 if pow2 else 0),
-                                           _stream(stream))
+                                           (MXG_QUANT_SQUARE if square else 0) | (MXG_QUANT_POW2 if pow2 else 0)
+                                           | MXG_TRUSTED_POINTERS, _stream(stream))
     if status != MXG_OK:
         _raise(status)
-    return out
+    return q, s, qt, st
 
 
 def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=False, workspace=None, stream=None):
@@ -593,40 +658,52 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
     (ceil(K/128), N) for b_block=1; K a multiple of 16; all with a leading L or none; E4M3 or E5M2 each.  c_dtype:
     float32, bfloat16 (the default) or float16.  c: the output, whose rows may be further apart than N; accumulate
     adds to a float32 c."""
-    import torch
-    if not _dtypes:
-        _dtype_tables()
-    fa, fb = _dtypes["fmt"].get(a.dtype), _dtypes["fmt"].get(b.dtype)
+    e = _env or _torch()
+    fa, fb = e.fmt.get(a.dtype), e.fmt.get(b.dtype)
     if fa is None or fb is None:
-        raise MxgemmValueError(MXG_ERR_FMT, "a and b must be float8_e4m3fn or float8_e5m2")
-    if a.dim() not in (2, 3) or b.dim() != a.dim() or a.shape[-1] != b.shape[-1] or a.shape[:-2] != b.shape[:-2]:
-        raise MxgemmValueError(MXG_ERR_SHAPE, "a and b must be (M, K) and (N, K), or (L, M, K) and (L, N, K)")
-    if b_block not in (1, 128):
-        raise MxgemmValueError(MXG_ERR_SHAPE, "b_block must be 1 or 128")
-    lead = tuple(a.shape[:-2])
-    l, m, n, k = lead[0] if lead else 1, a.shape[-2], b.shape[-2], a.shape[-1]
-    kb = -(-k // 128)
-    _same(sa, a, lead + (kb, m), torch.float32, "sa")
-    _same(sb, a, lead + ((kb, n) if b_block == 1 else (-(-n // 128), kb)), torch.float32, "sb")
-    for t, name in ((a, "a"), (sa, "sa"), (b, "b"), (sb, "sb")):
-        _contiguous(t, name)
-    if c is None:
-        if accumulate:
-            raise MxgemmValueError(MXG_ERR_NULL, "accumulate needs c")
-        ct, ldc = _dt(c_dtype or torch.bfloat16, "c_dtype"), n
-        c = _empty(lead + (m, n), c_dtype or torch.bfloat16, a.device, stream)
+        _refuse(MXG_ERR_FMT, "a and b must be float8_e4m3fn or float8_e5m2")
+    sh, bh = a.shape, b.shape
+    if len(sh) == 2 and len(bh) == 2:
+        (m, k), n, l, lead = sh, bh[0], 1, ()
+    elif len(sh) == 3 and len(bh) == 3 and sh[0] == bh[0]:
+        (l, m, k), n = sh, bh[1]
+        lead = (l,)
     else:
-        ct = _dt(c, "c")
-        _same(c, a, lead + (m, n), c_dtype or c.dtype, "c")
-        ldc = c.stride(-2) if m > 1 else (c.stride(0) if lead and l > 1 else n)
-        if (n > 1 and c.stride(-1) != 1) or ldc < n or (l > 1 and m * n > 0 and c.stride(0) != m * ldc):
-            raise MxgemmValueError(MXG_ERR_ALIGN, "c must have contiguous rows, evenly spaced over rows and batches")
+        _refuse(MXG_ERR_SHAPE, "a and b must be (M, K) and (N, K), or (L, M, K) and (L, N, K)")
+    if bh[-1] != k:
+        _refuse(MXG_ERR_SHAPE, f"a and b disagree on K: {k} and {bh[-1]}")
+    if b_block not in (1, 128):
+        _refuse(MXG_ERR_SHAPE, "b_block must be 1 or 128")
+    kb = -(-k // 128)
+    _expect(sa, lead + (kb, m), e.f32, "sa")
+    _expect(sb, lead + ((kb, n) if b_block == 1 else (-(-n // 128), kb)), e.f32, "sb")
+    if not a.is_contiguous() or not b.is_contiguous():
+        _refuse(MXG_ERR_ALIGN, "a and b must be contiguous")
+    if c is not None:
+        if c.shape != lead + (m, n):
+            _refuse(MXG_ERR_SHAPE, f"c must have shape {lead + (m, n)}, got {tuple(c.shape)}")
+        if c_dtype is not None and c.dtype != c_dtype:
+            _refuse(MXG_ERR_FMT, f"c must be {c_dtype}, got {c.dtype}")
+        c_dtype, ldc = c.dtype, _matrix_rows(c, "c")[4]
+    elif accumulate:
+        _refuse(MXG_ERR_NULL, "accumulate needs c")
+    else:
+        ldc = n
+        if c_dtype is None:
+            c_dtype = e.bf16
+    ct = e.dt.get(c_dtype)
+    if ct is None:
+        _refuse(MXG_ERR_FMT, "c must be float32, bfloat16 or float16")
+    _here(a.get_device(), sa, b, sb, c, workspace)
+    if c is None:
+        c = _empty(e, lead + (m, n), c_dtype, a.device, stream)
     need = _lib.mxgemm_block128_workspace_bytes(m, n, k, l, ct)
     if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, a.device, stream)
-    st = _lib.mxgemm_block128(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(c), ldc, m, n, k, l, fa, fb, ct,
-                              (MXG_B128_B_ROWS if b_block == 1 else 0) | (MXG_B128_ACCUMULATE if accumulate else 0),
-                              _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        workspace = _empty(e, (need,), e.u8, a.device, stream)
+    st = _lib.mxgemm_block128(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), c.data_ptr(), ldc, m, n, k, l,
+                              fa, fb, ct, (MXG_B128_B_ROWS if b_block == 1 else 0)
+                              | (MXG_B128_ACCUMULATE if accumulate else 0) | MXG_TRUSTED_POINTERS, _ptr(workspace),
+                              workspace.numel() * workspace.element_size() if workspace is not None else 0,
                               _stream(stream))
     if st != MXG_OK:
         _raise(st)
@@ -671,57 +748,80 @@ def rope_table(length, rot, base=10000.0, scaling="none", factor=1.0, original_l
             torch.from_numpy((m * np.sin(angle)).astype(np.float32)).to(device))
 
 
-def _rotary(cos, sin, positions, tokens, layout, x):
-    """(rot, table rows, layout number, flags) of the rotary arguments, checked against x."""
-    import torch
+def _rotary(e, cos, sin, positions, tokens, layout):
+    """(rot, table rows, layout number, flags) of the rotary arguments."""
     lay = _ROPE_LAYOUTS.get(layout)
     if lay is None:
-        raise MxgemmValueError(MXG_ERR_FMT, f"layout must be one of {sorted(_ROPE_LAYOUTS)}")
-    flags = 0
+        _refuse(MXG_ERR_FMT, f"layout must be one of {sorted(_ROPE_LAYOUTS)}")
     if cos is None or sin is None:
         if cos is not None or sin is not None or positions is not None:
-            raise MxgemmValueError(MXG_ERR_NULL, "cos and sin come together, and positions with them")
-        return 0, 0, lay, 0
-    if cos.dim() != 2 or cos.shape != sin.shape:
-        raise MxgemmValueError(MXG_ERR_SHAPE, "cos and sin must be (table rows, rot / 2)")
-    for t, name in ((cos, "cos"), (sin, "sin")):
-        if t.dtype != torch.float32:
-            raise MxgemmValueError(MXG_ERR_FMT, f"{name} must be float32")
-        _contiguous(t, name)
+            _refuse(MXG_ERR_NULL, "cos and sin come together, and positions with them")
+        return 0, 0, lay, MXG_TRUSTED_POINTERS
+    table = cos.shape
+    if len(table) != 2 or sin.shape != table:
+        _refuse(MXG_ERR_SHAPE, "cos and sin must be (table rows, rot / 2)")
+    if cos.dtype != e.f32 or sin.dtype != e.f32:
+        _refuse(MXG_ERR_FMT, "cos and sin must be float32")
+    if not cos.is_contiguous() or not sin.is_contiguous():
+        _refuse(MXG_ERR_ALIGN, "cos and sin must be contiguous")
+    flags = MXG_TRUSTED_POINTERS
     if positions is not None:
-        if tuple(positions.shape) != (tokens,):
-            raise MxgemmValueError(MXG_ERR_SHAPE, "positions must have one entry per token")
-        if positions.dtype == torch.int64:
-            flags = MXG_ROPE_POS64
-        elif positions.dtype != torch.int32:
-            raise MxgemmValueError(MXG_ERR_FMT, "positions must be int32 or int64")
-        _contiguous(positions, "positions")
-    return 2 * cos.shape[1], cos.shape[0], lay, flags
+        if positions.shape != (tokens,):
+            _refuse(MXG_ERR_SHAPE, "positions must have one entry per token")
+        if positions.dtype == e.i64:
+            flags |= MXG_ROPE_POS64
+        elif positions.dtype != e.i32:
+            _refuse(MXG_ERR_FMT, "positions must be int32 or int64")
+        if not positions.is_contiguous():
+            _refuse(MXG_ERR_ALIGN, "positions must be contiguous")
+    return 2 * table[1], table[0], lay, flags
 
 
-def _heads_of(x, name, like=None):
-    """Checks of a (T, heads, D) tensor with contiguous features; `like`: T, D, dtype and device to share."""
-    if x.dim() != 3:
-        raise MxgemmValueError(MXG_ERR_SHAPE, f"{name} must be (tokens, heads, features)")
-    if x.shape[2] > 1 and x.stride(2) != 1:
-        raise MxgemmValueError(MXG_ERR_ALIGN, f"{name} must have contiguous features")
-    if like is not None:
-        _same(x, like, (like.shape[0], x.shape[1], like.shape[2]), like.dtype, name)
+def _heads_of(x, name):
+    """Shape and strides of a (T, heads, D) tensor with contiguous features."""
+    sh, st = x.shape, x.stride()
+    if len(sh) != 3:
+        _refuse(MXG_ERR_SHAPE, f"{name} must be (tokens, heads, features)")
+    if st[2] != 1 and sh[2] > 1:
+        _refuse(MXG_ERR_ALIGN, f"{name} must have contiguous features")
+    return sh, st
 
 
-def _new_heads(x, stream):
-    return _empty(tuple(x.shape), x.dtype, x.device, stream)
+def _like(t, x, shape, name):
+    """Strides of a tensor that must have a (T, heads, D) shape and x's dtype."""
+    sh, st = _heads_of(t, name)
+    if sh != shape:
+        _refuse(MXG_ERR_SHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(sh)}")
+    if t.dtype != x.dtype:
+        _refuse(MXG_ERR_FMT, f"{name} must be {x.dtype}, got {t.dtype}")
+    return st
 
 
-def _strides(*tensors):
-    flat = []
-    for t in tensors:
-        if t is None:
-            flat += (0, 0)
-        else:
-            st = t.stride()
-            flat += (st[0], st[1])
-    return (ctypes.c_int64 * len(flat))(*flat)
+def _keys(k, q):
+    """(shape, strides, heads) of the keys that go with q; k may be None."""
+    if k is None:
+        return None, (0, 0), 0
+    sh, st = _heads_of(k, "k")
+    if sh[0] != q.shape[0] or sh[2] != q.shape[2]:
+        _refuse(MXG_ERR_SHAPE, "q and k must have the same tokens and features")
+    if k.dtype != q.dtype:
+        _refuse(MXG_ERR_FMT, f"k must be {q.dtype}, got {k.dtype}")
+    return sh, st, sh[1]
+
+
+def _pair(e, out, q, k, kh, names, stream):
+    """Outputs for q and k, new or given: (for q, for k, strides of each)."""
+    if out is None:
+        yq = _empty(e, q.shape, q.dtype, q.device, stream)
+        yk = None if k is None else _empty(e, kh, k.dtype, k.device, stream)
+        return yq, yk, yq.stride(), (0, 0) if yk is None else yk.stride()
+    yq, yk = out
+    if yq is None or (yk is None) != (k is None):
+        _refuse(MXG_ERR_NULL, "outputs must be given for q, and for k where there is one")
+    return yq, yk, _like(yq, q, q.shape, names[0]), (0, 0) if yk is None else _like(yk, k, kh, names[1])
+
+
+_Strides4, _Strides8, _Strides12 = ctypes.c_int64 * 4, ctypes.c_int64 * 8, ctypes.c_int64 * 12
 
 
 def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=False, out=None, stream=None):
@@ -733,33 +833,38 @@ def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=Fal
     whose position lies outside the tables gets NaN there.  layout: "half" (pairs i, i + rot/2), "interleaved"
     (pairs 2i, 2i + 1) or "interleaved_to_half" (the latter in, the former out).  transpose: the transposed map, which takes
     the output's gradient to the input's.  out: the result, which may be x; a new tensor by default."""
-    dt = _dt(x, "x")
-    _heads_of(x, "x")
-    t, h, d = x.shape
-    rot, rows, lay, flags = _rotary(cos, sin, positions, t, layout, x)
+    e = _env or _torch()
+    dt = e.dt.get(x.dtype)
+    if dt is None:
+        _refuse(MXG_ERR_FMT, "x must be float32, bfloat16 or float16")
+    sh, xs = _heads_of(x, "x")
+    t, h, d = sh
+    rot, rows, lay, flags = _rotary(e, cos, sin, positions, t, layout)
+    if out is not None:
+        os_ = _like(out, x, sh, "out")
+    _here(x.get_device(), cos, sin, positions, out)
     if out is None:
-        out = _new_heads(x, stream)
-    else:
-        _heads_of(out, "out", x)
-        _same(out, x, x.shape, x.dtype, "out")
-    st = _lib.mxgemm_rope(_ptr(x), _ptr(out), _ptr(cos), _ptr(sin), _ptr(positions), _strides(x, out), t, h, d, rot,
-                          rot_offset, rows, lay, dt, flags | (MXG_ROPE_TRANSPOSE if transpose else 0), _stream(stream))
+        out = _empty(e, sh, x.dtype, x.device, stream)
+        os_ = out.stride()
+    st = _lib.mxgemm_rope(x.data_ptr(), out.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions),
+                          _Strides4(xs[0], xs[1], os_[0], os_[1]), t, h, d, rot, rot_offset, rows, lay, dt,
+                          flags | (MXG_ROPE_TRANSPOSE if transpose else 0), _stream(stream))
     if st != MXG_OK:
         _raise(st)
     return out
 
 
-def _weights(q_weight, k_weight, q, k):
-    import torch
-    for w, x, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
-        if x is None:
-            continue
-        _same(w, x, (x.shape[2],), w.dtype, name)
-        _contiguous(w, name)
-    w_dtype = q_weight.dtype
-    if w_dtype not in (q.dtype, torch.float32) or (k is not None and k_weight.dtype != w_dtype):
-        raise MxgemmValueError(MXG_ERR_FMT, "weights must both be float32 or of the dtype of q and k")
-    return _dt(w_dtype, "q_weight")
+def _weights(e, q_weight, k_weight, q, k):
+    """MXG_DT_* of the norm weights."""
+    d, w_dtype = q.shape[2], q_weight.dtype
+    if w_dtype not in (q.dtype, e.f32) or (k is not None and k_weight.dtype != w_dtype):
+        _refuse(MXG_ERR_FMT, "weights must both be float32 or of the dtype of q and k")
+    for w in (q_weight,) if k is None else (q_weight, k_weight):
+        if w.shape != (d,):
+            _refuse(MXG_ERR_SHAPE, f"weights must have {d} elements")
+        if not w.is_contiguous():
+            _refuse(MXG_ERR_ALIGN, "weights must be contiguous")
+    return e.dt[w_dtype]
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, eps=1e-6, layout="half", rot_offset=0,
@@ -767,27 +872,23 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, e
     """C-ABI mxgemm_qk_norm_rope: each head of q (T, Hq, D) and k (T, Hk, D) divided by its root mean square,
     multiplied with its weight (D) and rotated, in one launch.  Returns (q_out, k_out); out: that pair, which may be
     (q, k).  k and k_weight may be None.  cos, sin None: no rotation.  The other arguments are rope's."""
-    dt = _dt(q, "q")
-    _heads_of(q, "q")
-    if k is not None:
-        _heads_of(k, "k", q)
-    wdt = _weights(q_weight, k_weight, q, k)
-    t, hq, d = q.shape
-    hk = 0 if k is None else k.shape[1]
-    rot, rows, lay, flags = _rotary(cos, sin, positions, t, layout, q)
-    if out is None:
-        yq, yk = _new_heads(q, stream), None if k is None else _new_heads(k, stream)
-    else:
-        yq, yk = out
-        for y, x, name in ((yq, q, "q_out"), (yk, k, "k_out")):
-            if (y is None) != (x is None):
-                raise MxgemmValueError(MXG_ERR_NULL, f"{name} must be given with its input")
-            if y is not None:
-                _heads_of(y, name, q)
-                _same(y, x, x.shape, x.dtype, name)
-    st = _lib.mxgemm_qk_norm_rope(_ptr(q), _ptr(k), _ptr(yq), _ptr(yk), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-                                  _ptr(sin), _ptr(positions), _strides(q, k, yq, yk), t, hq, hk, d, rot, rot_offset,
-                                  rows, eps, lay, dt, wdt, flags, _stream(stream))
+    e = _env or _torch()
+    dt = e.dt.get(q.dtype)
+    if dt is None:
+        _refuse(MXG_ERR_FMT, "q must be float32, bfloat16 or float16")
+    (t, hq, d), qs = _heads_of(q, "q")
+    kh, ks, hk = _keys(k, q)
+    wdt = _weights(e, q_weight, k_weight, q, k)
+    rot, rows, lay, flags = _rotary(e, cos, sin, positions, t, layout)
+    dev = q.get_device()
+    _here(dev, k, q_weight, k_weight, cos, sin, positions)
+    yq, yk, yqs, yks = _pair(e, out, q, k, kh, ("q_out", "k_out"), stream)
+    if out is not None:
+        _here(dev, yq, yk)
+    st = _lib.mxgemm_qk_norm_rope(q.data_ptr(), _ptr(k), yq.data_ptr(), _ptr(yk), q_weight.data_ptr(), _ptr(k_weight),
+                                  _ptr(cos), _ptr(sin), _ptr(positions),
+                                  _Strides8(qs[0], qs[1], ks[0], ks[1], yqs[0], yqs[1], yks[0], yks[1]), t, hq, hk, d,
+                                  rot, rot_offset, rows, eps, lay, dt, wdt, flags, _stream(stream))
     if st != MXG_OK:
         _raise(st)
     return yq, yk
@@ -798,40 +899,35 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, 
     """C-ABI mxgemm_qk_norm_rope_backward: from the gradients dq, dk of qk_norm_rope's outputs and its inputs,
     (dq_in, dk_in, dq_weight, dk_weight), the weight gradients float32 (None for a missing k).  out: the first two,
     which may be (dq, dk) or (q, k)."""
-    import torch
-    dt = _dt(q, "q")
-    _heads_of(q, "q")
-    _heads_of(dq, "dq", q)
-    _same(dq, q, q.shape, q.dtype, "dq")
+    e = _env or _torch()
+    dt = e.dt.get(q.dtype)
+    if dt is None:
+        _refuse(MXG_ERR_FMT, "q must be float32, bfloat16 or float16")
+    qh, qs = _heads_of(q, "q")
+    t, hq, d = qh
+    kh, ks, hk = _keys(k, q)
+    gqs = _like(dq, q, qh, "dq")
     if (dk is None) != (k is None):
-        raise MxgemmValueError(MXG_ERR_NULL, "dk must be given with k")
-    if k is not None:
-        _heads_of(k, "k", q)
-        _heads_of(dk, "dk", q)
-        _same(dk, k, k.shape, k.dtype, "dk")
-    wdt = _weights(q_weight, k_weight, q, k)
-    t, hq, d = q.shape
-    hk = 0 if k is None else k.shape[1]
-    rot, rows, lay, flags = _rotary(cos, sin, positions, t, layout, q)
-    if out is None:
-        xq, xk = _new_heads(q, stream), None if k is None else _new_heads(k, stream)
-    else:
-        xq, xk = out
-        for y, x, name in ((xq, q, "dq_in"), (xk, k, "dk_in")):
-            if (y is None) != (x is None):
-                raise MxgemmValueError(MXG_ERR_NULL, f"{name} must be given with its input")
-            if y is not None:
-                _heads_of(y, name, q)
-                _same(y, x, x.shape, x.dtype, name)
-    dwq = _empty((d,), torch.float32, q.device, stream)
-    dwk = None if k is None else _empty((d,), torch.float32, q.device, stream)
+        _refuse(MXG_ERR_NULL, "dk must be given with k")
+    gks = (0, 0) if dk is None else _like(dk, k, kh, "dk")
+    wdt = _weights(e, q_weight, k_weight, q, k)
+    rot, rows, lay, flags = _rotary(e, cos, sin, positions, t, layout)
+    dev = q.get_device()
+    _here(dev, k, dq, dk, q_weight, k_weight, cos, sin, positions, workspace)
+    xq, xk, xqs, xks = _pair(e, out, q, k, kh, ("dq_in", "dk_in"), stream)
+    if out is not None:
+        _here(dev, xq, xk)
+    dwq = _empty(e, (d,), e.f32, q.device, stream)
+    dwk = None if k is None else _empty(e, (d,), e.f32, q.device, stream)
     if workspace is None:
         need = _lib.mxgemm_qk_norm_rope_backward_workspace_bytes(t, d)
-        workspace = _empty((need,), torch.uint8, q.device, stream)
+        workspace = _empty(e, (need,), e.u8, q.device, stream)
     st = _lib.mxgemm_qk_norm_rope_backward(
-        _ptr(dq), _ptr(dk), _ptr(q), _ptr(k), _ptr(xq), _ptr(xk), _ptr(dwq), _ptr(dwk), _ptr(q_weight), _ptr(k_weight),
-        _ptr(cos), _ptr(sin), _ptr(positions), _strides(dq, dk, q, k, xq, xk), t, hq, hk, d, rot, rot_offset, rows,
-        eps, lay, dt, wdt, flags, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        dq.data_ptr(), _ptr(dk), q.data_ptr(), _ptr(k), xq.data_ptr(), _ptr(xk), dwq.data_ptr(), _ptr(dwk),
+        q_weight.data_ptr(), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
+        _Strides12(gqs[0], gqs[1], gks[0], gks[1], qs[0], qs[1], ks[0], ks[1], xqs[0], xqs[1], xks[0], xks[1]), t, hq, hk,
+        d, rot, rot_offset, rows, eps, lay, dt, wdt, flags, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
     if st != MXG_OK:
         _raise(st)
     return xq, xk, dwq, dwk
@@ -850,5 +946,5 @@ __all__ = [
     "block128_quantize", "block128_gemm", "rope_table", "rope", "qk_norm_rope", "qk_norm_rope_backward",
     "MXG_DT_F32", "MXG_DT_BF16", "MXG_DT_F16", "MXG_QUANT_SQUARE", "MXG_QUANT_POW2", "MXG_B128_B_ROWS",
     "MXG_B128_ACCUMULATE", "MXG_ROPE_HALF", "MXG_ROPE_INTERLEAVED", "MXG_ROPE_INTERLEAVED_TO_HALF",
-    "MXG_ROPE_TRANSPOSE", "MXG_ROPE_POS64",
+    "MXG_ROPE_TRANSPOSE", "MXG_ROPE_POS64", "MXG_TRUSTED_POINTERS",
 ]

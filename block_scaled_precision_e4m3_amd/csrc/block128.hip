@@ -12,6 +12,13 @@
 namespace {
 
 using namespace mxg::host;
+
+// Takes MXG_TRUSTED_POINTERS out of a call's flags.
+bool take_trust(unsigned* flags) {
+  const bool trusted = (*flags & MXG_TRUSTED_POINTERS) != 0;
+  *flags &= ~(unsigned)MXG_TRUSTED_POINTERS;
+  return trusted;
+}
 using mxg::b128::GemmParams;
 using mxg::b128::QuantParams;
 
@@ -141,6 +148,7 @@ extern "C" {
 
 int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void* QT, float* ST, int64_t M, int64_t K,
                              int64_t L, int x_dtype, int fmt, unsigned flags, void* stream) {
+  const bool trusted = take_trust(&flags);
   int st = check_quantize(ldx, M, K, L, x_dtype, fmt, flags);
   if (st != MXG_OK) return st;
   if (M == 0 || K == 0 || L == 0) return MXG_OK;
@@ -152,8 +160,8 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
   int dev = 0, cus = 0;
   st = device_check(&dev, &cus);
   if (st != MXG_OK) return st;
-  if (!on_device(X, dev) || (rows && (!on_device(Q, dev) || !on_device(S, dev))) ||
-      (cols && (!on_device(QT, dev) || !on_device(ST, dev))))
+  if (!trusted && (!on_device(X, dev) || (rows && (!on_device(Q, dev) || !on_device(S, dev))) ||
+      (cols && (!on_device(QT, dev) || !on_device(ST, dev)))))
     return MXG_ERR_DEVICE;
   QuantParams p{};
   p.X = X;
@@ -193,6 +201,7 @@ size_t mxgemm_block128_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t 
 int mxgemm_block128(const void* A, const float* SA, const void* B, const float* SB, void* C, int64_t ldc, int64_t M,
                     int64_t N, int64_t K, int64_t L, int a_fmt, int b_fmt, int c_dtype, unsigned flags, void* workspace,
                     size_t workspace_bytes, void* stream) {
+  const bool trusted = take_trust(&flags);
   int st = check_gemm(ldc, M, N, K, L, a_fmt, b_fmt, c_dtype, flags);
   if (st != MXG_OK) return st;
   if (M == 0 || N == 0 || L == 0) return MXG_OK;
@@ -206,9 +215,9 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
   int dev = 0, cus = 0;
   st = device_check(&dev, &cus);
   if (st != MXG_OK) return st;
-  if (!on_device(C, dev) || (K > 0 && (!on_device(A, dev) || !on_device(B, dev) || !on_device(SA, dev) ||
+  if (!trusted && (!on_device(C, dev) || (K > 0 && (!on_device(A, dev) || !on_device(B, dev) || !on_device(SA, dev) ||
                                        !on_device(SB, dev))) ||
-      (need > 0 && !on_device(workspace, dev)))
+      (need > 0 && !on_device(workspace, dev))))
     return MXG_ERR_DEVICE;
   GemmParams p{};
   p.A = static_cast<const uint8_t*>(A);

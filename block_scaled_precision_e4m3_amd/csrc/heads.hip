@@ -11,6 +11,13 @@
 namespace {
 
 using namespace mxg::host;
+
+// Takes MXG_TRUSTED_POINTERS out of a call's flags.
+bool take_trust(unsigned* flags) {
+  const bool trusted = (*flags & MXG_TRUSTED_POINTERS) != 0;
+  *flags &= ~(unsigned)MXG_TRUSTED_POINTERS;
+  return trusted;
+}
 using mxg::heads::Params;
 using mxg::heads::Tensor;
 
@@ -132,6 +139,7 @@ extern "C" {
 int mxgemm_rope(const void* X, void* Y, const float* cos, const float* sin, const void* positions,
                 const int64_t* strides, int64_t T, int64_t H, int64_t D, int64_t rot, int64_t rot_offset,
                 int64_t table_rows, int layout, int dtype, unsigned flags, void* stream) {
+  const bool trusted = take_trust(&flags);
   int st = check(T, H, 0, D, rot, rot_offset, table_rows, positions != nullptr, layout, dtype, dtype, flags,
                  MXG_ROPE_TRANSPOSE | MXG_ROPE_POS64, strides, 2);
   if (st != MXG_OK) return st;
@@ -144,8 +152,8 @@ int mxgemm_rope(const void* X, void* Y, const float* cos, const float* sin, cons
   int dev = 0, cus = 0;
   st = device_check(&dev, &cus);
   if (st != MXG_OK) return st;
-  if (!on_device(X, dev) || !on_device(Y, dev) || (rot > 0 && (!on_device(cos, dev) || !on_device(sin, dev))) ||
-      (positions && !on_device(positions, dev)))
+  if (!trusted && (!on_device(X, dev) || !on_device(Y, dev) || (rot > 0 && (!on_device(cos, dev) || !on_device(sin, dev))) ||
+      (positions && !on_device(positions, dev))))
     return MXG_ERR_DEVICE;
   Params p{};
   p.x[0] = {const_cast<void*>(X), strides[0], strides[1]};
@@ -169,6 +177,7 @@ int mxgemm_qk_norm_rope(const void* Q, const void* K, void* YQ, void* YK, const 
                         const float* cos, const float* sin, const void* positions, const int64_t* strides, int64_t T,
                         int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t rot_offset, int64_t table_rows,
                         float eps, int layout, int dtype, int w_dtype, unsigned flags, void* stream) {
+  const bool trusted = take_trust(&flags);
   int st = check(T, Hq, Hk, D, rot, rot_offset, table_rows, positions != nullptr, layout, dtype, w_dtype, flags,
                  MXG_ROPE_POS64, strides, 4);
   if (st != MXG_OK) return st;
@@ -184,14 +193,16 @@ int mxgemm_qk_norm_rope(const void* Q, const void* K, void* YQ, void* YK, const 
   int dev = 0, cus = 0;
   st = device_check(&dev, &cus);
   if (st != MXG_OK) return st;
-  if (Hq > 0)
-    for (const void* q : {Q, (const void*)YQ, WQ})
-      if (!on_device(q, dev)) return MXG_ERR_DEVICE;
-  if (Hk > 0)
-    for (const void* q : {K, (const void*)YK, WK})
-      if (!on_device(q, dev)) return MXG_ERR_DEVICE;
-  if ((rot > 0 && (!on_device(cos, dev) || !on_device(sin, dev))) || (positions && !on_device(positions, dev)))
-    return MXG_ERR_DEVICE;
+  if (!trusted) {
+    if (Hq > 0)
+      for (const void* q : {Q, (const void*)YQ, WQ})
+        if (!on_device(q, dev)) return MXG_ERR_DEVICE;
+    if (Hk > 0)
+      for (const void* q : {K, (const void*)YK, WK})
+        if (!on_device(q, dev)) return MXG_ERR_DEVICE;
+    if ((rot > 0 && (!on_device(cos, dev) || !on_device(sin, dev))) || (positions && !on_device(positions, dev)))
+      return MXG_ERR_DEVICE;
+  }
   Params p{};
   p.x[0] = {const_cast<void*>(Q), strides[0], strides[1]};
   p.x[1] = {const_cast<void*>(K), strides[2], strides[3]};
@@ -229,6 +240,7 @@ int mxgemm_qk_norm_rope_backward(const void* GQ, const void* GK, const void* Q, 
                                  int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t rot_offset,
                                  int64_t table_rows, float eps, int layout, int dtype, int w_dtype, unsigned flags,
                                  void* workspace, size_t workspace_bytes, void* stream) {
+  const bool trusted = take_trust(&flags);
   int st = check(T, Hq, Hk, D, rot, rot_offset, table_rows, positions != nullptr, layout, dtype, w_dtype, flags,
                  MXG_ROPE_POS64, strides, 6);
   if (st != MXG_OK) return st;
@@ -247,8 +259,9 @@ int mxgemm_qk_norm_rope_backward(const void* GQ, const void* GK, const void* Q, 
   int dev = 0, cus = 0;
   st = device_check(&dev, &cus);
   if (st != MXG_OK) return st;
-  if (!on_device(DWQ, dev) || (DWK && !on_device(DWK, dev)) || !on_device(workspace, dev)) return MXG_ERR_DEVICE;
-  if (!empty) {
+  if (!trusted && (!on_device(DWQ, dev) || (DWK && !on_device(DWK, dev)) || !on_device(workspace, dev)))
+    return MXG_ERR_DEVICE;
+  if (!empty && !trusted) {
     if (Hq > 0)
       for (const void* q : {GQ, Q, (const void*)DQ, WQ})
         if (!on_device(q, dev)) return MXG_ERR_DEVICE;

@@ -449,6 +449,14 @@ enum {
   MXG_DT_F16 = 2   /* float16  */
 };
 
+/* a flag of all of them */
+enum {
+  /* The caller vouches that every buffer is memory of the current device: the
+     library does not ask HIP where each one lives (as a plan's execute does not;
+     0.25 us of host time per buffer). */
+  MXG_TRUSTED_POINTERS = 1073741824 /* 2^30 */
+};
+
 /* flags of mxgemm_block128_quantize */
 enum {
   MXG_QUANT_SQUARE = 1u, /* blocks of 128x128 instead of 1x128 / 128x1        */
