@@ -514,7 +514,13 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.torch = torch
+        try:
+            from . import _bind
+        except ImportError:  # a library built without torch at hand: every call goes through the checks below
+            _bind = None
+        else:
+            _bind.on_status(_raise)
+        self.torch, self.fast = torch, _bind
         self.empty = torch.empty_strided
         self.f32, self.bf16, self.u8 = torch.float32, torch.bfloat16, torch.uint8
         self.i32, self.i64 = torch.int32, torch.int64
@@ -609,6 +615,10 @@ def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, 
 
     pow2: scales are powers of two.  out: those four tensors preallocated (None where not wanted)."""
     e = _env or _torch()
+    if out is None and stream is None and e.fast is not None:
+        done = e.fast.quantize(x, fmt, rows, cols, square, pow2)
+        if done is not None:
+            return done
     dt = e.dt.get(x.dtype)
     if dt is None:
         _refuse(MXG_ERR_FMT, "x must be float32, bfloat16 or float16")
@@ -659,6 +669,10 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
     float32, bfloat16 (the default) or float16.  c: the output, whose rows may be further apart than N; accumulate
     adds to a float32 c."""
     e = _env or _torch()
+    if stream is None and workspace is None and e.fast is not None:
+        done = e.fast.gemm(a, sa, b, sb, b_block, c_dtype, c, accumulate)
+        if done is not None:
+            return done
     fa, fb = e.fmt.get(a.dtype), e.fmt.get(b.dtype)
     if fa is None or fb is None:
         _refuse(MXG_ERR_FMT, "a and b must be float8_e4m3fn or float8_e5m2")
@@ -834,6 +848,10 @@ def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=Fal
     (pairs 2i, 2i + 1) or "interleaved_to_half" (the latter in, the former out).  transpose: the transposed map, which takes
     the output's gradient to the input's.  out: the result, which may be x; a new tensor by default."""
     e = _env or _torch()
+    if stream is None and e.fast is not None:
+        done = e.fast.rope(x, cos, sin, positions, layout, rot_offset, transpose, out)
+        if done is not None:
+            return done
     dt = e.dt.get(x.dtype)
     if dt is None:
         _refuse(MXG_ERR_FMT, "x must be float32, bfloat16 or float16")
@@ -873,6 +891,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, e
     multiplied with its weight (D) and rotated, in one launch.  Returns (q_out, k_out); out: that pair, which may be
     (q, k).  k and k_weight may be None.  cos, sin None: no rotation.  The other arguments are rope's."""
     e = _env or _torch()
+    if out is None and stream is None and e.fast is not None:
+        done = e.fast.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, layout, rot_offset, eps)
+        if done is not None:
+            return done
     dt = e.dt.get(q.dtype)
     if dt is None:
         _refuse(MXG_ERR_FMT, "q must be float32, bfloat16 or float16")
@@ -900,6 +922,10 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, 
     (dq_in, dk_in, dq_weight, dk_weight), the weight gradients float32 (None for a missing k).  out: the first two,
     which may be (dq, dk) or (q, k)."""
     e = _env or _torch()
+    if out is None and stream is None and workspace is None and e.fast is not None:
+        done = e.fast.qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions, layout, rot_offset, eps)
+        if done is not None:
+            return done
     dt = e.dt.get(q.dtype)
     if dt is None:
         _refuse(MXG_ERR_FMT, "q must be float32, bfloat16 or float16")

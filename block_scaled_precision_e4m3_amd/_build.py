@@ -21,6 +21,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mxgemm.hip", "launch_t256_bf16_f32.h
                                            "block128_tile128.hip", "block128_tile64.hip", "block128_exact.hip",
                                            "block128_rows.hip", "heads.hip")]
 LIB = os.path.join(PKG_DIR, "libmxgemm.so")
+# The torch wrappers' short way into the library (host code only, against torch's headers).
+BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(PKG_DIR, "_bind.so")
 OBJ_DIR = os.path.join(PKG_DIR, "_build")
 
 HIPCC_FLAGS = [
@@ -41,8 +44,31 @@ def hipcc():
     return exe
 
 
+def build_bind(verbose=False):
+    """Compile _bind.so against torch and the built library; without torch there is nothing for it to serve."""
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch_dir = os.path.dirname(spec.origin)
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           "-I" + os.path.join(torch_dir, "include"), "-I" + os.path.join(torch_dir, "include/torch/csrc/api/include"),
+           "-I" + sysconfig.get_path("include"), "-I" + os.path.join(rocm, "include"), BIND_SOURCE, "-o", BIND + ".tmp",
+           "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           "-L" + PKG_DIR, "-l:libmxgemm.so", "-L" + os.path.join(rocm, "lib"), "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed on bind.cpp:\n" + res.stdout + res.stderr)
+    os.replace(BIND + ".tmp", BIND)
+    return BIND
+
+
 def build(verbose=False, extra_flags=(), jobs=None):
-    """Compile libmxgemm.so (always recompiles every unit). Returns the library path."""
+    """Compile libmxgemm.so (always recompiles every unit) and _bind.so. Returns the library path."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     cc = hipcc()
     objs, procs = [], []
@@ -68,6 +94,7 @@ def build(verbose=False, extra_flags=(), jobs=None):
     if res.returncode != 0:
         raise RuntimeError("hipcc link failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB)
+    build_bind(verbose)
     return LIB
 
 
