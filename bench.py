@@ -659,6 +659,66 @@ def bench_proj(args):
     print(json.dumps(out), flush=True)
 
 
+def bench_qkv(args):
+    """One JSON line for the input half of an attention layer (examples/attention_input.py) in bfloat16: a step is
+    quantise, product, norm + rotary positions, and the backward pass of all of it with both gradients' products.
+    Also the forward pass alone, and a decode step of one token, called as it is and replayed from a graph."""
+    import torch
+
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import attention_input
+    tokens, hidden, heads, kv_heads, head_dim = 8192, 4096, 32, 8, 128
+    torch.manual_seed(5)
+    layer = attention_input.AttentionInput(hidden, heads, kv_heads, head_dim, tokens)
+    x = torch.randn(tokens, hidden, device="cuda").bfloat16().requires_grad_()
+    grads = [torch.randn_like(o) for o in layer(x)]
+    inputs = (x, layer.weight, layer.q_norm, layer.k_norm)
+    one, at = x[:1].detach(), torch.tensor([tokens - 1], device="cuda")
+
+    def step():
+        return torch.autograd.grad(layer(x), inputs, grads)
+
+    def forward():
+        with torch.no_grad():
+            return layer(x)
+
+    def decode():
+        with torch.no_grad():
+            return layer(one, at)
+
+    def timed(f, steps):
+        for _ in range(args.warmup):
+            f()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for _ in range(steps):
+            f()
+        torch.cuda.synchronize()
+        return (time.perf_counter() - t0) * 1e3 / steps
+
+    ms = timed(step, args.steps)
+    forward_ms, decode_ms = timed(forward, args.steps), timed(decode, 10 * args.steps)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        decode()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        decode()
+    graph_ms = timed(graph.replay, 10 * args.steps)
+    flops = 2.0 * tokens * hidden * (heads + 2 * kv_heads) * head_dim
+    print(json.dumps({
+        "metric": "attention input layer, forward and backward, TFLOP/s (the three products' flops over the whole step)",
+        "value": round(3 * flops / (ms * 1e-3) / 1e12, 2), "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(ms, 4), "higher_is_better": True, "scaling": "weak",
+        "vs_baseline": None, "dtype": "bf16 in and out, e4m3 codes with float32 scales per 128", "data": "synthetic (seeded normal)",
+        "config": {"workload": "attention input", "tokens": tokens, "hidden": hidden, "num_heads": heads,
+                   "num_kv_heads": kv_heads, "head_dim": head_dim},
+        "forward_ms": round(forward_ms, 4), "forward_tflops": round(flops / (forward_ms * 1e-3) / 1e12, 1),
+        "decode_us": round(decode_ms * 1e3, 2), "decode_graph_us": round(graph_ms * 1e3, 2)}), flush=True)
+
+
 def bench_probe(args):
     """One JSON line of hardware ceilings measured on this GPU (include/mxgemm_probe.h): the dense MFMA
     rate and shader clock with all CUs busy (bf16 32x32x16 and scaled FP8 32x32x64), the global->LDS
@@ -738,10 +798,11 @@ def main():
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--workload", type=int, default=5)
-    ap.add_argument("--op", choices=["gemm", "quantize", "proj", "probe"], default="gemm",
+    ap.add_argument("--op", choices=["gemm", "quantize", "proj", "qkv", "probe"], default="gemm",
                     help="gemm: the GEMM + amax step (default); quantize: the MX quantisation of the "
                          "workload's float32 operands; proj: the projection pipeline (row-wise scales -> GEMM -> "
-                         "RoPE + dual-direction MXFP8) at the projection workload's shape; probe: hardware "
+                         "RoPE + dual-direction MXFP8) at the projection workload's shape; qkv: the input half of "
+                         "an attention layer on block-128 codes, forward and backward; probe: hardware "
                          "ceilings (MFMA rate and clock, global->LDS path, HBM bandwidth)")
     ap.add_argument("--fp8-mfma", action="store_true", help="time the reduced-precision FP8 MFMA path")
     ap.add_argument("--fp4", action="store_true",
@@ -780,6 +841,9 @@ def main():
         return
     if args.op == "proj":
         bench_proj(args)
+        return
+    if args.op == "qkv":
+        bench_qkv(args)
         return
     if args.op == "probe":
         bench_probe(args)
