@@ -10,8 +10,11 @@
 // multiply and one multiply-add per element, which rounds the quotient to
 // float32 correctly: a ratio that lies on a boundary between two codes, as those
 // of 16-bit values often do, stays on it.  With hi alone 0.3% of the codes of
-// bfloat16 activations came out on the other side.  No clamp is needed: the
-// quotient never exceeds FMAX.
+// bfloat16 activations came out on the other side.  Quotients of 16-bit values
+// are either on a boundary or 2^-16 of themselves away; one of float32 values can
+// be so near that float32 rounds it onto the boundary, about one in 2^20, and
+// settle() then looks at what was rounded off.  No clamp is needed: the quotient
+// never exceeds FMAX.
 //
 // A workgroup takes a tile of 16 RT rows x 128 columns: thread (g, c) holds
 // rows RT g .. RT g + RT - 1 of columns 8c .. 8c + 7 in registers, RT chunks of
@@ -74,6 +77,44 @@ __device__ __forceinline__ Scale block_scale(unsigned bits, bool pow2) {
 }
 
 __device__ __forceinline__ float scaled(float x, const Scale& s) { return __builtin_fmaf(x, s.hi, x * s.lo); }
+
+// A quotient r that float32 has rounded onto a boundary between codes, moved to the side it came from by one unit in
+// its last place.  One that is not on the boundary is at least 2^-30 r away from it (x FMAX and boundary times a are
+// integers of 27 and 29 bits, times one power of two), one that is, is found to be within about 2^-46 r.
+__device__ __forceinline__ float settle(float r, float x, const Scale& s) {
+  const float off = __builtin_fmaf(x, s.hi, -r) + x * s.lo;
+  const int away = (__float_as_int(off) ^ __float_as_int(r)) < 0 ? -1 : 1;
+  const bool move = (__float_as_uint(r) & 0x7FFFFu) == 0 && fabsf(off) > fabsf(r) * 0x1p-38f;
+  return __int_as_float(__float_as_int(r) + (move ? away : 0));
+}
+
+// The four columns of a 4 x 4 square of bytes from its four rows.
+__device__ __forceinline__ void turn4(unsigned a, unsigned b, unsigned c, unsigned d, unsigned* w) {
+  const unsigned ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+  const unsigned cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  w[0] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
+  w[1] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
+  w[2] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100u);
+  w[3] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302u);
+}
+
+// Codes of four elements of a block.
+template <int DT, int FMT>
+__device__ __forceinline__ unsigned codes_of(float x0, float x1, float x2, float x3, const Scale& s) {
+  float r0 = scaled(x0, s), r1 = scaled(x1, s), r2 = scaled(x2, s), r3 = scaled(x3, s);
+  if constexpr (DT == 0) {
+    // boundaries have at most 5 significant bits, so the last 19 of the 23 stored ones are zero
+    const unsigned a = min(__float_as_uint(r0) << 13, __float_as_uint(r1) << 13);
+    const unsigned b = min(__float_as_uint(r2) << 13, __float_as_uint(r3) << 13);
+    if (min(a, b) == 0) {
+      r0 = settle(r0, x0, s);
+      r1 = settle(r1, x1, s);
+      r2 = settle(r2, x2, s);
+      r3 = settle(r3, x3, s);
+    }
+  }
+  return quant::codes4<FMT>(r0, r1, r2, r3);
+}
 
 // Bits of the magnitudes of 8 elements, as loaded: two 16-bit ones to a dword.
 template <int DT>
@@ -189,8 +230,6 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
     const Scale s = block_scale<FMT>(t, p.pow2);
 #pragma unroll
     for (int i = 0; i < RT; ++i) row[i] = s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) col[i] = s;
     if (tid == 0) {
       if constexpr (ROWS) p.S[((int64_t)l * p.Mb + tm) * p.Kb + kb] = s.scale;
       if constexpr (COLS) p.ST[((int64_t)l * p.Kb + kb) * p.Mb + tm] = s.scale;
@@ -245,29 +284,40 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
     }
   }
 
+  uint2 u[RT];  // codes of the rows
+  if constexpr (ROWS || SQUARE) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const v8f f = widen8<DT>(v[i]);
+      const Scale& s = row[SQUARE ? 0 : i];
+      u[i] = make_uint2(codes_of<DT, FMT>(f[0], f[1], f[2], f[3], s), codes_of<DT, FMT>(f[4], f[5], f[6], f[7], s));
+    }
+  }
   if constexpr (ROWS) {
     uint8_t* q = p.Q + ((int64_t)l * p.M + m0) * p.K16 + k;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int m = RT * g + i;
-      v8f f = widen8<DT>(v[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = scaled(f[j], row[i]);
-      const uint2 u = make_uint2(quant::codes4<FMT>(f[0], f[1], f[2], f[3]), quant::codes4<FMT>(f[4], f[5], f[6], f[7]));
-      if (m0 + m < p.M && k < p.K16) *reinterpret_cast<uint2*>(q + (int64_t)m * p.K16) = u;
+      if (m0 + m < p.M && k < p.K16) *reinterpret_cast<uint2*>(q + (int64_t)m * p.K16) = u[i];
     }
   }
   if constexpr (COLS) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const v8f f0 = widen8<DT>(v[4 * h]), f1 = widen8<DT>(v[4 * h + 1]), f2 = widen8<DT>(v[4 * h + 2]),
-                f3 = widen8<DT>(v[4 * h + 3]);
+      unsigned w[8];  // column j's codes of rows 4h .. 4h + 3
+      if constexpr (SQUARE) {
+        // the same codes, turned in registers
+        turn4(u[4 * h].x, u[4 * h + 1].x, u[4 * h + 2].x, u[4 * h + 3].x, w);
+        turn4(u[4 * h].y, u[4 * h + 1].y, u[4 * h + 2].y, u[4 * h + 3].y, w + 4);
+      } else {
+        const v8f f0 = widen8<DT>(v[4 * h]), f1 = widen8<DT>(v[4 * h + 1]), f2 = widen8<DT>(v[4 * h + 2]),
+                  f3 = widen8<DT>(v[4 * h + 3]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const Scale& s = col[j];
-        *reinterpret_cast<unsigned*>(tile + (8 * c + j) * kPitch + 8 * g + 4 * h) =
-            quant::codes4<FMT>(scaled(f0[j], s), scaled(f1[j], s), scaled(f2[j], s), scaled(f3[j], s));
+        for (int j = 0; j < 8; ++j) w[j] = codes_of<DT, FMT>(f0[j], f1[j], f2[j], f3[j], col[j]);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<unsigned*>(tile + (8 * c + j) * kPitch + 8 * g + 4 * h) = w[j];
     }
     __syncthreads();
     uint8_t* q = p.QT + ((int64_t)l * p.K + k0) * p.M16 + m0;

@@ -3,9 +3,9 @@
 TEST INFRASTRUCTURE ONLY (see the package docstring).
 
 ``quantize``: for a block with largest magnitude a, at least 448 * 2^-100, scale = float32(a / FMAX) and code =
-nearest(float32(x FMAX / a)), or with powers of two scale = 2^e with the smallest e that has FMAX * 2^e >= a and code =
-nearest(x 2^-e); the GPU must give the same bits.  ``gemm`` dequantises to float64 and
-contracts; it also returns S = sum |a||b|, which the tolerances scale with.
+nearest(x FMAX / a), or with powers of two scale = 2^e with the smallest e that has FMAX * 2^e >= a and code =
+nearest(x 2^-e), where nearest looks at the exact quotient; the GPU must give the same bits.  ``gemm`` dequantises to
+float64 and contracts; it also returns S = sum |a||b|, which the tolerances scale with.
 
 Pins (``tests/test_oracle_block128.py``): the scale rule against exact fractions, codes against a brute-force nearest
 search over the decode table, and the product against a scalar loop over blocks.
@@ -40,7 +40,7 @@ def _codes(x, amax, fmt, pow2):
     if pow2:
         q = x.astype(np.float64) * block_scales(amax, fmt, True)[1].astype(np.float64)
     else:
-        q = (x.astype(np.float64) * float(FMAX[fmt]) / a).astype(np.float32)
+        q = x.astype(np.float64) * float(FMAX[fmt]) / a  # exact product; boundaries between codes are 2^-30 away or hit
     return encode_rne(q, fmt)
 
 

@@ -338,3 +338,19 @@ def test_training_products_of_a_layer(lib):
         assert (np.abs(got.double().cpu().numpy() - ref) <= bound(s, ref, k + 16, torch.float32)).all()
     assert np.array_equal(code(wt)[:, :N], code(wq)[:, :K].T)
     assert decode(code(xq), 0).shape == (T, K)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("square", [False, True])
+def test_quantize_next_to_boundaries(lib, fmt, square):
+    """float32 values whose quotient float32 would round onto the boundary between two codes, and those exactly on it."""
+    from test_oracle_block128 import near_boundaries
+    x = near_boundaries(fmt, 512, 9, 128 if square else 1)
+    q, _, qt, _ = lib.block128_quantize(torch.from_numpy(x).cuda(), fmt, True, True, square)
+    rq, _, rqt, _ = B.quantize(x, fmt, True, True, square)
+    assert np.array_equal(q.view(torch.uint8).cpu().numpy(), rq)
+    assert np.array_equal(qt.view(torch.uint8).cpu().numpy(), rqt)
+    if not square:
+        xt = np.ascontiguousarray(x.T)
+        _, _, qt, _ = lib.block128_quantize(torch.from_numpy(xt).cuda(), fmt, False, True)
+        assert np.array_equal(qt.view(torch.uint8).cpu().numpy(), B.quantize(xt, fmt, False, True)[2])

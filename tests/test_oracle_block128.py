@@ -81,3 +81,30 @@ def test_product_against_a_loop_over_blocks(b_block):
             want += w * sum(x * y for x, y in zip(da[m, at], db[n, at]))
             mag += w * sum(abs(x * y) for x, y in zip(da[m, at], db[n, at]))
         assert abs(c[m, n] - want) <= 1e-12 * mag and abs(big[m, n] - mag) <= 1e-12 * mag
+
+
+def near_boundaries(fmt, rows, seed, block=1):
+    """(rows, 128) float32: in each row one largest magnitude a, the same in `block` rows, and 127 values that float32 has around boundary * a / FMAX,
+    boundaries being the midpoints of neighbouring codes."""
+    rng = np.random.default_rng(seed)
+    vals = np.unique(table(fmt)[table(fmt) >= 0])
+    mid = (vals[1:] + vals[:-1]) / 2
+    a = np.repeat(rng.uniform(1, 2, (rows // block, 1)).astype(np.float32), block, 0)
+    x = (rng.choice(mid, (rows, 128)) * a / B.FMAX[fmt]).astype(np.float32)
+    x = (x.view(np.int32) + rng.integers(-1, 2, x.shape, dtype=np.int32)).view(np.float32)
+    x *= rng.choice(np.float32([-1, 1]), x.shape)
+    x[:, 5] = a[:, 0]
+    return x
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_codes_next_to_boundaries(fmt):
+    x = near_boundaries(fmt, 6, 4)
+    q = decode(B.quantize(x, fmt)[0], fmt)
+    vals = [Fraction(float(v)) for v in np.unique(table(fmt))]
+    for row, codes in zip(x, q):
+        a = Fraction(float(np.abs(row).max()))
+        for v, c in zip(row, codes):
+            e = Fraction(float(v)) * Fraction(float(B.FMAX[fmt])) / a
+            best = min(abs(t - e) for t in vals)
+            assert abs(Fraction(float(c)) - e) == best
