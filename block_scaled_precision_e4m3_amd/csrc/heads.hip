@@ -64,6 +64,9 @@ int64_t backward_parts(int64_t T) {
   return std::max<int64_t>(2, std::min<int64_t>(cdiv(T, mxg::heads::kWaves), mxg::heads::kMaxParts));
 }
 
+// Those of the vector kernel, of which there are no more.
+int64_t vector_parts(int64_t T) { return std::min<int64_t>(backward_parts(T), mxg::heads::kBackParts); }
+
 // Whether every access of the vector kernels is a whole 16-byte one: 8-feature chunks of the head, of its rotary part
 // and of what lies before it, at aligned addresses.
 bool whole_chunks(const Params& p, int dtype, const Tensor* tensors[], int count) {
@@ -78,9 +81,11 @@ bool whole_chunks(const Params& p, int dtype, const Tensor* tensors[], int count
 
 template <int DT, int MODE, bool IN, bool OUT>
 void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
-  const dim3 g((unsigned)grid), b(mxg::heads::kThreads);
-  if constexpr (MODE == mxg::heads::kBackward) hipLaunchKernelGGL((mxg::heads::heads_backward_kernel<DT, IN, OUT>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((mxg::heads::heads_kernel<DT, MODE, IN, OUT>), g, b, 0, s, p);
+  const dim3 g((unsigned)grid);
+  if constexpr (MODE == mxg::heads::kBackward)
+    hipLaunchKernelGGL((mxg::heads::heads_backward_kernel<DT, IN, OUT>), g, dim3(64 * mxg::heads::kBackWaves), 0, s, p);
+  else
+    hipLaunchKernelGGL((mxg::heads::heads_kernel<DT, MODE, IN, OUT>), g, dim3(mxg::heads::kThreads), 0, s, p);
 }
 
 template <int DT, int MODE>
@@ -115,11 +120,11 @@ int launch(Params& p, int dtype, int cus, hipStream_t s) {
     p.gpw = (int)std::max<int64_t>(1, std::min<int64_t>({groups, MODE == mxg::heads::kRope ? 2 : 8, p.T * groups / (16LL * cus)}));
     if (MODE == mxg::heads::kBackward) {
       // workgroups in proportion to the groups of queries and keys, at least one of each that there is
-      const int64_t parts = backward_parts(p.T);
+      const int64_t parts = vector_parts(p.T);
       const int64_t q = p.groups[1] == 0 ? parts : std::min(parts - 1, std::max<int64_t>(1, cdiv(parts * p.groups[0], groups)));
       p.parts_q = p.groups[0] == 0 ? 0 : (int)q;
     }
-    grid = MODE == mxg::heads::kBackward ? backward_parts(p.T) : cdiv(p.T * cdiv(groups, p.gpw), mxg::heads::kWaves);
+    grid = MODE == mxg::heads::kBackward ? vector_parts(p.T) : cdiv(p.T * cdiv(groups, p.gpw), mxg::heads::kWaves);
     if (dtype == MXG_DT_F32) launch_heads<0, MODE>(p, grid, s);
     else if (dtype == MXG_DT_BF16) launch_heads<1, MODE>(p, grid, s);
     else launch_heads<2, MODE>(p, grid, s);

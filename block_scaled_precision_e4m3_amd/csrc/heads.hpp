@@ -21,9 +21,12 @@ namespace heads {
 constexpr int kWaves = 4;           // waves per workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxD = 1024;
-// Workgroups of the backward pass, each with a row of its workspace: two per compute unit (1024 46 us, 512 43 us at
-// 4001 tokens, 32 + 8 heads of 128)
-constexpr int kMaxParts = 512;
+// Workgroups of the backward pass, each with a row of its workspace, at most.  The vector kernel's are of 16 waves, one
+// to a compute unit: as many waves as four workgroups of four, and fewer sums to add up at the end (workgroups x waves,
+// 4001 tokens, 32 + 8 heads of 128, both kernels: 512 x 4 38.9 us, 1024 x 4 35.6, 512 x 8 35.4, 256 x 16 34.6, 512 x 16
+// 41.4).
+constexpr int kMaxParts = 512, kBackParts = 256;
+constexpr int kBackWaves = 16;
 
 constexpr int kRope = 0, kNorm = 1, kBackward = 2;
 
@@ -384,12 +387,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(Params p) {
 
 // Backward.  A workgroup works on the queries only or on the keys only (the first p.parts_q on queries), so that a
 // lane holds one weight and one weight gradient for each of its features, to the end.  A work item is one token and
-// one group of its heads.  More waves hide the loads better than more loads per wave: two groups at a time 47 us,
-// asking for the next item ahead 45 us, neither 43 us (4001 tokens, 32 + 8 heads of 128, both kernels).
+// one group of its heads.  More waves hide the loads better than more loads per wave; asking for the next item's
+// position ahead changes nothing.  4001 tokens of 32 + 8 heads of 128: 30.6 us, 4.05 TB/s, besides 3.3 for the sums;
+// the bound is memory, its latency more than its rate, at five items to a wave.
 template <int DT, bool IN, bool OUT>
-__global__ __launch_bounds__(kThreads) void heads_backward_kernel(Params p) {
+__global__ __launch_bounds__(64 * kBackWaves) void heads_backward_kernel(Params p) {
   using E = elem_t<DT>;
-  __shared__ float lds[kWaves][kMaxD];
+  __shared__ float lds[kBackWaves][kMaxD];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int k = (int)blockIdx.x < p.parts_q ? 0 : 1;
@@ -400,12 +404,12 @@ __global__ __launch_bounds__(kThreads) void heads_backward_kernel(Params p) {
   const bool mine = 16 * q < p.D;
   const Lane l = lane_of(p, q, IN, OUT);
   const int per = p.groups[k];  // items per token
-  const int64_t items = p.T * per, step = (int64_t)wgs * kWaves;
+  const int64_t items = p.T * per, step = (int64_t)wgs * kBackWaves;
   Two w, dw;
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw.a[i] = dw.b[i] = w.a[i] = w.b[i] = 0.f;
   if (mine) w = split<IN>(weights8<DT>(p, k, l.in0), weights8<DT>(p, k, l.in1));
-  for (int64_t it = (int64_t)wg * kWaves + wave; it < items; it += step) {
+  for (int64_t it = (int64_t)wg * kBackWaves + wave; it < items; it += step) {
     const int64_t t = it / per;
     const int h = (int)(it - t * per) * p.rpw + sub;
     const bool live = mine && h < H;
@@ -463,10 +467,10 @@ __global__ __launch_bounds__(kThreads) void heads_backward_kernel(Params p) {
     }
   }
   __syncthreads();
-  for (int f = threadIdx.x; f < p.D; f += kThreads) {
+  for (int f = threadIdx.x; f < p.D; f += 64 * kBackWaves) {
     float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) sum += lds[v][f];
+    for (int v = 0; v < kBackWaves; ++v) sum += lds[v][f];
     p.parts[(int64_t)blockIdx.x * p.D + f] = sum;
   }
 }
