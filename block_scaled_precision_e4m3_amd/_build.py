@@ -18,8 +18,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mxgemm.hip", "launch_t256_bf16_f32.h
                                            "launch_t128_bf16_f32.hip", "launch_t128_bf16_c16.hip",
                                            "launch_t256_proj.hip", "launch_fp8.hip", "launch_t256_mj.hip",
                                            "launch_t128_mj.hip", "probes.hip", "block128.hip", "block128_tile256.hip",
-                                           "block128_tile128.hip", "block128_tile64.hip", "block128_exact.hip",
-                                           "block128_rows.hip", "heads.hip")]
+                                           "block128_tile128x256.hip", "block128_tile128.hip",
+                                           "block128_tile64x128.hip", "block128_tile64.hip",
+                                           "block128_exact.hip", "block128_rows.hip", "heads.hip")]
 LIB = os.path.join(PKG_DIR, "libmxgemm.so")
 # The torch wrappers' short way into the library (host code only, against torch's headers).
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")

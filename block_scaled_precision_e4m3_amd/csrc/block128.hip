@@ -95,14 +95,20 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
 // Which kernel, tile and division of K.  rows: a kernel for up to 16 rows of A.
 //
 // Tiles: the time in microseconds of a tile size is taken as
-//   rounds of work items over the compute units x (blocks of K x block + end)
-// and, where K is divided, the second kernel that adds the parts up.  block and
-// end were measured on MI355X, one size forced at a time: 16-bit C, tiles of 64
-// (300x2048x7168: 15.4 us), 128 (2048x2048x2048: 13.2 us, with 64 20.4 us and
-// with 256 30.8 us) and 256 (4096x4096x4096: 63 us, with 128 73 us); float32 C,
-// 64 (300x1024x4096: 15.3 us), 128 (2048x2048x2048: 22 us, with 64 30 us) and
-// 256 x 128 (4096x4096x4096: 129 us, with 128 135 us).  K is divided only where
-// tiles leave compute units idle: 64x1024x7168 in 4 parts 10.3 us, in one 14.8.
+//   rounds of work items over the compute units x (blocks of K x block x (0.7 + 0.3 x busy) + end)
+// where busy is the share of compute units with work (one that shares the chip
+// and its power with idle ones is faster), and, where K is divided, the second
+// kernel that adds the parts up.  block and end were measured on MI355X, one
+// size forced at a time.  16-bit C, the best and its neighbours:
+//   128x7168x2048     64 x 64 7.1     64 x 128 8.4   128 x 128 11.1
+//   512x4096x7168     64 x 128 21.7   64 x 64 27.7   128 x 128 28.6
+//   1024x4096x7168    128 x 128 36.5  64 x 128 40.9  128 x 256 54.1
+//   2048x4096x4096    128 x 256 38.6  128 x 128 46.6 256 x 256 48.5
+//   4096x4096x4096    256 x 256 63.3  128 x 256 74.9 128 x 128 81.5
+// float32 C: 64 (300x1024x4096: 15.3 us), 128 (2048x2048x2048: 22 us, with 64
+// 30 us) and 256 x 128 (4096x4096x4096: 129 us, with 128 135 us).  K is divided
+// only where tiles leave compute units idle: 64x1024x7168 in 4 parts 10.3 us,
+// in one 14.8.
 struct Choice {
   int rows;                // columns per workgroup of the rows kernel, 0: tiles
   int bm, bn, kb, splits;  // tile; blocks of K per step; parts of K
@@ -116,19 +122,26 @@ Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
   if (M <= 16) return {L * cdiv(N, 32) >= kUnits * 3 / 4 ? 32 : 16, 16, 0, 1, 1};
   struct Size {
     int bm, bn, kb;
+    bool divides;  // its kernel can take part of K
     double block, end;
   };
-  static constexpr Size kSizes[2][3] = {{{64, 64, 2, 0.24, 0.5}, {128, 128, 2, 0.6, 1.0}, {256, 256, 1, 1.95, 3.0}},
-                                        {{64, 64, 2, 0.40, 0.7}, {128, 128, 2, 1.05, 1.5}, {256, 128, 1, 1.9, 2.0}}};
+  static constexpr Size kSizes[2][5] = {{{64, 64, 2, true, 0.215, 0.5},
+                                         {64, 128, 2, true, 0.335, 0.7},
+                                         {128, 128, 1, false, 0.64, 1.0},
+                                         {128, 256, 1, false, 1.08, 2.0},
+                                         {256, 256, 1, false, 1.8, 3.0}},
+                                        {{64, 64, 2, true, 0.40, 0.7}, {128, 128, 2, true, 1.05, 1.5}, {256, 128, 1, false, 1.9, 2.0}}};
   const int64_t blocks = cdiv(K, 128);
   Choice best{};
   double best_time = 0;
   for (const Size& t : kSizes[exact]) {
+    if (t.bm == 0) break;
     const int64_t tiles = L * cdiv(M, t.bm) * cdiv(N, t.bn), steps = cdiv(blocks, t.kb);
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (splits > 1 && (t.bm == 256 || splits > steps || tiles * (splits - 1) >= kUnits)) break;
+      if (splits > 1 && (!t.divides || splits > steps || tiles * (splits - 1) >= kUnits)) break;
       const int64_t per = cdiv(steps, splits), parts = cdiv(steps, per);
-      double time = (double)cdiv(tiles * parts, kUnits) * (per * t.kb * t.block + t.end);
+      const double busy = std::min<double>(tiles * parts, kUnits) / kUnits;
+      double time = (double)cdiv(tiles * parts, kUnits) * (per * t.kb * t.block * (0.7 + 0.3 * busy) + t.end);
       if (parts > 1) time += 4.0 + parts * L * M * N * 8 / 3e6;  // written and read at 3 TB/s
       if (best.bm == 0 || time < best_time) {
         best = {0, t.bm, t.bn, t.kb, (int)parts};
@@ -277,7 +290,11 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
     const auto f = ch.bm == 256 ? mxg::b128::launch_exact256 : ch.bm == 128 ? mxg::b128::launch_exact128 : mxg::b128::launch_exact64;
     e = f(p, a_fmt, b_fmt, grid, s);
   } else {
-    const auto f = ch.bm == 256 ? mxg::b128::launch_tile256 : ch.bm == 128 ? mxg::b128::launch_tile128 : mxg::b128::launch_tile64;
+    const auto f = ch.bm == 256   ? mxg::b128::launch_tile256
+                   : ch.bn == 256 ? mxg::b128::launch_tile128x256
+                   : ch.bm == 128 ? mxg::b128::launch_tile128
+                   : ch.bn == 128 ? mxg::b128::launch_tile64x128
+                                  : mxg::b128::launch_tile64;
     e = f(p, a_fmt, b_fmt, c_dtype, grid, s);
   }
   if (e == hipSuccess && p.splits > 1) {

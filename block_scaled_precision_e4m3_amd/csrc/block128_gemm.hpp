@@ -37,11 +37,11 @@ struct GemmParams {
 constexpr unsigned kOob = 0x80000000u;  // an offset past every resource: reads as zero, is not stored
 
 // A tile of BM x BN outputs by WM x WN waves, operands in a ring of NST stages of KB blocks of K each, moved by the
-// same waves (NP = 0) or by NP more that do nothing else.
-template <int BM, int BN, int WM, int WN, int NST, int KB, int NP = 0>
+// same waves (NP = 0) or by NP more that do nothing else.  PARTS: the kernel can take part of K.
+template <int BM, int BN, int WM, int WN, int NST, int KB, int NP = 0, bool PARTS = (NP > 0)>
 struct TileShape {
   static constexpr int kBM = BM, kBN = BN, kWaves = WM * WN, kWn = WN, kStages = NST, kKB = KB;
-  static constexpr bool kParts = NP > 0;                 // K may be divided (the host's rule)
+  static constexpr bool kParts = PARTS;
   static constexpr int kProducers = NP, kDmaWaves = NP ? NP : kWaves, kAllWaves = kWaves + NP;
   static constexpr int kTM = BM / WM, kTN = BN / WN;     // a wave's outputs
   static constexpr int kOffB = BM * 128, kOffSA = kOffB + BN * 128, kOffSB = kOffSA + BM * 4;
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
     const uint8_t *a_lo = st + a_off, *a_hi = st + (a_off ^ 64), *b_lo = st + b_off, *b_hi = st + (b_off ^ 64);
     const float* ssa = reinterpret_cast<const float*>(st + T::kOffSA) + a_row;
     const float* ssb = reinterpret_cast<const float*>(st + T::kOffSB) + (BROWS ? T::kTN * wn + 8 * g : T::kTN * wn / 128);
-    // row t of MFMAs is row t % kMt of block t / kMt; A's fragments come three rows ahead of their use
+    // row t of MFMAs is row t % kMt of block t / kMt; A's fragments are read two rows ahead of their use
     auto a_frag = [&](int t) { return frag(a_lo, a_hi, t / kMt * T::kBlock + 2048 * (t % kMt)); };
     v8i b[T::kKB][kNt], a[3];
     a[0] = a_frag(0);
@@ -324,35 +324,40 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] = zero;
     }
-    v4f part[2][kNt];
-    auto fold = [&](int t) {
+    v4f part[kNt];
+    auto fold = [&](int t, int nt) {
       const int kb = t / kMt, mt = t % kMt;
-      const v4f* pt = part[t & 1];
+      const v4f pt = part[nt];
       const float s0 = BROWS ? sa[kb][mt] : sa[kb][mt] * sb[kb][0][0];
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[mt][nt][e] = __builtin_fmaf(pt[nt][e], BROWS ? s0 * sb[kb][nt][e] : s0, acc[mt][nt][e]);
-        // keeps the multiply-adds here: moved past the step's branches, all parts would have to be kept
-        asm volatile("" : "+v"(acc[mt][nt]));
-      }
+      for (int e = 0; e < 4; ++e) acc[mt][nt][e] = __builtin_fmaf(pt[e], BROWS ? s0 * sb[kb][nt][e] : s0, acc[mt][nt][e]);
+      // keeps the multiply-adds here: moved past the step's branches, all parts would have to be kept
+      asm volatile("" : "+v"(acc[mt][nt]));
     };
-    // the stage the step before used takes the DMA that is furthest ahead, issued between the rows of MFMAs
+    // Each MFMA's result goes into the accumulators right before the MFMA of the next row that overwrites it, one
+    // between two MFMAs: a wave that issues a row's MFMAs and then all its multiply-adds leaves the matrix core idle
+    // under most of them (8192 x 24576 x 1536: 319 -> 295 us, 1024 x 4096 x 7168: 41.3 -> 36.5 us).
+    // The stage the step before used takes the DMA that is furthest ahead, issued between the rows of MFMAs.
     if constexpr (T::kProducers == 0) in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
 #pragma unroll
     for (int t = 0; t < kRows; ++t) {
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-        part[t & 1][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[t / kMt][nt], a[t % 3], zero, FB, FA, 0, 0, 0, 0);
-      if (t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
-      if (t > 0) fold(t - 1);
+      for (int nt = 0; nt < kNt; ++nt) {
+        if (t > 0) fold(t - 1, nt);
+        part[nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[t / kMt][nt], a[t % 3], zero, FB, FA, 0, 0, 0, 0);
+        if (T::kProducers > 0 && nt == 0 && t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (T::kProducers == 0) {
+        if (t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
 #pragma unroll
-      for (int q = 0; q < T::kIssued; ++q)
-        if (T::kProducers == 0 && q / kPerRow == t) in.one(q);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int q = 0; q < T::kIssued; ++q)
+          if (q / kPerRow == t) in.one(q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    fold(kRows - 1);
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) fold(kRows - 1, nt);
     if constexpr (T::kProducers == 0) in.end();
     stage = stage + 1 == T::kStages ? 0 : stage + 1;
 

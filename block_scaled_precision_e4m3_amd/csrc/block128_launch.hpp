@@ -8,18 +8,22 @@
 namespace mxg {
 namespace b128 {
 
-// The tile shapes.  16-bit C: the eight waves of a 256 x 256 tile hold all registers and move the operands
-// themselves; the smaller tiles, whose steps are short, leave that to four more waves.  float32 C: the accumulators
-// and the block's sums together allow 64 x 64 outputs per wave.
+// The tile shapes.  16-bit C: the eight waves of a 256 x 256 or 128 x 256 tile hold most registers and move the
+// operands themselves; the smaller tiles, whose steps are short, leave that to four more waves.  float32 C: the
+// accumulators and the block's sums together allow 64 x 64 outputs per wave.
 using Tile256 = TileShape<256, 256, 2, 4, 2, 1>;
-using Tile128 = TileShape<128, 128, 2, 2, 2, 2, 4>;
-using Tile64 = TileShape<64, 64, 2, 2, 4, 2, 4>;
+using Tile128x256 = TileShape<128, 256, 2, 4, 3, 1>;
+using Tile128 = TileShape<128, 128, 2, 2, 3, 1, 4, false>;
+using Tile64x128 = TileShape<64, 128, 2, 2, 3, 2, 4>;
+using Tile64 = TileShape<64, 64, 2, 2, 3, 2, 4>;
 using Exact256 = TileShape<256, 128, 4, 2, 2, 1>;
-using Exact128 = Tile128;
-using Exact64 = Tile64;
+using Exact128 = TileShape<128, 128, 2, 2, 2, 2, 4>;
+using Exact64 = TileShape<64, 64, 2, 2, 4, 2, 4>;
 
 hipError_t launch_tile256(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
+hipError_t launch_tile128x256(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
+hipError_t launch_tile64x128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile64(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_exact256(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 hipError_t launch_exact128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);

@@ -201,6 +201,19 @@ def test_gemm_tiles_and_parts(lib, m, n, k):
     check_gemm(lib, m, n, k, 0, 1, 1, torch.float32, c0=c0, seed=4)
 
 
+# a wide and a flat tile between those sizes, in one and two rounds, K divided, and the largest tile with 16-byte stores
+BETWEEN = [(500, 3000, 2064), (260, 1000, 24592), (2001, 4001, 400), (1000, 7904, 272), (1030, 4104, 1040),
+           (1300, 9000, 272)]
+
+
+@pytest.mark.parametrize("m,n,k", BETWEEN)
+def test_gemm_tiles_between(lib, m, n, k):
+    print(f"gemm {m}x{n}x{k}", flush=True)
+    for dtype in (torch.bfloat16, torch.float16):
+        check_gemm(lib, m, n, k, 0, 1, 128, dtype, seed=m)
+        check_gemm(lib, m, n, k, 1, 0, 1, dtype, seed=n)
+
+
 def test_gemm_workspace(lib):
     """K is divided for few tiles and a long K; a short or missing workspace is refused."""
     need = lib._lib.mxgemm_block128_workspace_bytes(64, 512, 7168, 1, lib.MXG_DT_BF16)
