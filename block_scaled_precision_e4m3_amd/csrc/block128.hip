@@ -105,10 +105,13 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
 //   1024x4096x7168    128 x 128 36.5  64 x 128 40.9  128 x 256 54.1
 //   2048x4096x4096    128 x 256 38.6  128 x 128 46.6 256 x 256 48.5
 //   4096x4096x4096    256 x 256 63.3  128 x 256 74.9 128 x 128 81.5
-// float32 C: 64 (300x1024x4096: 15.3 us), 128 (2048x2048x2048: 22 us, with 64
-// 30 us) and 256 x 128 (4096x4096x4096: 129 us, with 128 135 us).  K is divided
-// only where tiles leave compute units idle: 64x1024x7168 in 4 parts 10.3 us,
-// in one 14.8.
+// float32 C:
+//   128x7168x2048     64 x 64 10.1    64 x 128 12.4  128 x 128 17.0
+//   512x4096x7168     64 x 128 36.4   64 x 64 44.1   128 x 128 47.5
+//   4000x7168x2048    128 x 128 115.4 128 x 256 121.3 64 x 128 139.9
+//   2048x4096x4096    128 x 256 61.6  128 x 128 64.1 64 x 128 77.1
+// K is divided only where tiles leave compute units idle: 64x1024x7168 in 4
+// parts 10.3 us, in one 14.8.
 struct Choice {
   int rows;                // columns per workgroup of the rows kernel, 0: tiles
   int bm, bn, kb, splits;  // tile; blocks of K per step; parts of K
@@ -130,7 +133,10 @@ Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
                                          {128, 128, 1, false, 0.64, 1.0},
                                          {128, 256, 1, false, 1.08, 2.0},
                                          {256, 256, 1, false, 1.8, 3.0}},
-                                        {{64, 64, 2, true, 0.40, 0.7}, {128, 128, 2, true, 1.05, 1.5}, {256, 128, 1, false, 1.9, 2.0}}};
+                                        {{64, 64, 2, true, 0.355, 0.8},
+                                         {64, 128, 2, true, 0.585, 1.0},
+                                         {128, 128, 2, true, 0.97, 1.3},
+                                         {128, 256, 1, false, 1.85, 2.0}}};
   const int64_t blocks = cdiv(K, 128);
   Choice best{};
   double best_time = 0;
@@ -287,7 +293,10 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
   }
   hipError_t e;
   if (exact) {
-    const auto f = ch.bm == 256 ? mxg::b128::launch_exact256 : ch.bm == 128 ? mxg::b128::launch_exact128 : mxg::b128::launch_exact64;
+    const auto f = ch.bn == 256   ? mxg::b128::launch_exact128x256
+                   : ch.bm == 128 ? mxg::b128::launch_exact128
+                   : ch.bn == 128 ? mxg::b128::launch_exact64x128
+                                  : mxg::b128::launch_exact64;
     e = f(p, a_fmt, b_fmt, grid, s);
   } else {
     const auto f = ch.bm == 256   ? mxg::b128::launch_tile256

@@ -16,17 +16,19 @@ using Tile128x256 = TileShape<128, 256, 2, 4, 3, 1>;
 using Tile128 = TileShape<128, 128, 2, 2, 3, 1, 4, false>;
 using Tile64x128 = TileShape<64, 128, 2, 2, 3, 2, 4>;
 using Tile64 = TileShape<64, 64, 2, 2, 3, 2, 4>;
-using Exact256 = TileShape<256, 128, 4, 2, 2, 1>;
+using Exact128x256 = TileShape<128, 256, 2, 4, 2, 1>;
 using Exact128 = TileShape<128, 128, 2, 2, 2, 2, 4>;
-using Exact64 = TileShape<64, 64, 2, 2, 4, 2, 4>;
+using Exact64x128 = TileShape<64, 128, 2, 2, 3, 2, 4>;
+using Exact64 = TileShape<64, 64, 2, 2, 3, 2, 4>;
 
 hipError_t launch_tile256(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile128x256(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile64x128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
 hipError_t launch_tile64(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s);
-hipError_t launch_exact256(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
+hipError_t launch_exact128x256(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 hipError_t launch_exact128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
+hipError_t launch_exact64x128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 hipError_t launch_exact64(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 // up to 16 rows; p.tilesN counts groups of `cols` (16 or 32) columns
 hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int cols, int64_t grid, hipStream_t s);

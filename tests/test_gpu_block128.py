@@ -212,6 +212,12 @@ def test_gemm_tiles_between(lib, m, n, k):
     for dtype in (torch.bfloat16, torch.float16):
         check_gemm(lib, m, n, k, 0, 1, 128, dtype, seed=m)
         check_gemm(lib, m, n, k, 1, 0, 1, dtype, seed=n)
+    check_gemm(lib, m, n, k, 1, 0, 1, torch.float32, seed=n)
+
+
+def test_gemm_long_sum(lib):
+    """K long enough for the 128 x 128 tiles of a float32 C to take parts of it."""
+    check_gemm(lib, 1000, 1000, 32784, 0, 1, 1, torch.float32, seed=1)
 
 
 def test_gemm_workspace(lib):
