@@ -2,9 +2,10 @@
 
     x (T, hidden) -> codes in blocks of 1 x 128
                   -> product with the weight's codes (blocks of 128 x 128)      block128_quantize, block128_gemm
-                  -> q, k: root-mean-square norm and rotary positions; v as is  qk_norm_rope
+                  -> q, k: root-mean-square norm and rotary positions,          qk_norm_rope,
+                     or only the positions; v as is                             rope
 
-The backward pass turns the heads' gradients into the projection's (qk_norm_rope_backward), quantises those once for
+The backward pass turns the heads' gradients into the projection's (qk_norm_rope_backward, or rope's transpose), quantises those once for
 both directions and runs two more products: the input's gradient over the weight's transposed codes, and the weight's
 gradient, float32, over the tokens.
 
@@ -22,18 +23,20 @@ import block_scaled_precision_e4m3_amd as mx  # noqa: E402
 
 
 class AttentionInput(torch.nn.Module):
-    """q (T, heads, D), k (T, kv_heads, D) and v (T, kv_heads, D) of hidden states x (T, hidden), bfloat16.
+    """q (T, heads, D), k (T, kv_heads, D) and v (T, kv_heads, D) of hidden states x (T, hidden), bfloat16; norm: q and k
+    are normed per head before the positions turn them.
 
     weight ((heads + 2 kv_heads) D, hidden) is kept in bfloat16 and in codes of both directions; requantise() after it
     has changed."""
 
-    def __init__(self, hidden, heads, kv_heads, head_dim, max_positions, rot=None, eps=1e-6, device="cuda"):
+    def __init__(self, hidden, heads, kv_heads, head_dim, max_positions, rot=None, norm=True, eps=1e-6,
+                 device="cuda"):
         super().__init__()
         self.heads, self.kv_heads, self.head_dim, self.eps = heads, kv_heads, head_dim, eps
         n = (heads + 2 * kv_heads) * head_dim
         self.weight = torch.nn.Parameter((torch.randn(n, hidden, device=device) / hidden ** 0.5).bfloat16())
-        self.q_norm = torch.nn.Parameter(torch.ones(head_dim, device=device))
-        self.k_norm = torch.nn.Parameter(torch.ones(head_dim, device=device))
+        self.q_norm = torch.nn.Parameter(torch.ones(head_dim, device=device)) if norm else None
+        self.k_norm = torch.nn.Parameter(torch.ones(head_dim, device=device)) if norm else None
         self.cos, self.sin = mx.rope_table(max_positions, rot or head_dim, device=device)
         self.requantise()
 
@@ -46,13 +49,26 @@ class AttentionInput(torch.nn.Module):
         y = y.view(-1, self.heads + 2 * self.kv_heads, self.head_dim)
         return y.split((self.heads, self.kv_heads, self.kv_heads), 1)
 
+    def positioned(self, q, k, positions):
+        if self.q_norm is None:
+            return mx.rope(q, self.cos, self.sin, positions), mx.rope(k, self.cos, self.sin, positions)
+        return mx.qk_norm_rope(q, k, self.q_norm, self.k_norm, self.cos, self.sin, positions, eps=self.eps)
+
+    def positioned_backward(self, dq, dk, q, k, q_norm, k_norm, positions, out):
+        """Gradients of q and k into out; returns the norm weights'."""
+        if q_norm is None:
+            mx.rope(dq, self.cos, self.sin, positions, transpose=True, out=out[0])
+            mx.rope(dk, self.cos, self.sin, positions, transpose=True, out=out[1])
+            return None, None
+        return mx.qk_norm_rope_backward(dq, dk, q, k, q_norm, k_norm, self.cos, self.sin, positions, eps=self.eps,
+                                        out=out)[2:]
+
     def forward(self, x, positions=None):
         if torch.is_grad_enabled():
             return _AttentionInput.apply(x, self.weight, self.q_norm, self.k_norm, self, positions)
         xq, xs, _, _ = mx.block128_quantize(x)
         q, k, v = self.split(mx.block128_gemm(xq, xs, self.codes[0], self.codes[1]))
-        q, k = mx.qk_norm_rope(q, k, self.q_norm, self.k_norm, self.cos, self.sin, positions, eps=self.eps)
-        return q, k, v
+        return *self.positioned(q, k, positions), v
 
 
 class _AttentionInput(torch.autograd.Function):
@@ -63,8 +79,8 @@ class _AttentionInput(torch.autograd.Function):
         q, k, v = layer.split(y)
         ctx.layer, ctx.positions = layer, positions
         ctx.save_for_backward(y, xqt, xst, q_norm, k_norm, *layer.codes[2:])
-        qo, ko = mx.qk_norm_rope(q, k, q_norm, k_norm, layer.cos, layer.sin, positions, eps=layer.eps)
-        return qo, ko, v.clone()  # a view of y may not leave: y is kept as it is for the backward pass
+        # a view of y may not leave: y is kept as it is for the backward pass
+        return *layer.positioned(q, k, positions), v.clone()
 
     @staticmethod
     def backward(ctx, dq, dk, dv):
@@ -74,8 +90,7 @@ class _AttentionInput(torch.autograd.Function):
         dq, dk = dq.contiguous(), dk.contiguous()  # an expanded gradient (of a sum) has no features side by side
         dy = torch.empty_like(y)
         gq, gk, gv = layer.split(dy)
-        _, _, dqn, dkn = mx.qk_norm_rope_backward(dq, dk, q, k, q_norm, k_norm, layer.cos, layer.sin, ctx.positions,
-                                                  eps=layer.eps, out=(gq, gk))
+        dqn, dkn = layer.positioned_backward(dq, dk, q, k, q_norm, k_norm, ctx.positions, (gq, gk))
         gv.copy_(dv)
         g, gs, gt, gts = mx.block128_quantize(dy, cols=True)
         dx = mx.block128_gemm(g, gs, wt, wts)
@@ -91,35 +106,36 @@ def plain(layer, x, weight, q_norm, k_norm, positions):
     c, s = layer.cos[p][:, None], layer.sin[p][:, None]
 
     def one(h, w):
-        h = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + layer.eps) * w
+        if w is not None:
+            h = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + layer.eps) * w
         a, b = h[..., :rot // 2], h[..., rot // 2:rot]
         return torch.cat((a * c - b * s, b * c + a * s, h[..., rot:]), -1)
     return one(q, q_norm), one(k, k_norm), v
 
 
-def check(hidden=1024, heads=8, kv_heads=2, head_dim=128, tokens=300, seed=0):
+def check(hidden=1024, heads=8, kv_heads=2, head_dim=128, tokens=300, norm=True, seed=0):
     """Relative errors (Frobenius) of a training step's outputs and gradients, and of a decode step's outputs, against
     float32 torch.  The codes carry 4 significant bits (relative error at most 1/16 per value, about 1/40 in the mean
     square), so a product of two such operands is off by about 1/28."""
     torch.manual_seed(seed)
-    layer = AttentionInput(hidden, heads, kv_heads, head_dim, 4096)
+    layer = AttentionInput(hidden, heads, kv_heads, head_dim, 4096, norm=norm)
     x = torch.randn(tokens, hidden, device="cuda").bfloat16().requires_grad_()
     out = layer(x)
     grads = [torch.randn_like(o) for o in out]
     torch.autograd.backward(out, grads)
-    ref_in = [t.detach().float().requires_grad_() for t in (x, layer.weight, layer.q_norm, layer.k_norm)]
+    mine = (x, layer.weight) + ((layer.q_norm, layer.k_norm) if norm else ())
+    ref_in = [t.detach().float().requires_grad_() for t in mine] + ([] if norm else [None, None])
     ref = plain(layer, *ref_in, None)
     torch.autograd.backward(ref, [g.float() for g in grads])
 
     def off(a, b):
         return ((a.detach().float() - b.detach()).norm() / b.detach().norm()).item()
     errors = {n: off(a, b) for n, a, b in zip(("q", "k", "v"), out, ref)}
-    mine = (x, layer.weight, layer.q_norm, layer.k_norm)
     errors.update({n: off(a.grad, b.grad) for n, a, b in zip(("dx", "dweight", "dq_norm", "dk_norm"), mine, ref_in)})
     at = torch.tensor([1000, 17, 4095], device="cuda")
     with torch.no_grad():
         step = layer(x[:3], at)
-        ref = plain(layer, *[t.detach() for t in (ref_in[0][:3], *ref_in[1:])], at)
+        ref = plain(layer, *[t if t is None else t.detach() for t in (ref_in[0][:3], *ref_in[1:])], at)
     errors.update({"decode " + n: off(a, b) for n, a, b in zip(("q", "k", "v"), step, ref)})
     return errors
 

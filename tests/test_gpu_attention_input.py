@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
-@pytest.mark.parametrize("sizes", [{}, dict(hidden=528, heads=3, kv_heads=1, head_dim=64, tokens=131),
+@pytest.mark.parametrize("sizes", [{}, dict(norm=False), dict(hidden=144, heads=5, kv_heads=5, head_dim=80, tokens=77, norm=False),
+                                   dict(hidden=528, heads=3, kv_heads=1, head_dim=64, tokens=131),
                                    dict(hidden=256, heads=4, kv_heads=4, head_dim=192, tokens=5)])
 def test_attention_input(sizes):
     """Each operand's codes are off by at most 1/16 of a value, in root mean square by no more than 1/16 / sqrt(3) (uniform
