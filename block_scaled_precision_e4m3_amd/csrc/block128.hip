@@ -41,35 +41,31 @@ int check_quantize(int64_t ldx, int64_t M, int64_t K, int64_t L, int dt, int fmt
   return MXG_OK;
 }
 
-template <int DT, int FMT, int RT, bool VEC>
+template <int DT, int FMT, int RT>
 void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, int64_t grid, hipStream_t s) {
   using namespace mxg::b128;
   const dim3 g((unsigned)grid), b(kQThreads);
   if constexpr (RT == 8) {
-    if (square && rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, true, true>), g, b, 0, s, p);
-    else if (square && rows) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, false, true>), g, b, 0, s, p);
-    else if (square) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, false, true, true>), g, b, 0, s, p);
-    else if (rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, true, false>), g, b, 0, s, p);
-    else if (cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, false, true, false>), g, b, 0, s, p);
-    else hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, false, false>), g, b, 0, s, p);
+    if (square && rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, true, true>), g, b, 0, s, p);
+    else if (square && rows) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, false, true>), g, b, 0, s, p);
+    else if (square) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, false, true, true>), g, b, 0, s, p);
+    else if (rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, true, false>), g, b, 0, s, p);
+    else if (cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, false, true, false>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, false, false>), g, b, 0, s, p);
   } else {
-    hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, VEC, true, false, false>), g, b, 0, s, p);
+    hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, false, false>), g, b, 0, s, p);
   }
 }
 
 template <int DT>
-void launch_quantize(const QuantParams& p, int fmt, bool vec, bool few, bool rows, bool cols, bool square, int64_t grid,
+void launch_quantize(const QuantParams& p, int fmt, bool few, bool rows, bool cols, bool square, int64_t grid,
                      hipStream_t s) {
   if (fmt == MXG_FMT_E4M3) {
-    if (few && vec) launch_quantize<DT, 0, 1, true>(p, rows, cols, square, grid, s);
-    else if (few) launch_quantize<DT, 0, 1, false>(p, rows, cols, square, grid, s);
-    else if (vec) launch_quantize<DT, 0, 8, true>(p, rows, cols, square, grid, s);
-    else launch_quantize<DT, 0, 8, false>(p, rows, cols, square, grid, s);
+    if (few) launch_quantize<DT, 0, 1>(p, rows, cols, square, grid, s);
+    else launch_quantize<DT, 0, 8>(p, rows, cols, square, grid, s);
   } else {
-    if (few && vec) launch_quantize<DT, 1, 1, true>(p, rows, cols, square, grid, s);
-    else if (few) launch_quantize<DT, 1, 1, false>(p, rows, cols, square, grid, s);
-    else if (vec) launch_quantize<DT, 1, 8, true>(p, rows, cols, square, grid, s);
-    else launch_quantize<DT, 1, 8, false>(p, rows, cols, square, grid, s);
+    if (few) launch_quantize<DT, 1, 1>(p, rows, cols, square, grid, s);
+    else launch_quantize<DT, 1, 8>(p, rows, cols, square, grid, s);
   }
 }
 
@@ -198,15 +194,14 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
   p.Kb = (int)cdiv(K, 128);
   p.pow2 = (flags & MXG_QUANT_POW2) != 0;
   // whole 8-element chunks at 16-byte addresses
-  const bool vec = aligned16(X) && K % 8 == 0 && ldx % 8 == 0;
   // rows alone, and too few of them for 128-row tiles to fill the chip: 16 rows to a workgroup
   const bool few = rows && !cols && !square && L * p.Mb * p.Kb < 4LL * cus;
   p.tiles_m = few ? (int)cdiv(M, 16) : p.Mb;
   const int64_t grid = L * p.tiles_m * p.Kb;
   hipStream_t s = (hipStream_t)stream;
-  if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, vec, few, rows, cols, square, grid, s);
-  else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, vec, few, rows, cols, square, grid, s);
-  else launch_quantize<2>(p, fmt, vec, few, rows, cols, square, grid, s);
+  if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, few, rows, cols, square, grid, s);
+  else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, few, rows, cols, square, grid, s);
+  else launch_quantize<2>(p, fmt, few, rows, cols, square, grid, s);
   return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 

@@ -151,31 +151,33 @@ __device__ __forceinline__ unsigned mag_bits(unsigned m) {
   else return half_bits<DT>(max(m & 0xFFFFu, m >> 16));
 }
 
-// 8 elements at p, those at or past `valid` read as zero.
-template <int DT, bool VEC>
+// 8 elements from any address an element may have: gfx950 takes 16-byte loads at any alignment, an aligned one as fast.
+template <int DT>
+struct __attribute__((packed, aligned(DT == 0 ? 4 : 2))) AnyChunk {
+  Raw8<DT> v;
+};
+// 8 elements at p, those at or past `valid` as zero.
+template <int DT>
 __device__ __forceinline__ Raw8<DT> load_chunk(const elem_t<DT>* p, int valid) {
+  if (valid >= 8) return reinterpret_cast<const AnyChunk<DT>*>(p)->v;
   Raw8<DT> r;
-  if constexpr (VEC) {
-    if (valid > 0) return load8<DT>(p);
 #pragma unroll
-    for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) r.w[i] = (v4u){0, 0, 0, 0};
-  } else {
+  for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) r.w[i] = (v4u){0, 0, 0, 0};
+  if (valid > 0) {  // the end of a row
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 7; ++i) {
       if constexpr (DT == 0) {
         r.w[i >> 2][i & 3] = i < valid ? __float_as_uint(p[i]) : 0u;
       } else {
-        const unsigned short h = i < valid ? __builtin_bit_cast(unsigned short, p[i]) : (unsigned short)0;
-        if (i & 1) r.w[0][i >> 1] |= (unsigned)h << 16;
-        else r.w[0][i >> 1] = h;
+        const unsigned h = i < valid ? (unsigned)__builtin_bit_cast(unsigned short, p[i]) : 0u;
+        r.w[0][i >> 1] |= h << (16 * (i & 1));
       }
     }
   }
   return r;
 }
 
-// VEC: 16-byte loads (X, ldx and K in multiples of 8 elements, base aligned).
-template <int DT, int FMT, int RT, bool VEC, bool ROWS, bool COLS, bool SQUARE>
+template <int DT, int FMT, int RT, bool ROWS, bool COLS, bool SQUARE>
 __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParams p) {
   static_assert(RT == 8 || (!COLS && !SQUARE), "columns and squares need the 128 rows of a block");
   constexpr int kRows = 16 * RT, kPitch = 132;  // LDS bytes between columns of the transposed codes
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int m = RT * g + i;
-    v[i] = load_chunk<DT, VEC>(x + (int64_t)m * p.ldx, m0 + m < p.M ? p.K - k : 0);
+    v[i] = load_chunk<DT>(x + (int64_t)m * p.ldx, m0 + m < p.M ? p.K - k : 0);
   }
 
   // largest magnitudes: of the thread's rows, and of its columns
