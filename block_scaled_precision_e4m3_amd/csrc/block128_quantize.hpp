@@ -151,15 +151,10 @@ __device__ __forceinline__ unsigned mag_bits(unsigned m) {
   else return half_bits<DT>(max(m & 0xFFFFu, m >> 16));
 }
 
-// 8 elements from any address an element may have: gfx950 takes 16-byte loads at any alignment, an aligned one as fast.
-template <int DT>
-struct __attribute__((packed, aligned(DT == 0 ? 4 : 2))) AnyChunk {
-  Raw8<DT> v;
-};
 // 8 elements at p, those at or past `valid` as zero.
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load_chunk(const elem_t<DT>* p, int valid) {
-  if (valid >= 8) return reinterpret_cast<const AnyChunk<DT>*>(p)->v;
+  if (valid >= 8) return load8<DT>(p);
   Raw8<DT> r;
 #pragma unroll
   for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) r.w[i] = (v4u){0, 0, 0, 0};

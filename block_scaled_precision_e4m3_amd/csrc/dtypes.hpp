@@ -20,18 +20,19 @@ using elem_t = typename Elem<DT>::type;
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v8f __attribute__((ext_vector_type(8)));
 
-// 8 consecutive elements at a 16-byte aligned address, raw and as float32.
+// 8 consecutive elements, raw and as float32.  They may lie at any address an element may have: gfx950 takes 16-byte
+// accesses at any alignment, and aligned ones as fast.
 template <int DT>
 struct Raw8 {
   v4u w[DT == 0 ? 2 : 1];
 };
 template <int DT>
+struct __attribute__((packed, aligned(DT == 0 ? 4 : 2))) Raw8At {
+  Raw8<DT> v;
+};
+template <int DT>
 __device__ __forceinline__ Raw8<DT> load8(const elem_t<DT>* p) {
-  Raw8<DT> r;
-  const v4u* q = reinterpret_cast<const v4u*>(p);
-  r.w[0] = q[0];
-  if constexpr (DT == 0) r.w[1] = q[1];
-  return r;
+  return reinterpret_cast<const Raw8At<DT>*>(p)->v;
 }
 template <int DT>
 __device__ __forceinline__ v8f widen8(const Raw8<DT>& r) {
@@ -53,20 +54,16 @@ __device__ __forceinline__ v8f widen8(const Raw8<DT>& r) {
 // Rounded to nearest even (float16 overflows to infinity).
 template <int DT>
 __device__ __forceinline__ void store8(elem_t<DT>* p, const v8f& f) {
-  v4u* q = reinterpret_cast<v4u*>(p);
+  Raw8<DT> r;
   if constexpr (DT == 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4u u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[4 * h + i]);
-      q[h] = u;
-    }
+    for (int i = 0; i < 8; ++i) r.w[i >> 2][i & 3] = __float_as_uint(f[i]);
   } else if constexpr (DT == 1) {
-    q[0] = __builtin_bit_cast(v4u, __builtin_convertvector(f, v8bf));
+    r.w[0] = __builtin_bit_cast(v4u, __builtin_convertvector(f, v8bf));
   } else {
-    q[0] = __builtin_bit_cast(v4u, __builtin_convertvector(f, v8h));
+    r.w[0] = __builtin_bit_cast(v4u, __builtin_convertvector(f, v8h));
   }
+  reinterpret_cast<Raw8At<DT>*>(p)->v = r;
 }
 
 // The number of bytes of one element on the host.

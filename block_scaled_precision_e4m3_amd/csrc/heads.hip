@@ -67,17 +67,9 @@ int64_t backward_parts(int64_t T) {
 // Those of the vector kernel, of which there are no more.
 int64_t vector_parts(int64_t T) { return std::min<int64_t>(backward_parts(T), mxg::heads::kBackParts); }
 
-// Whether every access of the vector kernels is a whole 16-byte one: 8-feature chunks of the head, of its rotary part
-// and of what lies before it, at aligned addresses.
-bool whole_chunks(const Params& p, int dtype, const Tensor* tensors[], int count) {
-  const int e = mxg::elem_bytes(dtype);
-  if (p.D % 16 != 0 || p.rot % 16 != 0 || p.off % 8 != 0) return false;
-  for (int i = 0; i < count; ++i) {
-    const Tensor& x = *tensors[i];
-    if (!aligned16(x.p) || x.ts * e % 16 != 0 || x.hs * e % 16 != 0) return false;
-  }
-  return aligned16(p.cos) && aligned16(p.sin) && aligned16(p.w[0]) && aligned16(p.w[1]);
-}
+// Whether the head, its rotary part and what lies before it are whole chunks of 8 features, as the vector kernels want
+// them, in pairs of chunks.
+bool whole_chunks(const Params& p) { return p.D % 16 == 0 && p.rot % 16 == 0 && p.off % 8 == 0; }
 
 template <int DT, int MODE, bool IN, bool OUT>
 void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
@@ -99,16 +91,8 @@ void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
 // Launches the pass; returns its workgroups.
 template <int MODE>
 int launch(Params& p, int dtype, int cus, hipStream_t s) {
-  const Tensor* tensors[6];
-  int count = 0;
-  for (int k = 0; k < 2; ++k)
-    if (p.H[k] > 0) {
-      tensors[count++] = &p.x[k];
-      tensors[count++] = &p.y[k];
-      if (MODE == mxg::heads::kBackward) tensors[count++] = &p.g[k];
-    }
   int64_t grid;
-  if (whole_chunks(p, dtype, tensors, count)) {
+  if (whole_chunks(p)) {
     p.lpr = 1;
     while (16 * p.lpr < p.D) p.lpr *= 2;
     p.rpw = 64 / p.lpr;
