@@ -31,8 +31,12 @@ struct GemmParams {
   float* sums;       // splits > 1: (splits, L, M, ldw) float32 partial sums in place of C
   int ldw;
   bool b_rows, accumulate;
-  bool c_vec;        // 16-byte stores of C: base, ldc and N in multiples of 16 bytes
+  bool c_vec;        // base, ldc and N in multiples of 16 bytes: every store of C is a whole one
 };
+
+// 16 bytes where an element of C may lie: gfx950 takes 16-byte accesses at any alignment.
+typedef v4u v4u_at2 __attribute__((aligned(2)));
+typedef v4u v4u_at4 __attribute__((aligned(4)));
 
 constexpr unsigned kOob = 0x80000000u;  // an offset past every resource: reads as zero, is not stored
 
@@ -384,16 +388,10 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
       count = item < items ? part_of<T>(p, item).count : 0;
       using E = elem_t<CT>;
       E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
-      if (p.c_vec) {
-        // N and ldc are multiples of 8 here: a lane's 8 columns lie inside or outside N together
-        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * p.ldc + min(p.N - at.n0, T::kBN)));
-        const bool odd = (r & 1) != 0;
-        auto store = [&](const v4u& u, int m, int n) {
-          const unsigned off = m < rows && at.n0 + n < p.N ? 2u * (unsigned)(m * (int)p.ldc + n) : kOob;
-          // non-temporal: C is not read here, and keeping it would push A and B out of the caches (8192 x
-          // 24576 x 1536: 341 -> 318 us)
-          __builtin_amdgcn_raw_buffer_store_b128(u, rc, (int)off, 0, 2);
-        };
+      const bool odd = (r & 1) != 0;
+      // stores 8 columns to a call; non-temporal: C is not read here, and keeping it would push A and B out of the
+      // caches (8192 x 24576 x 1536: 341 -> 318 us)
+      auto put = [&](auto store) {
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt) {
           v4u u[kPairs];
@@ -429,16 +427,32 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
             for (int h = 0; h < kPairs; ++h) store(u[h], m, n + 32 * h);
           }
         }
+      };
+      if (p.c_vec) {
+        // N and ldc are multiples of 8 here: a lane's 8 columns lie inside or outside N together
+        int ldc = (int)p.ldc;
+        asm volatile("" : "+s"(ldc));  // the stores' offsets are made here, not kept in registers through the K loop
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * ldc + min(p.N - at.n0, T::kBN)));
+        put([&](const v4u& u, int m, int n) {
+          const unsigned off = m < rows && at.n0 + n < p.N ? 2u * (unsigned)(m * ldc + n) : kOob;
+          __builtin_amdgcn_raw_buffer_store_b128(u, rc, (int)off, 0, 2);
+        });
       } else {
+        // 16-byte stores at any alignment but for the last columns of a row (8192 x 8191 x 1024: 184 us element by
+        // element)
+        int64_t ldc = p.ldc;
+        asm volatile("" : "+s"(ldc));
+        put([&](const v4u& u, int m, int n) {
+          const int left = p.N - at.n0 - n;
+          E* to = c + m * ldc + n;
+          if (m < rows && left >= 8) {
+            __builtin_nontemporal_store(u, reinterpret_cast<v4u_at2*>(to));
+          } else if (m < rows) {
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int m = a_row + 16 * mt, n = T::kTN * wn + 32 * (nt >> 1) + 8 * g + 4 * (nt & 1) + e;
-              if (m < rows && at.n0 + n < p.N) c[(int64_t)m * p.ldc + n] = (E)acc[mt][nt][e];
-            }
+            for (int e = 0; e < 7; ++e)
+              if (e < left) to[e] = __builtin_bit_cast(E, (unsigned short)(u[e >> 1] >> (16 * (e & 1))));
+          }
+        });
       }
     }
   }
@@ -572,9 +586,8 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
       count = item < items ? part_of<T>(p, item).count : 0;
       const int rows = min(p.M - at.m0, T::kBM);
       float* c = static_cast<float*>(p.C) + ((int64_t)l * p.M + at.m0) * p.ldc + at.n0;
-      if (p.c_vec) {
-        // N and ldc are multiples of 4 here
-        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 4u * (unsigned)((int64_t)(rows - 1) * p.ldc + min(p.N - at.n0, T::kBN)));
+      // finish(v, m, n): quad q of v is columns n .. n + 3 of row m + q
+      auto quads = [&](auto finish) {
 #pragma unroll
         for (int m = 0; m < kMt; ++m)
 #pragma unroll
@@ -601,39 +614,54 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
                 }
               }
             }
-            unsigned off[4];
+            finish(v, (a_row & ~3) + 32 * m, T::kTN * wn + 32 * n + 16 * h + 4 * (r & 3));
+          }
+      };
+      if (p.c_vec) {
+        // N and ldc are multiples of 4 here
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 4u * (unsigned)((int64_t)(rows - 1) * p.ldc + min(p.N - at.n0, T::kBN)));
+        quads([&](float(&v)[4][4], int m, int n) {
+          unsigned off[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int mm = (a_row & ~3) + q + 32 * m, nn = T::kTN * wn + 32 * n + 16 * h + 4 * (r & 3);
-              off[q] = mm < rows && at.n0 + nn < p.N ? 4u * (unsigned)(mm * (int)p.ldc + nn) : kOob;
-            }
-            if (p.accumulate) {
-              v4u old[4];
+          for (int q = 0; q < 4; ++q) off[q] = m + q < rows && at.n0 + n < p.N ? 4u * (unsigned)((m + q) * (int)p.ldc + n) : kOob;
+          if (p.accumulate) {
+            v4u old[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) old[q] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off[q], 0, 0);
+            for (int q = 0; q < 4; ++q) old[q] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off[q], 0, 0);
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) v[q][w] += __uint_as_float(old[q][w]);
-            }
+              for (int w = 0; w < 4; ++w) v[q][w] += __uint_as_float(old[q][w]);
+          }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 4; ++q) {
+            const v4u out = {__float_as_uint(v[q][0]), __float_as_uint(v[q][1]), __float_as_uint(v[q][2]), __float_as_uint(v[q][3])};
+            __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 2);
+          }
+        });
+      } else {
+        // 16-byte accesses at any alignment but for the last columns of a row (8192 x 8191 x 1024: 396 us element by
+        // element)
+        quads([&](float(&v)[4][4], int m, int n) {
+          const int left = p.N - at.n0 - n;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float* to = c + (int64_t)(m + q) * p.ldc + n;
+            if (m + q < rows && left >= 4) {
+              if (p.accumulate) {
+                const v4u old = *reinterpret_cast<const v4u_at4*>(to);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[q][w] += __uint_as_float(old[w]);
+              }
               const v4u out = {__float_as_uint(v[q][0]), __float_as_uint(v[q][1]), __float_as_uint(v[q][2]), __float_as_uint(v[q][3])};
-              __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 2);
+              __builtin_nontemporal_store(out, reinterpret_cast<v4u_at4*>(to));
+            } else if (m + q < rows) {
+#pragma unroll
+              for (int w = 0; w < 3; ++w)
+                if (w < left) to[w] = (p.accumulate ? to[w] : 0.f) + v[q][w];
             }
           }
-      } else {
-#pragma unroll
-        for (int m = 0; m < kMt; ++m)
-#pragma unroll
-          for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int mm = a_row + 32 * m, nn = T::kTN * wn + 32 * n + 16 * h + e;
-              if (mm >= rows || at.n0 + nn >= p.N) continue;
-              float* to = c + (int64_t)mm * p.ldc + nn;
-              *to = (p.accumulate ? *to : 0.f) + acc[m][n][e];
-            }
+        });
       }
     }
   }
