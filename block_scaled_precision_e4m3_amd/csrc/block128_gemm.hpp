@@ -431,7 +431,8 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
       if (p.c_vec) {
         // N and ldc are multiples of 8 here: a lane's 8 columns lie inside or outside N together
         int ldc = (int)p.ldc;
-        asm volatile("" : "+s"(ldc));  // the stores' offsets are made here, not kept in registers through the K loop
+        // with 16 scales more to a lane, the stores' offsets are made here, not kept in registers through the K loop
+        if constexpr (BROWS) asm volatile("" : "+s"(ldc));
         const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * ldc + min(p.N - at.n0, T::kBN)));
         put([&](const v4u& u, int m, int n) {
           const unsigned off = m < rows && at.n0 + n < p.N ? 2u * (unsigned)(m * ldc + n) : kOob;
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
         // 16-byte stores at any alignment but for the last columns of a row (8192 x 8191 x 1024: 184 us element by
         // element)
         int64_t ldc = p.ldc;
-        asm volatile("" : "+s"(ldc));
+        asm volatile("" : "+s"(ldc));  // as above
         put([&](const v4u& u, int m, int n) {
           const int left = p.N - at.n0 - n;
           E* to = c + m * ldc + n;
