@@ -193,7 +193,6 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
   p.Mb = (int)cdiv(M, 128);
   p.Kb = (int)cdiv(K, 128);
   p.pow2 = (flags & MXG_QUANT_POW2) != 0;
-  // whole 8-element chunks at 16-byte addresses
   // rows alone, and too few of them for 128-row tiles to fill the chip: 16 rows to a workgroup
   const bool few = rows && !cols && !square && L * p.Mb * p.Kb < 4LL * cus;
   p.tiles_m = few ? (int)cdiv(M, 16) : p.Mb;

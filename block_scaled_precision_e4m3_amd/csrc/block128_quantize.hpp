@@ -25,6 +25,10 @@
 // lost nor finite.  The transposed codes are converted along the thread's 8
 // rows, gathered in LDS as (column, row) bytes and stored as whole 128-byte
 // rows.
+//
+// The bound is memory: 8192 x 7168 bfloat16, rows and columns, 51 us (4.65
+// TB/s), 7168 x 2048 float32 squares with their transpose 14.9 us; 8 x 7168 rows
+// take 2.3 us, of which 1.95 are an empty launch.
 #pragma once
 
 #include "dtypes.hpp"

@@ -208,7 +208,9 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(Params p) {
 // of two (lpr), share a head; a wave works on 64 / lpr heads of one token at a
 // time, and keeps that token's cos and sin (and the weights) in registers over
 // the heads it does.  The bound is memory: every feature is read once and
-// written once, cos and sin once per wave and token.  Rows and heads may lie at
+// written once, cos and sin once per wave and token (rope, 8192 tokens of 128
+// heads of 192, 64 of them rotary: 140 us, 5.8 TB/s; norm and rope, 8192 tokens
+// of 32 + 8 heads of 128: 38 us, 4.5 TB/s).  Rows and heads may lie at
 // any stride: chunks that are not aligned to 16 bytes are accessed all the same
 // (1024 tokens of 32 + 8 heads of 128, rows one element apart from aligned ones,
 // backward: 130 us in the wave-per-row kernel, 14.5 us here).

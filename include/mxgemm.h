@@ -470,8 +470,8 @@ enum {
  *
  *   scale = a / FMAX,  code = rne(x FMAX / a)             FMAX 448 or 57344
  *
- * with both quotients rounded to float32 (the second before it is rounded to a
- * code), or, with MXG_QUANT_POW2, scale = 2^e with e the smallest integer giving
+ * with the scale rounded to float32 and the code nearest to the exact quotient,
+ * or, with MXG_QUANT_POW2, scale = 2^e with e the smallest integer giving
  * FMAX * 2^e >= a and code = rne(x * 2^-e).
  *
  *   X  : (L, M, K) of x_dtype, K contiguous, rows ldx >= K elements apart,
