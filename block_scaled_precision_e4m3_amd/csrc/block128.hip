@@ -88,7 +88,7 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
   return MXG_OK;
 }
 
-// Which kernel, tile and division of K.  rows: a kernel for up to 16 rows of A.
+// Which kernel, tile and division of K.  rows: a kernel for few rows of A.
 //
 // Tiles: the time in microseconds of a tile size is taken as
 //   rounds of work items over the compute units x (blocks of K x block x (0.7 + 0.3 x busy) + end)
@@ -118,7 +118,10 @@ constexpr int kUnits = 256;  // compute units: the choice, and with it the works
 Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
   // a rows workgroup reads A once for its columns, so more columns are better as long as they leave enough
   // workgroups (7168 columns: 32 at a time 4.9 us, 16 5.1 us; 4096: 7.3 and 5.8 us; K = 2048 and 4096)
-  if (M <= 16) return {L * cdiv(N, 32) >= kUnits * 3 / 4 ? 32 : 16, 16, 0, 1, 1};
+  // Up to 32 rows too, unless there are more workgroups than compute units (32x24576x1536: 11.7 us, tiles 9.7) or, for
+  // a 16-bit C, K is long (32x7168x2048: 6.8 us, tiles 7.0; 32x6144x4096: 10.4 and 9.7; float32 C: 7.1 and 9.4, 11.0
+  // and 14.7).  With 64 rows tiles are as fast or faster (64x7168x2048: 9.2 us, tiles 7.2; float32 C: 9.5 and 9.6).
+  if (M <= 16 || (M <= 32 && L * cdiv(N, 32) <= kUnits && (exact || K <= 2048))) return {L * cdiv(N, 32) >= kUnits * 3 / 4 ? 32 : 16, 16, 0, 1, 1};
   struct Size {
     int bm, bn, kb;
     bool divides;  // its kernel can take part of K

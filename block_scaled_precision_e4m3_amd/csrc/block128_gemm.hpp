@@ -676,7 +676,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 
 // --- few rows of A -----------------------------------------------------------------
 //
-// Up to 16 rows.  B is read once, straight from memory into the MFMA's
+// Up to 16 MT rows.  B is read once, straight from memory into the MFMA's
 // registers: a workgroup takes COLS columns, its W waves every W-th block of K,
 // and the waves' sums meet in LDS in a fixed order.  B's bytes bound it, so a
 // wave asks for its next block before it uses this one (1 x 7168 x 2048: 4.9 us,
@@ -687,17 +687,22 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 // C the widened codes, as in the tile kernels.
 constexpr int kRowWaves = 8;
 
-template <int FA, int FB, int CT, bool BROWS, int COLS>
+template <int FA, int FB, int CT, bool BROWS, int COLS, int MT>
 __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParams p) {
   constexpr int W = kRowWaves;
   constexpr int NT = COLS / 16;
-  __shared__ float lds[W][16][16 * NT + 4];
+  __shared__ float lds[W][16 * MT][16 * NT + 4];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l = (int)blockIdx.x / p.tilesN, n0 = ((int)blockIdx.x % p.tilesN) * COLS;
-  const int m = min(r, p.M - 1);
-  const uint8_t* a = p.A + ((int64_t)l * p.M + m) * p.K + 16 * g;
-  const float* sa = p.SA + (int64_t)l * p.Kb * p.M + m;
+  const uint8_t* a[MT];
+  const float* sa[MT];
+#pragma unroll
+  for (int s = 0; s < MT; ++s) {
+    const int m = min(16 * s + r, p.M - 1);
+    a[s] = p.A + ((int64_t)l * p.M + m) * p.K + 16 * g;
+    sa[s] = p.SA + (int64_t)l * p.Kb * p.M + m;
+  }
   const uint8_t* b[NT];
   const float* sb[NT];
 #pragma unroll
@@ -706,8 +711,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
     sb[t] = BROWS ? p.SB + (int64_t)l * p.Kb * p.N : p.SB + ((int64_t)l * p.Nb + min(n0 + 16 * t, p.N - 1) / 128) * p.Kb;
   }
   struct Block {
-    v4u a[2], b[NT][2];
-    float sa;
+    v4u a[MT][2], b[NT][2];
+    float sa[MT];
     v4f sb[NT];
   };
   auto load = [&](Block& k, int j) {
@@ -718,9 +723,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
       k.b[t][0] = *reinterpret_cast<const v4u*>(b[t] + lo);
       k.b[t][1] = *reinterpret_cast<const v4u*>(b[t] + hi);
     }
-    k.a[0] = *reinterpret_cast<const v4u*>(a + lo);
-    k.a[1] = *reinterpret_cast<const v4u*>(a + hi);
-    k.sa = sa[(int64_t)j * p.M];
+#pragma unroll
+    for (int s = 0; s < MT; ++s) {
+      k.a[s][0] = *reinterpret_cast<const v4u*>(a[s] + lo);
+      k.a[s][1] = *reinterpret_cast<const v4u*>(a[s] + hi);
+      k.sa[s] = sa[s][(int64_t)j * p.M];
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if constexpr (BROWS) {
@@ -732,9 +740,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
     }
   };
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
-  v4f acc[NT];
+  v4f acc[MT][NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = zero;
+  for (int s = 0; s < MT; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[s][t] = zero;
   auto multiply = [&](Block& k, int j) {
     if (128 * j + 128 > p.K) {
       const v4u none = {0, 0, 0, 0};
@@ -744,26 +754,30 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
         k.b[t][0] = lo_in ? k.b[t][0] : none;
         k.b[t][1] = hi_in ? k.b[t][1] : none;
       }
-      k.a[0] = lo_in ? k.a[0] : none;
-      k.a[1] = hi_in ? k.a[1] : none;
+#pragma unroll
+      for (int s = 0; s < MT; ++s) {
+        k.a[s][0] = lo_in ? k.a[s][0] : none;
+        k.a[s][1] = hi_in ? k.a[s][1] : none;
+      }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int i = 0; i < MT * NT; ++i) {
+      const int s = i / NT, t = i % NT;
       v4f part = zero;
       if constexpr (CT != 0) {
         struct Bytes32 { v4u lo, hi; };
         part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(v8i, (Bytes32{k.b[t][0], k.b[t][1]})),
-                                                                __builtin_bit_cast(v8i, (Bytes32{k.a[0], k.a[1]})), zero,
+                                                                __builtin_bit_cast(v8i, (Bytes32{k.a[s][0], k.a[s][1]})), zero,
                                                                 FB, FA, 0, 0, 0, 0);
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cvt8<FB>(k.b[t][q >> 1][2 * (q & 1)], k.b[t][q >> 1][2 * (q & 1) + 1], 1.f),
-                                                         cvt8<FA>(k.a[q >> 1][2 * (q & 1)], k.a[q >> 1][2 * (q & 1) + 1], 1.f),
+                                                         cvt8<FA>(k.a[s][q >> 1][2 * (q & 1)], k.a[s][q >> 1][2 * (q & 1) + 1], 1.f),
                                                          part, 0, 0, 0);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(part[e], k.sa * k.sb[t][BROWS ? e : 0], acc[t][e]);
+      for (int e = 0; e < 4; ++e) acc[s][t][e] = __builtin_fmaf(part[e], k.sa[s] * k.sb[t][BROWS ? e : 0], acc[s][t][e]);
     }
   };
   if (wave < p.Kb) {
@@ -783,7 +797,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
     }
   }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&lds[wave][r][16 * t + 4 * g]) = acc[t];
+  for (int s = 0; s < MT; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&lds[wave][16 * s + r][16 * t + 4 * g]) = acc[s][t];
   __syncthreads();
   elem_t<CT>* c = static_cast<elem_t<CT>*>(p.C) + (int64_t)l * p.M * p.ldc + n0;
   for (int i = threadIdx.x; i < p.M * COLS; i += 64 * W) {

@@ -9,8 +9,13 @@ namespace {
 template <int FA, int FB, int CT, bool BROWS>
 void launch(const GemmParams& p, int cols, int64_t grid, hipStream_t s) {
   const dim3 g((unsigned)grid), b(64 * kRowWaves);
-  if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32>), g, b, 0, s, p);
+  if (p.M <= 16) {
+    if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 1>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 1>), g, b, 0, s, p);
+  } else {
+    if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 2>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 2>), g, b, 0, s, p);
+  }
 }
 
 }  // namespace

@@ -174,7 +174,8 @@ def check_gemm(lib, m, n, k, fa=0, fb=0, b_block=128, dtype=torch.bfloat16, seed
 
 SIZES = [(1, 1, 16), (1, 7168, 2048), (2, 130, 144), (7, 96, 1040), (16, 256, 128), (17, 100, 256), (33, 72, 400),
          (64, 512, 512), (65, 300, 640), (100, 1000, 272), (128, 128, 128), (129, 257, 384), (200, 700, 2064),
-         (256, 256, 256), (300, 520, 1024), (513, 1030, 528), (1000, 2056, 160)]
+         (256, 256, 256), (300, 520, 1024), (513, 1030, 528), (1000, 2056, 160),
+         (31, 500, 1040), (32, 4000, 2064), (25, 1001, 4112), (18, 8200, 144)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
