@@ -91,10 +91,10 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
 // Which kernel, tile and division of K.  rows: a kernel for few rows of A.
 //
 // Tiles: the time in microseconds of a tile size is taken as
-//   rounds of work items over the compute units x (blocks of K x block x (0.7 + 0.3 x busy) + end)
-// where busy is the share of compute units with work (one that shares the chip
-// and its power with idle ones is faster), and, where K is divided, the second
-// kernel that adds the parts up.  block and end were measured on MI355X, one
+//   rounds of work items over the compute units x (blocks of K x block x (1 - idle x gain) + end)
+// where idle is the share of compute units without work (the larger tiles, which
+// power bounds, gain by it; the smaller ones wait for memory), and, where K is
+// divided, the second kernel that adds the parts up.  block and end were measured on MI355X, one
 // size forced at a time.  16-bit C, the best and its neighbours:
 //   128x7168x2048     64 x 64 7.1     64 x 128 8.4   128 x 128 11.1
 //   512x4096x7168     64 x 128 21.7   64 x 64 27.7   128 x 128 28.6
@@ -107,7 +107,8 @@ int check_gemm(int64_t ldc, int64_t M, int64_t N, int64_t K, int64_t L, int fa, 
 //   4000x7168x2048    128 x 128 115.4 128 x 256 121.3 64 x 128 139.9
 //   2048x4096x4096    128 x 256 61.6  128 x 128 64.1 64 x 128 77.1
 // K is divided only where tiles leave compute units idle: 64x1024x7168 in 4
-// parts 10.3 us, in one 14.8.
+// parts 10.3 us, in one 14.8; 128x2048x7168 12.7 and 14.3; 256x1024x4096 10.5
+// and 9.9, with a float32 C 12.7 and 15.4.
 struct Choice {
   int rows;                // columns per workgroup of the rows kernel, 0: tiles
   int bm, bn, kb, splits;  // tile; blocks of K per step; parts of K
@@ -125,17 +126,17 @@ Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
   struct Size {
     int bm, bn, kb;
     bool divides;  // its kernel can take part of K
-    double block, end;
+    double block, end, gain;
   };
-  static constexpr Size kSizes[2][5] = {{{64, 64, 2, true, 0.215, 0.5},
-                                         {64, 128, 2, true, 0.335, 0.7},
-                                         {128, 128, 1, false, 0.64, 1.0},
-                                         {128, 256, 1, false, 1.08, 2.0},
-                                         {256, 256, 1, false, 1.8, 3.0}},
-                                        {{64, 64, 2, true, 0.355, 0.8},
-                                         {64, 128, 2, true, 0.585, 1.0},
-                                         {128, 128, 2, true, 0.97, 1.3},
-                                         {128, 256, 1, false, 1.85, 2.0}}};
+  static constexpr Size kSizes[2][5] = {{{64, 64, 2, true, 0.215, 0.5, 0.0},
+                                         {64, 128, 2, true, 0.335, 0.7, 0.0},
+                                         {128, 128, 1, false, 0.64, 1.0, 0.3},
+                                         {128, 256, 1, false, 1.08, 2.0, 0.3},
+                                         {256, 256, 1, false, 1.8, 3.0, 0.3}},
+                                        {{64, 64, 2, true, 0.355, 0.8, 0.0},
+                                         {64, 128, 2, true, 0.585, 1.0, 0.0},
+                                         {128, 128, 2, true, 0.97, 1.3, 0.3},
+                                         {128, 256, 1, false, 1.85, 2.0, 0.3}}};
   const int64_t blocks = cdiv(K, 128);
   Choice best{};
   double best_time = 0;
@@ -145,9 +146,10 @@ Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (splits > 1 && (!t.divides || splits > steps || tiles * (splits - 1) >= kUnits)) break;
       const int64_t per = cdiv(steps, splits), parts = cdiv(steps, per);
-      const double busy = std::min<double>(tiles * parts, kUnits) / kUnits;
-      double time = (double)cdiv(tiles * parts, kUnits) * (per * t.kb * t.block * (0.7 + 0.3 * busy) + t.end);
-      if (parts > 1) time += 4.0 + parts * L * M * N * 8 / 3e6;  // written and read at 3 TB/s
+      const double idle = 1.0 - std::min<double>(tiles * parts, kUnits) / kUnits;
+      double time = (double)cdiv(tiles * parts, kUnits) * (per * t.kb * t.block * (1.0 - idle * t.gain) + t.end);
+      // written and read at 3 TB/s, one part after the other
+      if (parts > 1) time += 4.0 + 0.12 * parts + parts * L * M * N * 8 / 3e6;
       if (best.bm == 0 || time < best_time) {
         best = {0, t.bm, t.bn, t.kb, (int)parts};
         best_time = time;
