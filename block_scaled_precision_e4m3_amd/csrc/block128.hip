@@ -44,7 +44,7 @@ int check_quantize(int64_t ldx, int64_t M, int64_t K, int64_t L, int dt, int fmt
 template <int DT, int FMT, int RT>
 void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, int64_t grid, hipStream_t s) {
   using namespace mxg::b128;
-  const dim3 g((unsigned)grid), b(kQThreads);
+  const dim3 g = grid_of(grid), b(kQThreads);
   if constexpr (RT == 8) {
     if (square && rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, true, true>), g, b, 0, s, p);
     else if (square && rows) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, false, true>), g, b, 0, s, p);
@@ -202,6 +202,7 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
   const bool few = rows && !cols && !square && L * p.Mb * p.Kb < 4LL * cus;
   p.tiles_m = few ? (int)cdiv(M, 16) : p.Mb;
   const int64_t grid = L * p.tiles_m * p.Kb;
+  p.blocks = (unsigned)grid;
   hipStream_t s = (hipStream_t)stream;
   if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, few, rows, cols, square, grid, s);
   else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, few, rows, cols, square, grid, s);
@@ -267,7 +268,8 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
   const Choice ch = choose(M, N, K, L, exact);
   if (ch.rows) {
     p.tilesN = (int)cdiv(N, ch.rows);
-    const hipError_t e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.rows, L * p.tilesN, s);
+    p.num_tiles = (int)(L * p.tilesN);
+    const hipError_t e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.rows, grid_of(p.num_tiles), s);
     return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
   }
   p.tilesM = (int)cdiv(M, ch.bm);

@@ -694,7 +694,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
   __shared__ float lds[W][16 * MT][16 * NT + 4];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int l = (int)blockIdx.x / p.tilesN, n0 = ((int)blockIdx.x % p.tilesN) * COLS;
+  const unsigned item = blockIdx.y * gridDim.x + blockIdx.x;
+  if (item >= (unsigned)p.num_tiles) return;
+  const int l = (int)item / p.tilesN, n0 = ((int)item % p.tilesN) * COLS;
   const uint8_t* a[MT];
   const float* sa[MT];
 #pragma unroll

@@ -32,6 +32,8 @@ int check(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t off
   if (flags & ~known) return MXG_ERR_FLAGS;
   if (!fits_i32(T) || !fits_i32(Hq + Hk) || Hq + Hk > (1 << 20) || !fits_i32(table)) return MXG_ERR_SHAPE;
   if (!positions && rot > 0 && T > table) return MXG_ERR_SHAPE;
+  // a wave takes a head of a token at least, four waves a workgroup
+  if (T > 0 && Hq + Hk > (1LL << 36) / T) return MXG_ERR_SHAPE;
   if (!strides) return MXG_ERR_NULL;
   for (int i = 0; i < tensors; ++i) {
     // byte offsets stay below 2^62
@@ -73,7 +75,7 @@ bool whole_chunks(const Params& p) { return p.D % 16 == 0 && p.rot % 16 == 0 && 
 
 template <int DT, int MODE, bool IN, bool OUT>
 void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
-  const dim3 g((unsigned)grid);
+  const dim3 g = grid_of(grid);
   if constexpr (MODE == mxg::heads::kBackward)
     hipLaunchKernelGGL((mxg::heads::heads_backward_kernel<DT, IN, OUT>), g, dim3(64 * mxg::heads::kBackWaves), 0, s, p);
   else

@@ -173,3 +173,10 @@ def test_rope_tables(lib):
     for bad in ({"rot": 15}, {"rot": 16, "scaling": "other"}, {"rot": 16, "factor": 0.0}, {"rot": 16, "length": -1}):
         with pytest.raises(lib.MxgemmValueError):
             lib.rope_table(**{"length": 4, "device": "cpu", **bad})
+
+
+def test_more_heads_than_a_launch_has_waves(lib):
+    f = lib._lib.mxgemm_rope
+    for T, H, want in ((1 << 30, 1 << 6, lib.MXG_ERR_DEVICE), (1 << 30, (1 << 6) + 1, lib.MXG_ERR_SHAPE),
+                       ((1 << 31) - 1, 1 << 20, lib.MXG_ERR_SHAPE)):
+        assert f(GOOD, GOOD, GOOD, GOOD, GOOD, STRIDES, T, H, 128, 64, 0, 4, 0, 1, 0, None) == want, (T, H)
