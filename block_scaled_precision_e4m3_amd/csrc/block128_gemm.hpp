@@ -115,7 +115,8 @@ struct Stream {
   unsigned lds0, chunk_a, chunk_b, row_k, next_k;
   __amdgpu_buffer_rsrc_t ra, rb;
   const char* sc_at;        // the block's scales: the first waves fetch A's, 64 rows each, the next ones B's
-  unsigned sc_bytes, sc_voff, sc_inc;
+  unsigned sc_bytes, sc_voff;
+  int64_t sc_inc;           // bytes from one block's scales to the next one's: past 32 bits for 2^30 rows
   unsigned base, va[T::kKB], vb[T::kKB];  // of the step being fetched
 
   __device__ __forceinline__ Stream(const GemmParams& p_, const uint8_t* lds, int lane, int wave_, int first)
@@ -130,7 +131,7 @@ struct Stream {
     sc_voff = 4 * mine;
     if (!BROWS && wave >= T::kBM / 64)  // one scale per 128 columns: lane j takes block j of the tile
       sc_voff = mine < (unsigned)((T::kBN + 127) / 128) ? 4u * mine * (unsigned)p.Kb : kOob;
-    sc_inc = wave < T::kBM / 64 ? 4u * (unsigned)p.M : BROWS ? 4u * (unsigned)p.N : 4u;
+    sc_inc = 4 * (wave < T::kBM / 64 ? (int64_t)p.M : BROWS ? (int64_t)p.N : 1);
     open();
   }
   __device__ __forceinline__ void open() {

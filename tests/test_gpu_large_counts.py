@@ -1,6 +1,6 @@
-"""Counts near the ends of 32-bit arithmetic: launches of 2^32 work items and more, tensors of 2^31 elements and more.
-Expected results come from small calls on the repeating part of the inputs;
-the small calls are checked elsewhere."""
+"""Counts near the ends of 32-bit arithmetic: launches of 2^32 work items and more, tensors of 2^31 elements and more,
+scales whose blocks lie 2^31 bytes apart.  Expected results come from small calls on the repeating part of the inputs, which
+are checked elsewhere, or from the oracle."""
 
 import numpy as np
 import pytest
@@ -129,3 +129,27 @@ def test_quantize_and_product_past_32_bits(lib):
         # K is not divided at either size, and every tile sums a row's blocks in one order
         assert repeats(lib.block128_gemm(q, s, b, sb, c_dtype=dtype), lib.block128_gemm(*want[:2], b, sb, c_dtype=dtype))
         torch.cuda.empty_cache()
+
+
+def test_row_scales_of_many_rows(lib):
+    """Row scales of one block of K to the next lie 4 M bytes apart: 2^31 and more here, 2^32 and more for two blocks."""
+    need(160)
+    M, N, K = (1 << 29) + 5, 8, 272
+    print(f"gemm {M}x{N}x{K}", flush=True)
+    rng = np.random.default_rng(3)
+    rows = 96
+    host = B.quantize((rng.standard_normal((3 * rows, K)) * np.exp2(rng.integers(-9, 9, (3 * rows, 1)))).astype(np.float32))
+    hb, hsb, _, _ = B.quantize(rng.standard_normal((N, K)).astype(np.float32), square=True)
+    at = (0, M // 2 - 7, M - rows)             # the rows looked at; nothing depends on what the others hold
+    a = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    sa = torch.empty((3, M), device="cuda")
+    for i, r in enumerate(at):
+        a[r:r + rows] = torch.from_numpy(host[0][i * rows:(i + 1) * rows].copy()).cuda()
+        sa[:, r:r + rows] = torch.from_numpy(host[1][:, i * rows:(i + 1) * rows].copy()).cuda()
+    c = lib.block128_gemm(a.view(torch.float8_e4m3fn), sa, torch.from_numpy(hb.copy()).cuda().view(torch.float8_e4m3fn),
+                          torch.from_numpy(hsb.copy()).cuda())
+    ref, s = B.gemm(host[0], host[1], hb, hsb, 0, 0, 128)
+    for i, r in enumerate(at):
+        got, want, mag = c[r:r + rows].double().cpu().numpy(), ref[i * rows:(i + 1) * rows], s[i * rows:(i + 1) * rows]
+        # bfloat16, and what the 8-bit products may drop: as for the other sizes
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * mag).all(), r
