@@ -6,15 +6,15 @@
 //   code = rne(x FMAX / a);  power-of-two scales: 2^e, e the smallest integer
 //   with FMAX * 2^e >= a.
 //
-// x FMAX / a is taken as x hi + x lo with hi + lo = FMAX / a to about 2^-47, one
-// multiply and one multiply-add per element, which rounds the quotient to
-// float32 correctly: a ratio that lies on a boundary between two codes, as those
-// of 16-bit values often do, stays on it.  With hi alone 0.3% of the codes of
-// bfloat16 activations came out on the other side.  Quotients of 16-bit values
-// are either on a boundary or 2^-16 of themselves away; one of float32 values can
-// be so near that float32 rounds it onto the boundary, about one in 2^20, and
-// settle() then looks at what was rounded off.  No clamp is needed: the quotient
-// never exceeds FMAX.
+// x FMAX / a is taken as x hi + x lo with hi + lo = FMAX / a to about 2^-47, or
+// 2^-30.8 where a is so large that lo is subnormal: one multiply and one
+// multiply-add per element, after which a ratio that lies on a boundary between
+// two codes, as those of 16-bit values often do, stays on it.  With hi alone 0.3%
+// of the codes of bfloat16 activations came out on the other side.  Quotients of
+// 16-bit values are either on a boundary or 2^-16 of themselves away; one of
+// float32 values can be so near that float32 rounds it onto the boundary, about
+// one in 2^20, and settle() then looks at what was rounded off.  No clamp is
+// needed: the quotient never exceeds FMAX.
 //
 // A workgroup takes a tile of 16 RT rows x 128 columns: thread (g, c) holds
 // rows RT g .. RT g + RT - 1 of columns 8c .. 8c + 7 in registers, RT chunks of
@@ -84,12 +84,14 @@ __device__ __forceinline__ Scale block_scale(unsigned bits, bool pow2) {
 __device__ __forceinline__ float scaled(float x, const Scale& s) { return __builtin_fmaf(x, s.hi, x * s.lo); }
 
 // A quotient r that float32 has rounded onto a boundary between codes, moved to the side it came from by one unit in
-// its last place.  One that is not on the boundary is at least 2^-30 r away from it (x FMAX and boundary times a are
-// integers of 27 and 29 bits, times one power of two), one that is, is found to be within about 2^-46 r.
+// its last place.  One that is not on the boundary is more than 2^-29 r away from it (x FMAX and boundary times a are
+// integers of 27 and 29 bits, times powers of two).  What is known of it is within 2^-30.8 r: lo is off by 2^-150 at
+// most, half the smallest subnormal, next to hi of at least 448 / 2^128 (a below 2^103: within 2^-46 r).  So the
+// distance is found above 2^-29.5 r, or below 2^-30.8 r, and 2^-30 r tells them apart.
 __device__ __forceinline__ float settle(float r, float x, const Scale& s) {
   const float off = __builtin_fmaf(x, s.hi, -r) + x * s.lo;
   const int away = (__float_as_int(off) ^ __float_as_int(r)) < 0 ? -1 : 1;
-  const bool move = (__float_as_uint(r) & 0x7FFFFu) == 0 && fabsf(off) > fabsf(r) * 0x1p-38f;
+  const bool move = (__float_as_uint(r) & 0x7FFFFu) == 0 && fabsf(off) > fabsf(r) * 0x1p-30f;
   return __int_as_float(__float_as_int(r) + (move ? away : 0));
 }
 

@@ -374,3 +374,27 @@ def test_quantize_next_to_boundaries(lib, fmt, square):
         xt = np.ascontiguousarray(x.T)
         _, _, qt, _ = lib.block128_quantize(torch.from_numpy(xt).cuda(), fmt, False, True)
         assert np.array_equal(qt.view(torch.uint8).cpu().numpy(), B.quantize(xt, fmt, False, True)[2])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("square", [False, True])
+@pytest.mark.parametrize("exponent", [126, 123, 110, -60, -90])
+def test_quantize_next_to_boundaries_at_the_ends_of_the_range(lib, fmt, square, exponent):
+    """The same blocks times a power of two, to where 1 / max is subnormal and to the smallest maximum."""
+    from test_oracle_block128 import near_boundaries
+    x = np.ldexp(near_boundaries(fmt, 512, 10, 128 if square else 1), exponent).astype(np.float32)
+    check_quantize(lib, torch.from_numpy(x), fmt, True, True, square, False)
+    check_quantize(lib, torch.from_numpy(np.ascontiguousarray(x.T)), fmt, True, True, square, False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("exponent", [119, 0, -99])
+def test_quantize_ties(lib, dtype, exponent):
+    """Halves between codes at a scale of exactly 2^exponent: the codes' own grid rounds them to even."""
+    rng = np.random.default_rng(4)
+    x = np.ldexp(rng.integers(-448, 449, (130, 128)).astype(np.float32), exponent)
+    x[:, 0] = np.ldexp(np.float32(448), exponent)
+    x = torch.from_numpy(x).to(DT[dtype])
+    for fmt in (0, 1):
+        for square in (False, True):
+            check_quantize(lib, x, fmt, True, True, square, False)
