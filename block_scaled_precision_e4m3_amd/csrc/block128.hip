@@ -42,9 +42,9 @@ int check_quantize(int64_t ldx, int64_t M, int64_t K, int64_t L, int dt, int fmt
 }
 
 template <int DT, int FMT, int RT>
-void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, int64_t grid, hipStream_t s) {
+void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, unsigned grid, hipStream_t s) {
   using namespace mxg::b128;
-  const dim3 g = grid_of(grid), b(kQThreads);
+  const dim3 g(grid), b(kQThreads);
   if constexpr (RT == 8) {
     if (square && rows && cols) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, true, true>), g, b, 0, s, p);
     else if (square && rows) hipLaunchKernelGGL((block128_quantize_kernel<DT, FMT, RT, true, false, true>), g, b, 0, s, p);
@@ -58,7 +58,7 @@ void launch_quantize(const QuantParams& p, bool rows, bool cols, bool square, in
 }
 
 template <int DT>
-void launch_quantize(const QuantParams& p, int fmt, bool few, bool rows, bool cols, bool square, int64_t grid,
+void launch_quantize(const QuantParams& p, int fmt, bool few, bool rows, bool cols, bool square, unsigned grid,
                      hipStream_t s) {
   if (fmt == MXG_FMT_E4M3) {
     if (few) launch_quantize<DT, 0, 1>(p, rows, cols, square, grid, s);
@@ -202,11 +202,13 @@ int mxgemm_block128_quantize(const void* X, int64_t ldx, void* Q, float* S, void
   const bool few = rows && !cols && !square && L * p.Mb * p.Kb < 4LL * cus;
   p.tiles_m = few ? (int)cdiv(M, 16) : p.Mb;
   const int64_t grid = L * p.tiles_m * p.Kb;
-  p.blocks = (unsigned)grid;
   hipStream_t s = (hipStream_t)stream;
-  if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, few, rows, cols, square, grid, s);
-  else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, few, rows, cols, square, grid, s);
-  else launch_quantize<2>(p, fmt, few, rows, cols, square, grid, s);
+  launch_runs(grid, [&](int64_t first, unsigned count) {
+    p.first = (int)first;
+    if (x_dtype == MXG_DT_F32) launch_quantize<0>(p, fmt, few, rows, cols, square, count, s);
+    else if (x_dtype == MXG_DT_BF16) launch_quantize<1>(p, fmt, few, rows, cols, square, count, s);
+    else launch_quantize<2>(p, fmt, few, rows, cols, square, count, s);
+  });
   return hipGetLastError() == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 
@@ -268,8 +270,11 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
   const Choice ch = choose(M, N, K, L, exact);
   if (ch.rows) {
     p.tilesN = (int)cdiv(N, ch.rows);
-    p.num_tiles = (int)(L * p.tilesN);
-    const hipError_t e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.rows, grid_of(p.num_tiles), s);
+    hipError_t e = hipSuccess;
+    launch_runs(L * p.tilesN, [&](int64_t first, unsigned count) {
+      p.first = (int)first;
+      if (e == hipSuccess) e = mxg::b128::launch_rows(p, a_fmt, b_fmt, c_dtype, ch.rows, count, s);
+    });
     return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
   }
   p.tilesM = (int)cdiv(M, ch.bm);

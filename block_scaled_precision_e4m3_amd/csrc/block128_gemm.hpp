@@ -30,6 +30,7 @@ struct GemmParams {
   int steps, splits, per;  // steps of a tile's whole K; parts it is cut into, of `per` steps each (the last may be shorter)
   float* sums;       // splits > 1: (splits, L, M, ldw) float32 partial sums in place of C
   int ldw;
+  int first;         // kernel for few rows: the launch's first group of columns
   bool b_rows, accumulate;
   bool c_vec;        // base, ldc and N in multiples of 16 bytes: every store of C is a whole one
 };
@@ -695,9 +696,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
   __shared__ float lds[W][16 * MT][16 * NT + 4];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const unsigned item = blockIdx.y * gridDim.x + blockIdx.x;
-  if (item >= (unsigned)p.num_tiles) return;
-  const int l = (int)item / p.tilesN, n0 = ((int)item % p.tilesN) * COLS;
+  const int item = p.first + (int)blockIdx.x, l = item / p.tilesN, n0 = item % p.tilesN * COLS;
   const uint8_t* a[MT];
   const float* sa[MT];
 #pragma unroll

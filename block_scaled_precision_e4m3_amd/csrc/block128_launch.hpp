@@ -30,8 +30,8 @@ hipError_t launch_exact128x256(const GemmParams& p, int fa, int fb, int64_t grid
 hipError_t launch_exact128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 hipError_t launch_exact64x128(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
 hipError_t launch_exact64(const GemmParams& p, int fa, int fb, int64_t grid, hipStream_t s);
-// up to 32 rows; p.tilesN counts groups of `cols` (16 or 32) columns, p.num_tiles those of all batches
-hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int cols, dim3 grid, hipStream_t s);
+// up to 32 rows; p.tilesN counts groups of `cols` (16 or 32) columns
+hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int cols, unsigned grid, hipStream_t s);
 
 // f<FA, FB>(...) for the formats of A and B.
 template <class F>

@@ -50,7 +50,7 @@ struct QuantParams {
   int K16, M16;      // row lengths of Q and QT
   int Mb, Kb;        // ceil(M / 128), ceil(K / 128)
   int tiles_m;       // row tiles per batch
-  unsigned blocks;   // workgroups with a tile: all tiles
+  int first;         // the launch's first tile
   bool pow2;
 };
 
@@ -188,9 +188,7 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
   __shared__ float rowscale[ROWS && !SQUARE ? kRows : 1];
 
   const int tid = threadIdx.x, c = tid & 15, g = tid >> 4, wave = tid >> 6;
-  const unsigned item = blockIdx.y * gridDim.x + blockIdx.x;
-  if (item >= p.blocks) return;
-  int b = (int)item;
+  int b = p.first + (int)blockIdx.x;
   const int kb = b % p.Kb;
   b /= p.Kb;
   const int tm = b % p.tiles_m, l = b / p.tiles_m;

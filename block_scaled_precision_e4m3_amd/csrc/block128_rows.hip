@@ -7,8 +7,8 @@ namespace b128 {
 namespace {
 
 template <int FA, int FB, int CT, bool BROWS>
-void launch(const GemmParams& p, int cols, dim3 g, hipStream_t s) {
-  const dim3 b(64 * kRowWaves);
+void launch(const GemmParams& p, int cols, unsigned grid, hipStream_t s) {
+  const dim3 g(grid), b(64 * kRowWaves);
   if (p.M <= 16) {
     if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 1>), g, b, 0, s, p);
     else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 1>), g, b, 0, s, p);
@@ -20,7 +20,7 @@ void launch(const GemmParams& p, int cols, dim3 g, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int cols, dim3 grid, hipStream_t s) {
+hipError_t launch_rows(const GemmParams& p, int fa, int fb, int ct, int cols, unsigned grid, hipStream_t s) {
   return by_format(fa, fb, [&](auto a, auto c) {
     constexpr int FA = decltype(a)::value, FB = decltype(c)::value;
     if (ct == 0) {

@@ -32,7 +32,7 @@ int check(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t off
   if (flags & ~known) return MXG_ERR_FLAGS;
   if (!fits_i32(T) || !fits_i32(Hq + Hk) || Hq + Hk > (1 << 20) || !fits_i32(table)) return MXG_ERR_SHAPE;
   if (!positions && rot > 0 && T > table) return MXG_ERR_SHAPE;
-  // a wave takes a head of a token at least, four waves a workgroup
+  // a wave takes a head of a token at least
   if (T > 0 && Hq + Hk > (1LL << 36) / T) return MXG_ERR_SHAPE;
   if (!strides) return MXG_ERR_NULL;
   for (int i = 0; i < tensors; ++i) {
@@ -74,16 +74,19 @@ int64_t vector_parts(int64_t T) { return std::min<int64_t>(backward_parts(T), mx
 bool whole_chunks(const Params& p) { return p.D % 16 == 0 && p.rot % 16 == 0 && p.off % 8 == 0; }
 
 template <int DT, int MODE, bool IN, bool OUT>
-void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
-  const dim3 g = grid_of(grid);
-  if constexpr (MODE == mxg::heads::kBackward)
-    hipLaunchKernelGGL((mxg::heads::heads_backward_kernel<DT, IN, OUT>), g, dim3(64 * mxg::heads::kBackWaves), 0, s, p);
-  else
-    hipLaunchKernelGGL((mxg::heads::heads_kernel<DT, MODE, IN, OUT>), g, dim3(mxg::heads::kThreads), 0, s, p);
+void launch_heads(Params& p, int64_t grid, hipStream_t s) {
+  if constexpr (MODE == mxg::heads::kBackward) {
+    hipLaunchKernelGGL((mxg::heads::heads_backward_kernel<DT, IN, OUT>), dim3((unsigned)grid), dim3(64 * mxg::heads::kBackWaves), 0, s, p);
+  } else {
+    launch_runs(grid, [&](int64_t first, unsigned count) {
+      p.first = first * mxg::heads::kWaves;
+      hipLaunchKernelGGL((mxg::heads::heads_kernel<DT, MODE, IN, OUT>), dim3(count), dim3(mxg::heads::kThreads), 0, s, p);
+    });
+  }
 }
 
 template <int DT, int MODE>
-void launch_heads(const Params& p, int64_t grid, hipStream_t s) {
+void launch_heads(Params& p, int64_t grid, hipStream_t s) {
   if (p.halves_in && p.halves_out) launch_heads<DT, MODE, true, true>(p, grid, s);
   else if (p.halves_out) launch_heads<DT, MODE, false, true>(p, grid, s);
   else if (!p.halves_in) launch_heads<DT, MODE, false, false>(p, grid, s);

@@ -56,6 +56,7 @@ struct Params {
   float sign;         // -1: the transposed rotation (rope only)
   // vector kernel: lanes per row, rows per wave, groups of rows of q and k per token, groups per wave
   int lpr, rpw, groups[2], gpw;
+  int64_t first;      // the launch's first work item
 };
 
 // The position of token t as a table row, -1 if it lies outside the table.
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(Params p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int all = p.groups[0] + p.groups[1], parts = (all + p.gpw - 1) / p.gpw;
-  const int64_t item = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + wave;
+  const int64_t item = p.first + (int64_t)blockIdx.x * kWaves + wave;
   const int64_t t = item / parts;
   if (t >= p.T) return;
   const int first = (int)(item - t * parts) * p.gpw, last = min(first + p.gpw, all);

@@ -29,12 +29,13 @@ inline bool fits_i32(int64_t v) { return v >= 0 && v <= 0x7FFFFFFFLL; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A launch of `blocks` workgroups (fewer than 2^35) as a grid of two dimensions, whose kernel takes workgroup y * grid.x + x and
-// leaves out those past the last one.  A dimension has fewer than 2^32 work items; a launch of more is not refused but
-// runs the remainder by 2^32 alone.
-inline dim3 grid_of(int64_t blocks) {
-  constexpr int64_t kRow = 1 << 20;
-  return blocks <= kRow ? dim3((unsigned)blocks) : dim3((unsigned)kRow, (unsigned)cdiv(blocks, kRow));
+// launch(first, count) for `blocks` workgroups in runs of 2^22 at most, for kernels of up to 512 threads.  A launch has
+// fewer than 2^32 work items in a dimension; one of more is not refused but runs the remainder by 2^32 alone.  (Two
+// dimensions in place of runs cost every call of the quantiser 0.2 to 0.4 us.)
+template <class F>
+inline void launch_runs(int64_t blocks, F launch) {
+  constexpr int64_t kRun = 1 << 22;
+  for (int64_t first = 0; first < blocks; first += kRun) launch(first, (unsigned)(blocks - first < kRun ? blocks - first : kRun));
 }
 
 // Current device must be gfx950; returns its CU count through *cus.
