@@ -25,12 +25,12 @@ using mxg::heads::Tensor;
 int check(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t off, int64_t table, bool positions,
           int layout, int dtype, int w_dtype, unsigned flags, unsigned known, const int64_t* strides, int tensors) {
   if (T < 0 || Hq < 0 || Hk < 0 || D < 1 || D > mxg::heads::kMaxD) return MXG_ERR_SHAPE;
-  if (rot < 0 || rot % 2 != 0 || off < 0 || rot + off > D || table < 0) return MXG_ERR_SHAPE;
+  if (rot < 0 || rot % 2 != 0 || off < 0 || rot > D || off > D - rot || table < 0) return MXG_ERR_SHAPE;
   if (layout < MXG_ROPE_HALF || layout > MXG_ROPE_INTERLEAVED_TO_HALF) return MXG_ERR_FMT;
   if (dtype < MXG_DT_F32 || dtype > MXG_DT_F16) return MXG_ERR_FMT;
   if (w_dtype != dtype && w_dtype != MXG_DT_F32) return MXG_ERR_FMT;
   if (flags & ~known) return MXG_ERR_FLAGS;
-  if (!fits_i32(T) || !fits_i32(Hq + Hk) || Hq + Hk > (1 << 20) || !fits_i32(table)) return MXG_ERR_SHAPE;
+  if (!fits_i32(T) || Hq > (1 << 20) || Hk > (1 << 20) - Hq || !fits_i32(table)) return MXG_ERR_SHAPE;
   if (!positions && rot > 0 && T > table) return MXG_ERR_SHAPE;
   // a wave takes a head of a token at least
   if (T > 0 && Hq + Hk > (1LL << 36) / T) return MXG_ERR_SHAPE;

@@ -180,3 +180,13 @@ def test_more_heads_than_a_launch_has_waves(lib):
     for T, H, want in ((1 << 30, 1 << 6, lib.MXG_ERR_DEVICE), (1 << 30, (1 << 6) + 1, lib.MXG_ERR_SHAPE),
                        ((1 << 31) - 1, 1 << 20, lib.MXG_ERR_SHAPE)):
         assert f(GOOD, GOOD, GOOD, GOOD, GOOD, STRIDES, T, H, 128, 64, 0, 4, 0, 1, 0, None) == want, (T, H)
+
+
+def test_sums_of_arguments_that_overflow(lib):
+    """The end of the rotary part and the number of heads are not taken in arithmetic that overflows."""
+    f, n = lib._lib.mxgemm_rope, lib._lib.mxgemm_qk_norm_rope
+    for rot, off in ((64, (1 << 63) - 1), (64, (1 << 63) - 64), (1 << 62, 1 << 62), ((1 << 63) - 2, 2), (128, 1), (130, 0)):
+        assert f(GOOD, GOOD, GOOD, GOOD, GOOD, STRIDES, 4, 4, 128, rot, off, 4, 0, 1, 0, None) == lib.MXG_ERR_SHAPE, (rot, off)
+        assert n(*[GOOD] * 9, STRIDES, 4, 4, 2, 128, rot, off, 4, 1e-6, 0, 1, 1, 0, None) == lib.MXG_ERR_SHAPE, (rot, off)
+    for hq, hk in ((1 << 62, 1 << 62), ((1 << 63) - 1, (1 << 63) - 1), (1 << 20, 1), (1, 1 << 20)):
+        assert n(*[GOOD] * 9, STRIDES, 4, hq, hk, 128, 64, 0, 4, 1e-6, 0, 1, 1, 0, None) == lib.MXG_ERR_SHAPE, (hq, hk)
