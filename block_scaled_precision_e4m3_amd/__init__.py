@@ -268,6 +268,13 @@ def _as_lrk(t, name):
                                           f"m-major (strides (1, rows, rows*K)), batch outermost")
 
 
+def _workspace_bytes(t):
+    """The bytes of a given workspace: those that its memory has, which an expanded tensor's element count is not."""
+    if not t.is_contiguous():
+        raise MxgemmValueError(MXG_ERR_ALIGN, "workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def proj_rope_mxfp8(y, cos, sin, num_heads, head_dim=192, qk_rope=64, stream=None, out=None):
     """C-ABI mxgemm_proj_rope_mxfp8 on torch tensors: y (tokens, num_heads * head_dim) float32, cos / sin
     (tokens, qk_rope) bfloat16.  Returns (out_fp8_row, out_scales_row, out_fp8_col, out_scales_col) as the
@@ -335,7 +342,8 @@ def projection_mxfp8(x, w, x_scale, w_scale, cos, sin, num_heads, head_dim=192, 
     out = _proj_outputs(tokens, num_heads, head_dim, x.device, out)
     st = _lib.mxgemm_projection_mxfp8(_ptr(x), _ptr(w), _ptr(x_scale), _ptr(w_scale), _ptr(cos), _ptr(sin),
                                       _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), tokens, num_heads,
-                                      head_dim, qk_rope, k, _ptr(workspace), workspace.numel(), _stream(stream))
+                                      head_dim, qk_rope, k, _ptr(workspace), _workspace_bytes(workspace),
+                                      _stream(stream))
     if st != MXG_OK:
         _raise(st)
     return out
@@ -708,16 +716,16 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
     ct = e.dt.get(c_dtype)
     if ct is None:
         _refuse(MXG_ERR_FMT, "c must be float32, bfloat16 or float16")
+    given = 0 if workspace is None else _workspace_bytes(workspace)
     _here(a.get_device(), sa, b, sb, c, workspace)
     if c is None:
         c = _empty(e, lead + (m, n), c_dtype, a.device, stream)
     need = _lib.mxgemm_block128_workspace_bytes(m, n, k, l, ct)
     if need and workspace is None:
-        workspace = _empty(e, (need,), e.u8, a.device, stream)
+        workspace, given = _empty(e, (need,), e.u8, a.device, stream), need
     st = _lib.mxgemm_block128(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), c.data_ptr(), ldc, m, n, k, l,
                               fa, fb, ct, (MXG_B128_B_ROWS if b_block == 1 else 0)
-                              | (MXG_B128_ACCUMULATE if accumulate else 0) | MXG_TRUSTED_POINTERS, _ptr(workspace),
-                              workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                              | (MXG_B128_ACCUMULATE if accumulate else 0) | MXG_TRUSTED_POINTERS, _ptr(workspace), given,
                               _stream(stream))
     if st != MXG_OK:
         _raise(st)
@@ -939,6 +947,7 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, 
     wdt = _weights(e, q_weight, k_weight, q, k)
     rot, rows, lay, flags = _rotary(e, cos, sin, positions, t, layout)
     dev = q.get_device()
+    given = 0 if workspace is None else _workspace_bytes(workspace)
     _here(dev, k, dq, dk, q_weight, k_weight, cos, sin, positions, workspace)
     xq, xk, xqs, xks = _pair(e, out, q, k, kh, ("dq_in", "dk_in"), stream)
     if out is not None:
@@ -946,14 +955,13 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, 
     dwq = _empty(e, (d,), e.f32, q.device, stream)
     dwk = None if k is None else _empty(e, (d,), e.f32, q.device, stream)
     if workspace is None:
-        need = _lib.mxgemm_qk_norm_rope_backward_workspace_bytes(t, d)
-        workspace = _empty(e, (need,), e.u8, q.device, stream)
+        given = _lib.mxgemm_qk_norm_rope_backward_workspace_bytes(t, d)
+        workspace = _empty(e, (given,), e.u8, q.device, stream)
     st = _lib.mxgemm_qk_norm_rope_backward(
         dq.data_ptr(), _ptr(dk), q.data_ptr(), _ptr(k), xq.data_ptr(), _ptr(xk), dwq.data_ptr(), _ptr(dwk),
         q_weight.data_ptr(), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
         _Strides12(gqs[0], gqs[1], gks[0], gks[1], qs[0], qs[1], ks[0], ks[1], xqs[0], xqs[1], xks[0], xks[1]), t, hq, hk,
-        d, rot, rot_offset, rows, eps, lay, dt, wdt, flags, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        d, rot, rot_offset, rows, eps, lay, dt, wdt, flags, workspace.data_ptr(), given, _stream(stream))
     if st != MXG_OK:
         _raise(st)
     return xq, xk, dwq, dwk

@@ -190,3 +190,19 @@ def test_sums_of_arguments_that_overflow(lib):
         assert n(*[GOOD] * 9, STRIDES, 4, 4, 2, 128, rot, off, 4, 1e-6, 0, 1, 1, 0, None) == lib.MXG_ERR_SHAPE, (rot, off)
     for hq, hk in ((1 << 62, 1 << 62), ((1 << 63) - 1, (1 << 63) - 1), (1 << 20, 1), (1, 1 << 20)):
         assert n(*[GOOD] * 9, STRIDES, 4, hq, hk, 128, 64, 0, 4, 1e-6, 0, 1, 1, 0, None) == lib.MXG_ERR_SHAPE, (hq, hk)
+
+
+def test_workspaces_must_have_the_memory_they_count(lib):
+    """An expanded tensor counts one element many times."""
+    import torch
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 30)
+    q, s = torch.zeros(64, 7168, dtype=torch.float8_e4m3fn), torch.ones(56, 64)
+    h, w = torch.zeros(3, 2, 16), torch.ones(16)
+    x, xs = torch.zeros(32, 64, dtype=torch.float8_e4m3fn), torch.zeros(32, 2, dtype=torch.uint8)
+    table = torch.zeros(32, 64, dtype=torch.bfloat16)
+    out = tuple(torch.zeros(1) for _ in range(4))
+    for bad in (lambda: lib.block128_gemm(q, s, q, s, b_block=1, workspace=ws),
+                lambda: lib.qk_norm_rope_backward(h, h, h, h, w, w, workspace=ws),
+                lambda: lib.projection_mxfp8(x, x, xs, xs, table, table, 1, 64, 64, workspace=ws, out=out)):
+        with pytest.raises(lib.MxgemmValueError, match="workspace"):
+            bad()
