@@ -561,9 +561,28 @@ def _here(dev, *tensors):
         _raise(MXG_ERR_DEVICE)
 
 
-def _empty(e, shape, dtype, device, stream):
-    """A new contiguous tensor for a kernel on `stream`: its memory is not handed out again before that stream is done
-    with it."""
+def _new(make, stream, device, scratch=False):
+    """make(), a new tensor, for a call on `stream`.  Its memory (and a fill of it) belongs to that stream: memory that
+    Python has freed on the current stream may still be in use there by work that is queued, and only what is queued
+    after that work may write it.  The caller may use the tensor on the current stream, so that one is waited for, too,
+    before its memory is handed out again; a scratch tensor only ever meets `stream`."""
+    if stream is None:
+        return make()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if not scratch:
+        t.record_stream(here)
+    return t
+
+
+def _empty(e, shape, dtype, device, stream, scratch=False):
+    """A new contiguous tensor for a kernel on `stream`."""
     n = len(shape)
     if n == 2:
         strides = (shape[1] or 1, 1)
@@ -572,12 +591,7 @@ def _empty(e, shape, dtype, device, stream):
         strides = (b * c, c, 1)
     else:
         strides = (1,)
-    t = e.empty(shape, strides, dtype=dtype, device=device)
-    if stream is not None:
-        s = e.torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-        if s != e.torch.cuda.current_stream(t.device):
-            t.record_stream(s)
-    return t
+    return _new(lambda: e.empty(shape, strides, dtype=dtype, device=device), stream, device, scratch)
 
 
 def _expect(t, shape, dtype, name):
@@ -722,7 +736,7 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
         c = _empty(e, lead + (m, n), c_dtype, a.device, stream)
     need = _lib.mxgemm_block128_workspace_bytes(m, n, k, l, ct)
     if need and workspace is None:
-        workspace, given = _empty(e, (need,), e.u8, a.device, stream), need
+        workspace, given = _empty(e, (need,), e.u8, a.device, stream, True), need
     st = _lib.mxgemm_block128(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), c.data_ptr(), ldc, m, n, k, l,
                               fa, fb, ct, (MXG_B128_B_ROWS if b_block == 1 else 0)
                               | (MXG_B128_ACCUMULATE if accumulate else 0) | MXG_TRUSTED_POINTERS, _ptr(workspace), given,
@@ -956,7 +970,7 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, 
     dwk = None if k is None else _empty(e, (d,), e.f32, q.device, stream)
     if workspace is None:
         given = _lib.mxgemm_qk_norm_rope_backward_workspace_bytes(t, d)
-        workspace = _empty(e, (given,), e.u8, q.device, stream)
+        workspace = _empty(e, (given,), e.u8, q.device, stream, True)
     st = _lib.mxgemm_qk_norm_rope_backward(
         dq.data_ptr(), _ptr(dk), q.data_ptr(), _ptr(k), xq.data_ptr(), _ptr(xk), dwq.data_ptr(), _ptr(dwk),
         q_weight.data_ptr(), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
