@@ -190,6 +190,26 @@ def _bind_stream(torch):
         _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def _new(make, stream, device, scratch=False):
+    """make(), a new tensor, for a call on `stream`.  Its memory (and a fill of it) belongs to that stream: memory that
+    Python has freed on the current stream may still be in use there by work that is queued, and only what is queued
+    after that work may write it.  The caller may use the tensor on the current stream, so that one is waited for, too,
+    before its memory is handed out again; a scratch tensor only ever meets `stream`."""
+    if stream is None:
+        return make()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if not scratch:
+        t.record_stream(here)
+    return t
+
+
 def mxgemm_strerror(status):
     return _lib.mxgemm_strerror(int(status)).decode()
 
@@ -282,14 +302,8 @@ def proj_rope_mxfp8(y, cos, sin, num_heads, head_dim=192, qk_rope=64, stream=Non
     (tokens/32, H, D); `out` may hold those four tensors preallocated."""
     import torch
     tokens = y.shape[0]
-    if out is None:
-        dev = y.device
-        out = (torch.empty((tokens, num_heads, head_dim), dtype=torch.float8_e4m3fn, device=dev),
-               torch.empty((tokens, num_heads, head_dim // 32), dtype=torch.uint8, device=dev),
-               torch.empty((tokens, num_heads, head_dim), dtype=torch.float8_e4m3fn, device=dev),
-               torch.empty((tokens // 32, num_heads, head_dim), dtype=torch.uint8, device=dev))
-    for t, name in ((y, "y"), (cos, "cos"), (sin, "sin")) + tuple(zip(out, ("row", "row scales", "col",
-                                                                         "col scales"))):
+    out = _proj_outputs(tokens, num_heads, head_dim, y.device, out, stream)
+    for t, name in ((y, "y"), (cos, "cos"), (sin, "sin")):
         if not t.is_contiguous():
             raise MxgemmValueError(MXG_ERR_ALIGN, f"{name} must be contiguous")
     if y.dtype != torch.float32 or cos.dtype != torch.bfloat16 or sin.dtype != torch.bfloat16:
@@ -301,13 +315,12 @@ def proj_rope_mxfp8(y, cos, sin, num_heads, head_dim=192, qk_rope=64, stream=Non
     return out
 
 
-def _proj_outputs(tokens, num_heads, head_dim, dev, out):
+def _proj_outputs(tokens, num_heads, head_dim, dev, out, stream):
     import torch
     if out is None:
-        out = (torch.empty((tokens, num_heads, head_dim), dtype=torch.float8_e4m3fn, device=dev),
-               torch.empty((tokens, num_heads, head_dim // 32), dtype=torch.uint8, device=dev),
-               torch.empty((tokens, num_heads, head_dim), dtype=torch.float8_e4m3fn, device=dev),
-               torch.empty((tokens // 32, num_heads, head_dim), dtype=torch.uint8, device=dev))
+        out = tuple(_new(lambda: torch.empty((rows, num_heads, cols), dtype=dtype, device=dev), stream, dev)
+                    for rows, cols, dtype in ((tokens, head_dim, torch.float8_e4m3fn), (tokens, head_dim // 32, torch.uint8),
+                                              (tokens, head_dim, torch.float8_e4m3fn), (tokens // 32, head_dim, torch.uint8)))
     for t, name in zip(out, ("row", "row scales", "col", "col scales")):
         if not t.is_contiguous():
             raise MxgemmValueError(MXG_ERR_ALIGN, f"{name} must be contiguous")
@@ -319,7 +332,7 @@ def gemm_rope_mxfp8(A, B, SFA, SFB, cos, sin, tokens, num_heads, head_dim, qk_ro
     """C-ABI mxgemm_gemm_rope_mxfp8: the projection GEMM with RoPE and dual-direction MXFP8 fused into its
     epilogue, on k-major codes A (tokens, K) / B (num_heads * head_dim, K) and atom-layout scales.  Returns
     (out_fp8_row, out_scales_row, out_fp8_col, out_scales_col) shaped as proj_rope_mxfp8's."""
-    out = _proj_outputs(tokens, num_heads, head_dim, A.device, out)
+    out = _proj_outputs(tokens, num_heads, head_dim, A.device, out, stream)
     st = _lib.mxgemm_gemm_rope_mxfp8(_ptr(A), _ptr(B), _ptr(SFA), _ptr(SFB), _ptr(cos), _ptr(sin), _ptr(out[0]),
                                      _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), tokens, num_heads, head_dim, qk_rope,
                                      K, sf_vec_size, a_fmt, b_fmt, _stream(stream))
@@ -338,8 +351,8 @@ def projection_mxfp8(x, w, x_scale, w_scale, cos, sin, num_heads, head_dim=192, 
     tokens, k = x.shape
     need = _lib.mxgemm_projection_workspace_bytes(tokens, num_heads, head_dim, k)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    out = _proj_outputs(tokens, num_heads, head_dim, x.device, out)
+        workspace = _new(lambda: torch.empty(need, dtype=torch.uint8, device=x.device), stream, x.device, True)
+    out = _proj_outputs(tokens, num_heads, head_dim, x.device, out, stream)
     st = _lib.mxgemm_projection_mxfp8(_ptr(x), _ptr(w), _ptr(x_scale), _ptr(w_scale), _ptr(cos), _ptr(sin),
                                       _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), tokens, num_heads,
                                       head_dim, qk_rope, k, _ptr(workspace), _workspace_bytes(workspace),
@@ -355,7 +368,7 @@ def projection_mxfp8_noalloc(x, w, x_scale, w_scale, cos, sin, num_heads, head_d
     fixed per-device scratch array (nothing is allocated; `out` must then be given by a caller that cannot
     allocate either).  Calls that overlap on one device race."""
     tokens, k = x.shape
-    out = _proj_outputs(tokens, num_heads, head_dim, x.device, out)
+    out = _proj_outputs(tokens, num_heads, head_dim, x.device, out, stream)
     st = _lib.mxgemm_projection_mxfp8_noalloc(_ptr(x), _ptr(w), _ptr(x_scale), _ptr(w_scale), _ptr(cos),
                                               _ptr(sin), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
                                               tokens, num_heads, head_dim, qk_rope, k, _stream(stream))
@@ -407,21 +420,23 @@ def gemm_amax(a, b, sfa, sfb, c=None, amax=None, sf_vec_size=32, stream=None, ac
         raise MxgemmValueError(MXG_ERR_FLAGS, f"c_major must be 'n' or 'm', got {c_major!r}")
     if c_major == "m":
         if c is None:
-            c = torch.empty((l, n, m), dtype=c_dtype or torch.float32, device=a.device).permute(2, 1, 0)
+            c = _new(lambda: torch.empty((l, n, m), dtype=c_dtype or torch.float32, device=a.device), stream,
+                     a.device).permute(2, 1, 0)
         c_base = c.permute(2, 1, 0) if c.dim() == 3 else c.t().unsqueeze(0)
         c_flag = MXG_FLAG_C_MMAJOR if c.dtype == torch.float32 else None
         if c_flag is None or not c_base.is_contiguous():
             raise MxgemmValueError(MXG_ERR_ALIGN, "m-major C must be float32 (M, N, L) with strides (1, M, M*N)")
     else:
         if c is None:
-            c = torch.empty((l, m, n), dtype=c_dtype or torch.float32, device=a.device).permute(1, 2, 0)
+            c = _new(lambda: torch.empty((l, m, n), dtype=c_dtype or torch.float32, device=a.device), stream,
+                     a.device).permute(1, 2, 0)
         c_base = c.permute(2, 0, 1) if c.dim() == 3 else c.unsqueeze(0)
         c_flag = {torch.float32: 0, torch.bfloat16: MXG_FLAG_C_BF16, torch.float16: MXG_FLAG_C_F16}.get(c.dtype)
         if c_flag is None or not c_base.is_contiguous():
             raise MxgemmValueError(MXG_ERR_ALIGN, "C must be float32, bfloat16 or float16, n-major (M, N, L) with "
                                                   "strides (N, 1, M*N)")
     if amax is None:
-        amax = torch.zeros((1, 1, 1), dtype=torch.float32, device=a.device)
+        amax = _new(lambda: torch.zeros((1, 1, 1), dtype=torch.float32, device=a.device), stream, a.device)
     flags = (MXG_FLAG_AMAX_ACCUMULATE if accumulate else 0) | (MXG_FLAG_FP8_MFMA if fp8_mfma else 0) | c_flag | \
         (MXG_FLAG_A_MMAJOR if a_mm else 0) | (MXG_FLAG_B_NMAJOR if b_mm else 0)
     mxgemm_amax_ex(a_base, b_base, sfa_p, sfb_p, c_base, amax, m, n, k, l, sf_vec_size, fa, fb, flags, stream)
@@ -479,7 +494,7 @@ def sf_from_rowwise(rowwise, k, sf_vec_size=32, sf=None, stream=None):
                                               f"{-(-k // sf_vec_size)}")
     shape = (l, -(-mn // 128), -(-k // (4 * sf_vec_size)), 32, 4, 4)
     if sf is None:
-        sf = torch.empty(shape, dtype=torch.uint8, device=rowwise.device)
+        sf = _new(lambda: torch.empty(shape, dtype=torch.uint8, device=rowwise.device), stream, rowwise.device)
     if sf.numel() != 512 * shape[0] * shape[1] * shape[2] or not sf.is_contiguous():
         raise MxgemmValueError(MXG_ERR_SHAPE, "sf must be a contiguous buffer of the atom layout's size")
     mxgemm_sf_rowwise_to_atoms(rowwise, sf, mn, k, l, sf_vec_size, stream)
@@ -500,9 +515,9 @@ def mx_quantize(x, sf_vec_size=32, fmt=MXG_FMT_E4M3, q=None, sf=None, stream=Non
     l, mn, k = (1,) + tuple(x.shape) if x.dim() == 2 else tuple(x.shape)
     shape = (l, -(-mn // 128), -(-k // (4 * sf_vec_size)), 32, 4, 4)
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        q = _new(lambda: torch.empty(x.shape, dtype=torch.uint8, device=x.device), stream, x.device)
     if sf is None:
-        sf = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        sf = _new(lambda: torch.empty(shape, dtype=torch.uint8, device=x.device), stream, x.device)
     if q.numel() != x.numel() or not q.is_contiguous() or q.element_size() != 1:
         raise MxgemmValueError(MXG_ERR_SHAPE, "q must be a contiguous one-byte tensor with x's element count")
     if sf.numel() != 512 * shape[0] * shape[1] * shape[2] or not sf.is_contiguous():
@@ -559,26 +574,6 @@ def _here(dev, *tensors):
             _raise(MXG_ERR_DEVICE)
     if dev < 0 or dev != (_current_device or _env.torch.cuda.current_device)():
         _raise(MXG_ERR_DEVICE)
-
-
-def _new(make, stream, device, scratch=False):
-    """make(), a new tensor, for a call on `stream`.  Its memory (and a fill of it) belongs to that stream: memory that
-    Python has freed on the current stream may still be in use there by work that is queued, and only what is queued
-    after that work may write it.  The caller may use the tensor on the current stream, so that one is waited for, too,
-    before its memory is handed out again; a scratch tensor only ever meets `stream`."""
-    if stream is None:
-        return make()
-    import torch
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-    here = torch.cuda.current_stream(device)
-    if stream == here:
-        return make()
-    with torch.cuda.stream(stream):
-        t = make()
-    if not scratch:
-        t.record_stream(here)
-    return t
 
 
 def _empty(e, shape, dtype, device, stream, scratch=False):

@@ -22,6 +22,10 @@ def nbytes(t):
     return t.numel() * t.element_size()
 
 
+def raw(t):
+    return t.contiguous().reshape(-1).view(torch.uint8)
+
+
 def check(call, scratch=()):
     """call(stream=s) gives what it gives on the current stream, and work that was queued before it keeps its memory.
 
@@ -50,7 +54,7 @@ def check(call, scratch=()):
         s.synchronize()
         torch.cuda.synchronize()
         for g, w in zip([t for t in got if t is not None], want):
-            assert torch.equal(g.contiguous().view(torch.uint8), w.contiguous().view(torch.uint8))
+            assert torch.equal(raw(g), raw(w))
         for k in kept:
             assert torch.all(k == 0x5A).item()
         # and when they are freed while the current stream still reads them, the next call there leaves them alone
@@ -61,7 +65,7 @@ def check(call, scratch=()):
         again = call(stream=s)
         torch.cuda.synchronize()
         for c, w in zip(copies, want):
-            assert torch.equal(c.contiguous().view(torch.uint8), w.contiguous().view(torch.uint8))
+            assert torch.equal(raw(c), raw(w))
         del again
 
 
@@ -103,3 +107,30 @@ def test_default_stream_by_its_handle(lib):
         got = lib.rope(x, cos, sin, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_mx_quantize_and_gemm_amax(lib):
+    M, N, K = 512, 768, 1024
+    x, w = normal(M, K), normal(N, K, seed=1)
+    check(lambda **kw: lib.mx_quantize(x, **kw))
+    (a, sfa), (b, sfb) = lib.mx_quantize(x), lib.mx_quantize(w)
+    a, b = a.view(torch.float8_e4m3fn), b.view(torch.float8_e4m3fn)
+    check(lambda **kw: lib.gemm_amax(a, b, sfa, sfb, **kw))
+    check(lambda **kw: lib.gemm_amax(a, b, sfa, sfb, c_major="m", accumulate=True, **kw))
+    rowwise = torch.randint(120, 130, (M, K // 32), dtype=torch.uint8, device="cuda")
+    check(lambda **kw: (lib.sf_from_rowwise(rowwise, K, **kw),))
+
+
+def test_projection(lib):
+    tokens, heads, d, qr, K = 256, 4, 192, 64, 512
+    code = lambda *s: torch.randint(0, 120, s, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)  # noqa: E731
+    scale = lambda *s: torch.randint(120, 130, s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    x, w, xs, ws = code(tokens, K), code(heads * d, K), scale(tokens, K // 32), scale(heads * d, K // 32)
+    cos, sin = normal(tokens, qr).bfloat16(), normal(tokens, qr, seed=1).bfloat16()
+    need = lib._lib.mxgemm_projection_workspace_bytes(tokens, heads, d, K)
+    check(lambda **kw: lib.projection_mxfp8(x, w, xs, ws, cos, sin, heads, d, qr, **kw), [need])
+    check(lambda **kw: lib.projection_mxfp8_noalloc(x, w, xs, ws, cos, sin, heads, d, qr, **kw))
+    sfa, sfb = lib.sf_from_rowwise(xs, K), lib.sf_from_rowwise(ws, K)
+    check(lambda **kw: lib.gemm_rope_mxfp8(x, w, sfa, sfb, cos, sin, tokens, heads, d, qr, K, **kw))
+    y = normal(tokens, heads * d)
+    check(lambda **kw: lib.proj_rope_mxfp8(y, cos, sin, heads, d, qr, **kw))
