@@ -751,8 +751,10 @@ def rope_table(length, rot, base=10000.0, scaling="none", factor=1.0, original_l
     "linear": every frequency divided by factor;
     "ntk": base raised so that the slowest pair is stretched by factor and the fastest kept;
     "yarn": pairs that turn more than beta_fast times within original_length are kept, those below beta_slow
-    turns are divided by factor, a linear ramp over the pair index in between, and cos and sin are multiplied by
-    0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models", 2023)."""
+    turns are divided by factor, a linear ramp over the pair index in between (from the pair index of beta_fast turns,
+    rounded down and not below 0, to that of beta_slow turns, rounded up and not above rot - 1), and cos and sin are
+    multiplied by 0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models",
+    2023)."""
     import numpy as np
     import torch
     if length < 0 or rot < 0 or rot % 2:
@@ -770,7 +772,8 @@ def rope_table(length, rot, base=10000.0, scaling="none", factor=1.0, original_l
         # the (fractional) pair that turns a number of times within the original length
         def pair(turns):
             return rot * np.log(original_length / (turns * 2 * np.pi)) / (2 * np.log(base))
-        lo, hi = max(np.floor(pair(beta_fast)), 0.0), min(np.ceil(pair(beta_slow)), rot // 2 - 1.0)
+        # its ends may lie past the last pair, which is then stretched by a part of factor only
+        lo, hi = max(np.floor(pair(beta_fast)), 0.0), min(np.ceil(pair(beta_slow)), rot - 1.0)
         ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
         freq = freq * (1 - ramp) + freq / factor * ramp
         m = 0.1 * np.log(factor) + 1.0 if factor > 1 else 1.0

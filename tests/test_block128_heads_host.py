@@ -206,3 +206,28 @@ def test_workspaces_must_have_the_memory_they_count(lib):
                 lambda: lib.projection_mxfp8(x, x, xs, xs, table, table, 1, 64, 64, workspace=ws, out=out)):
         with pytest.raises(lib.MxgemmValueError, match="workspace"):
             bad()
+
+
+@pytest.mark.parametrize("length,rot,base,factor", [(4096, 64, 1e4, 4.0), (32768, 128, 1e6, 4.0), (65536, 128, 1e4, 4.0),
+                                                    (131072, 128, 1e4, 4.0), (4096, 128, 500.0, 4.0), (8192, 32, 1e4, 16.0),
+                                                    (1 << 20, 128, 100.0, 2.0), (100, 16, 1e4, 8.0)])
+def test_yarn_ramp(lib, length, rot, base, factor):
+    """Every pair's frequency, read off position 1 of the table, against turns = length base^(-2i/rot) / (2 pi): kept above
+    32 turns, divided by the factor below one, the ramp between the pairs where the (real) pair index has 32 turns and
+    one, those rounded outwards."""
+    cos, sin = lib.rope_table(2, rot, base=base, scaling="yarn", factor=factor, original_length=length, device="cpu")
+    got = np.arctan2(sin[1].double().numpy(), cos[1].double().numpy())
+    index = lambda turns: math.log(length / (2 * math.pi * turns)) * rot / (2 * math.log(base))  # noqa: E731
+    lo, hi = max(math.floor(index(32.0)), 0), min(math.ceil(index(1.0)), rot - 1)
+    for i in range(rot // 2):
+        freq = base ** (-2 * i / rot)
+        turns = length * freq / (2 * math.pi)
+        part = min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(i > lo)
+        want = freq * (1 - part) + freq / factor * part
+        # float32 sine and cosine: 2^-24 of their length in either, and in the angle
+        assert abs(got[i] - want) <= 2.0 ** -23, (i, turns)
+        if turns >= 32:
+            assert abs(got[i] - freq) <= 2.0 ** -23
+        if turns < 1:
+            assert part > 0.9, (i, turns)
+        assert part < 1 or turns < 1 or i >= hi
