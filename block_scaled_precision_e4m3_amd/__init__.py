@@ -705,6 +705,8 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
         _refuse(MXG_ERR_SHAPE, f"a and b disagree on K: {k} and {bh[-1]}")
     if b_block not in (1, 128):
         _refuse(MXG_ERR_SHAPE, "b_block must be 1 or 128")
+    if sa is None or sb is None:
+        _refuse(MXG_ERR_NULL, "sa and sb must be given")
     kb = -(-k // 128)
     _expect(sa, lead + (kb, m), e.f32, "sa")
     _expect(sb, lead + ((kb, n) if b_block == 1 else (-(-n // 128), kb)), e.f32, "sb")
@@ -894,6 +896,8 @@ def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=Fal
 
 def _weights(e, q_weight, k_weight, q, k):
     """MXG_DT_* of the norm weights."""
+    if q_weight is None or (k is not None and k_weight is None):
+        _refuse(MXG_ERR_NULL, "q_weight must be given, and k_weight with k")
     d, w_dtype = q.shape[2], q_weight.dtype
     if w_dtype not in (q.dtype, e.f32) or (k is not None and k_weight.dtype != w_dtype):
         _refuse(MXG_ERR_FMT, "weights must both be float32 or of the dtype of q and k")

@@ -231,3 +231,15 @@ def test_yarn_ramp(lib, length, rot, base, factor):
         if turns < 1:
             assert part > 0.9, (i, turns)
         assert part < 1 or turns < 1 or i >= hi
+
+
+def test_missing_weights_and_scales(lib):
+    import torch
+    h, w = torch.zeros(3, 2, 8), torch.ones(8)
+    q, s = torch.zeros(4, 32, dtype=torch.float8_e4m3fn), torch.ones(1, 4)
+    for bad in (lambda: lib.qk_norm_rope(h, h, w, None), lambda: lib.qk_norm_rope(h, h, None, w), lambda: lib.qk_norm_rope(h, None, None, None),
+                lambda: lib.qk_norm_rope_backward(h, h, h, h, w, None), lambda: lib.qk_norm_rope_backward(h, h, h, h, None, w),
+                lambda: lib.block128_gemm(q, None, q, s, b_block=1), lambda: lib.block128_gemm(q, s, q, None)):
+        with pytest.raises(lib.MxgemmValueError) as e:
+            bad()
+        assert e.value.status == lib.MXG_ERR_NULL
