@@ -589,6 +589,13 @@ def _empty(e, shape, dtype, device, stream, scratch=False):
     return _new(lambda: e.empty(shape, strides, dtype=dtype, device=device), stream, device, scratch)
 
 
+def _changed(e, *tensors):
+    """Tensors of the caller's that a call has written: autograd must not take them for what they were."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            e.torch.autograd.graph.increment_version(t)
+
+
 def _expect(t, shape, dtype, name):
     """Checks of a contiguous operand or output given by the caller."""
     if t.shape != shape:
@@ -675,6 +682,8 @@ def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, 
                                            | MXG_TRUSTED_POINTERS, _stream(stream))
     if status != MXG_OK:
         _raise(status)
+    if out is not None:
+        _changed(e, q, s, qt, st)
     return q, s, qt, st
 
 
@@ -729,7 +738,8 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
         _refuse(MXG_ERR_FMT, "c must be float32, bfloat16 or float16")
     given = 0 if workspace is None else _workspace_bytes(workspace)
     _here(a.get_device(), sa, b, sb, c, workspace)
-    if c is None:
+    own = c is None
+    if own:
         c = _empty(e, lead + (m, n), c_dtype, a.device, stream)
     need = _lib.mxgemm_block128_workspace_bytes(m, n, k, l, ct)
     if need and workspace is None:
@@ -740,6 +750,8 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
                               _stream(stream))
     if st != MXG_OK:
         _raise(st)
+    if not own:
+        _changed(e, c)
     return c
 
 
@@ -883,7 +895,8 @@ def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=Fal
     if out is not None:
         os_ = _like(out, x, sh, "out")
     _here(x.get_device(), cos, sin, positions, out)
-    if out is None:
+    own = out is None
+    if own:
         out = _empty(e, sh, x.dtype, x.device, stream)
         os_ = out.stride()
     st = _lib.mxgemm_rope(x.data_ptr(), out.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions),
@@ -891,6 +904,8 @@ def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=Fal
                           flags | (MXG_ROPE_TRANSPOSE if transpose else 0), _stream(stream))
     if st != MXG_OK:
         _raise(st)
+    if not own:
+        _changed(e, out)
     return out
 
 
@@ -937,6 +952,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, e
                                   rot, rot_offset, rows, eps, lay, dt, wdt, flags, _stream(stream))
     if st != MXG_OK:
         _raise(st)
+    if out is not None:
+        _changed(e, yq, yk)
     return yq, yk
 
 
@@ -980,6 +997,8 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos=None, sin=None, 
         d, rot, rot_offset, rows, eps, lay, dt, wdt, flags, workspace.data_ptr(), given, _stream(stream))
     if st != MXG_OK:
         _raise(st)
+    if out is not None:
+        _changed(e, xq, xk)
     return xq, xk, dwq, dwk
 
 

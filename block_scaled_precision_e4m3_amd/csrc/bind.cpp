@@ -68,6 +68,11 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// A tensor of the caller's that the call has written: autograd must not take it for what it was.
+void changed(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A flag argument: what Python takes for true (nothing that raises).
 bool truth(PyObject* o) {
   const int t = PyObject_IsTrue(o);
@@ -207,6 +212,7 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
                       cols, k, l, fa, fb, ct, flags, need ? ws.data_ptr() : nullptr, need, stream_of(dev));
   if (status != MXG_OK) return refused(status);
   if (given) {
+    changed(*given);
     Py_INCREF(v[6]);
     return v[6];
   }
@@ -264,6 +270,7 @@ PyObject* rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                  r.flags | (truth(v[6]) ? MXG_ROPE_TRANSPOSE : 0u), stream_of(dev));
   if (status != MXG_OK) return refused(status);
   if (given) {
+    changed(*given);
     Py_INCREF(v[7]);
     return v[7];
   }
