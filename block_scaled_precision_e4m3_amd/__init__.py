@@ -550,6 +550,7 @@ class _Torch:
         self.dt = {torch.float32: MXG_DT_F32, torch.bfloat16: MXG_DT_BF16, torch.float16: MXG_DT_F16}
         self.fmt = {torch.float8_e4m3fn: MXG_FMT_E4M3, torch.float8_e5m2: MXG_FMT_E5M2}
         self.code = {MXG_FMT_E4M3: torch.float8_e4m3fn, MXG_FMT_E5M2: torch.float8_e5m2}
+        self.rope, self.norm = _differentiable(torch)
 
 
 _env = None
@@ -596,6 +597,50 @@ def _changed(e, *tensors):
             e.torch.autograd.graph.increment_version(t)
 
 
+def _history(e, out, *tensors):
+    """Whether a call's result needs a history; one that goes into `out` cannot have any."""
+    if not e.torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (*tensors, *(out or ()))):
+        return False
+    if out is not None:
+        _refuse(MXG_ERR_FLAGS, "out has no gradient: call without out, or under torch.no_grad()")
+    return True
+
+
+def _differentiable(torch):
+    """The differentiable forms of rope and qk_norm_rope."""
+    def features(g):
+        # an expanded gradient (of a sum) has no features side by side
+        return g if g.shape[2] <= 1 or g.stride(2) == 1 else g.contiguous()
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, cos, sin, positions, layout, rot_offset, transpose, stream):
+            ctx.save_for_backward(cos, sin, positions)
+            ctx.how = layout, rot_offset, transpose
+            return rope(x, cos, sin, positions, layout, rot_offset, transpose, stream=stream)
+
+        @staticmethod
+        def backward(ctx, g):
+            layout, rot_offset, transpose = ctx.how
+            return rope(features(g), *ctx.saved_tensors, layout, rot_offset, not transpose), *(None,) * 7
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, layout, rot_offset, stream):
+            ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+            ctx.how = eps, layout, rot_offset
+            return qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, layout, rot_offset, stream=stream)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gq, gk):
+            q, k, q_weight, k_weight = ctx.saved_tensors[:4]
+            gk = None if k is None else features(gk)
+            dq, dk, dwq, dwk = qk_norm_rope_backward(features(gq), gk, *ctx.saved_tensors, *ctx.how)
+            return dq, dk, dwq.to(q_weight.dtype), None if dwk is None else dwk.to(k_weight.dtype), *(None,) * 7
+    return Rope, Norm
+
+
 def _expect(t, shape, dtype, name):
     """Checks of a contiguous operand or output given by the caller."""
     if t.shape != shape:
@@ -637,7 +682,9 @@ def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, 
     square: blocks of 128 x 128, s (ceil(M/128), ceil(K/128)) and st its transpose (a weight, for the forward
     product and the input gradient).
 
-    pow2: scales are powers of two.  out: those four tensors preallocated (None where not wanted)."""
+    pow2: scales are powers of two.  out: those four tensors preallocated (None where not wanted).
+
+    Codes and scales have no gradient; a layer that trains through them defines its own (examples/attention_input.py)."""
     e = _env or _torch()
     if out is None and stream is None and e.fast is not None:
         done = e.fast.quantize(x, fmt, rows, cols, square, pow2)
@@ -693,7 +740,9 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
     a (M, K) codes with sa (ceil(K/128), M), b (N, K) codes with sb (ceil(N/128), ceil(K/128)) for b_block=128 or
     (ceil(K/128), N) for b_block=1; K a multiple of 16; all with a leading L or none; E4M3 or E5M2 each.  c_dtype:
     float32, bfloat16 (the default) or float16.  c: the output, whose rows may be further apart than N; accumulate
-    adds to a float32 c."""
+    adds to a float32 c.
+
+    The product has no history for autograd: codes have no gradient (see block128_quantize)."""
     e = _env or _torch()
     if stream is None and workspace is None and e.fast is not None:
         done = e.fast.gemm(a, sa, b, sb, b_block, c_dtype, c, accumulate)
@@ -722,6 +771,7 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
     if not a.is_contiguous() or not b.is_contiguous():
         _refuse(MXG_ERR_ALIGN, "a and b must be contiguous")
     if c is not None:
+        _history(e, (c,))
         if c.shape != lead + (m, n):
             _refuse(MXG_ERR_SHAPE, f"c must have shape {lead + (m, n)}, got {tuple(c.shape)}")
         if c_dtype is not None and c.dtype != c_dtype:
@@ -880,12 +930,16 @@ def rope(x, cos, sin, positions=None, layout="half", rot_offset=0, transpose=Fal
     head rotate and the others are copied.  positions: (T) int32 or int64 table rows, None for 0, 1, ...; a token
     whose position lies outside the tables gets NaN there.  layout: "half" (pairs i, i + rot/2), "interleaved"
     (pairs 2i, 2i + 1) or "interleaved_to_half" (the latter in, the former out).  transpose: the transposed map, which takes
-    the output's gradient to the input's.  out: the result, which may be x; a new tensor by default."""
+    the output's gradient to the input's.  out: the result, which may be x; a new tensor by default.
+
+    Differentiable in x (not in the tables) unless out is given."""
     e = _env or _torch()
     if stream is None and e.fast is not None:
         done = e.fast.rope(x, cos, sin, positions, layout, rot_offset, transpose, out)
         if done is not None:
             return done
+    if _history(e, out if out is None else (out,), x):
+        return e.rope.apply(x, cos, sin, positions, layout, rot_offset, transpose, stream)
     dt = e.dt.get(x.dtype)
     if dt is None:
         _refuse(MXG_ERR_FMT, "x must be float32, bfloat16 or float16")
@@ -928,12 +982,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, e
                  out=None, stream=None):
     """C-ABI mxgemm_qk_norm_rope: each head of q (T, Hq, D) and k (T, Hk, D) divided by its root mean square,
     multiplied with its weight (D) and rotated, in one launch.  Returns (q_out, k_out); out: that pair, which may be
-    (q, k).  k and k_weight may be None.  cos, sin None: no rotation.  The other arguments are rope's."""
+    (q, k).  k and k_weight may be None.  cos, sin None: no rotation.  The other arguments are rope's.
+
+    Differentiable once, in q, k and the weights, by qk_norm_rope_backward, unless out is given."""
     e = _env or _torch()
     if out is None and stream is None and e.fast is not None:
         done = e.fast.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, layout, rot_offset, eps)
         if done is not None:
             return done
+    if _history(e, out, q, k, q_weight, k_weight):
+        return e.norm.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, layout, rot_offset, stream)
     dt = e.dt.get(q.dtype)
     if dt is None:
         _refuse(MXG_ERR_FMT, "q must be float32, bfloat16 or float16")

@@ -13,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <hip/hip_runtime_api.h>
@@ -67,6 +68,14 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
 }
 
 PyObject* none() { Py_RETURN_NONE; }
+
+// Whether the call's result needs a history, which the wrapper gives it.
+bool history(std::initializer_list<const Tensor*> all) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (const Tensor* t : all)
+    if (t && t->requires_grad()) return true;
+  return false;
+}
 
 // A tensor of the caller's that the call has written: autograd must not take it for what it was.
 void changed(const Tensor& t) {
@@ -177,7 +186,7 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (other || !a || !sa || !b || !sb || !integer(v[4], &block)) return none();
   const bool accumulate = truth(v[7]);
   const int fa = fmt_of(a->scalar_type()), fb = fmt_of(b->scalar_type());
-  if (fa < 0 || fb < 0 || (block != 1 && block != 128) || (accumulate && !given)) return none();
+  if (fa < 0 || fb < 0 || (block != 1 && block != 128) || (accumulate && !given) || history({given})) return none();
   const int64_t nd = a->dim();
   if ((nd != 2 && nd != 3) || b->dim() != nd || (nd == 3 && a->size(0) != b->size(0))) return none();
   const int64_t l = nd == 3 ? a->size(0) : 1, m = a->size(nd - 2), k = a->size(nd - 1), cols = b->size(nd - 2);
@@ -258,7 +267,7 @@ PyObject* rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (n != 8) return none();
   bool other = false;
   const Tensor *x = tensor(v[0], &other), *given = tensor(v[7], &other);
-  if (other || !x) return none();
+  if (other || !x || history({x, given})) return none();
   const int dev = x->is_cuda() ? x->get_device() : -1, dt = dt_of(x->scalar_type());
   Rotary r;
   if (dt < 0 || !current(dev) || !heads(*x, dev) || !rotary(v + 1, x->size(0), dev, &r)) return none();
@@ -329,7 +338,7 @@ PyObject* pack(std::initializer_list<const Tensor*> all) {
 // qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, layout, rot_offset, eps)
 PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
   Norm s;
-  if (n != 10 || !norm(v[0], v[1], v[2], v[3], v + 4, &s)) return none();
+  if (n != 10 || !norm(v[0], v[1], v[2], v[3], v + 4, &s) || history({s.q, s.k, s.wq, s.wk})) return none();
   const double eps = PyFloat_AsDouble(v[9]);
   if (PyErr_Occurred()) {
     PyErr_Clear();
