@@ -26,8 +26,8 @@ class AttentionInput(torch.nn.Module):
     """q (T, heads, D), k (T, kv_heads, D) and v (T, kv_heads, D) of hidden states x (T, hidden), bfloat16; norm: q and k
     are normed per head before the positions turn them.
 
-    weight ((heads + 2 kv_heads) D, hidden) is kept in bfloat16 and in codes of both directions; requantise() after it
-    has changed."""
+    weight ((heads + 2 kv_heads) D, hidden) is kept in bfloat16 and in codes of both directions, which follow the changes
+    that torch counts (an optimiser's step, load_state_dict); requantise() after others (through weight.data)."""
 
     def __init__(self, hidden, heads, kv_heads, head_dim, max_positions, rot=None, norm=True, eps=1e-6,
                  device="cuda"):
@@ -43,6 +43,11 @@ class AttentionInput(torch.nn.Module):
     @torch.no_grad()
     def requantise(self):
         self.codes = mx.block128_quantize(self.weight, square=True, cols=True)
+        self.codes_of = self.changes()
+
+    def changes(self):
+        """torch's count of the weight's changes; inference tensors have none."""
+        return None if self.weight.is_inference() else self.weight._version
 
     def split(self, y):
         """Views of the projection's output (T, (heads + 2 kv_heads) D)."""
@@ -64,6 +69,8 @@ class AttentionInput(torch.nn.Module):
                                         out=out)[2:]
 
     def forward(self, x, positions=None):
+        if self.codes_of != self.changes():
+            self.requantise()
         if torch.is_grad_enabled():
             return _AttentionInput.apply(x, self.weight, self.q_norm, self.k_norm, self, positions)
         xq, xs, _, _ = mx.block128_quantize(x)

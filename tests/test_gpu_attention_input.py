@@ -67,3 +67,37 @@ def test_decode_step_in_a_graph():
             torch.cuda.synchronize()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_codes_follow_the_weight():
+    """After an optimiser's step, and after load_state_dict, the layer gives what a layer made of those weights gives."""
+    import torch
+
+    import attention_input
+    torch.manual_seed(3)
+    layer, other = (attention_input.AttentionInput(256, 2, 1, 64, 64) for _ in range(2))
+    x = torch.randn(9, 256, device="cuda").bfloat16()
+    step = torch.optim.SGD(layer.parameters(), lr=0.5)
+    before = layer(x)
+    sum(o.float().square().sum() for o in before).backward()
+    step.step()
+    got = layer(x)
+    assert not torch.equal(got[2], before[2])
+    other.load_state_dict(layer.state_dict())
+    with torch.no_grad():
+        for a, b in zip(got, other(x)):
+            assert torch.equal(a, b)
+        layer.requantise()
+        for a, b in zip(got, layer(x)):
+            assert torch.equal(a, b)
+
+
+def test_a_layer_of_inference_tensors():
+    import torch
+
+    import attention_input
+    with torch.inference_mode():
+        layer = attention_input.AttentionInput(256, 2, 1, 64, 64)
+        x = torch.randn(9, 256, device="cuda").bfloat16()
+        for a, b in zip(layer(x), layer(x)):
+            assert torch.equal(a, b)
