@@ -84,20 +84,20 @@ class _AttentionInput(torch.autograd.Function):
         xq, xs, xqt, xst = mx.block128_quantize(x, cols=True)
         y = mx.block128_gemm(xq, xs, layer.codes[0], layer.codes[1])
         q, k, v = layer.split(y)
-        ctx.layer, ctx.positions = layer, positions
-        ctx.save_for_backward(y, xqt, xst, q_norm, k_norm, *layer.codes[2:])
+        ctx.layer = layer
+        ctx.save_for_backward(y, xqt, xst, q_norm, k_norm, *layer.codes[2:], positions)
         # a view of y may not leave: y is kept as it is for the backward pass
         return *layer.positioned(q, k, positions), v.clone()
 
     @staticmethod
     def backward(ctx, dq, dk, dv):
         layer = ctx.layer
-        y, xqt, xst, q_norm, k_norm, wt, wts = ctx.saved_tensors
+        y, xqt, xst, q_norm, k_norm, wt, wts, positions = ctx.saved_tensors
         q, k, _ = layer.split(y)
         dq, dk = dq.contiguous(), dk.contiguous()  # an expanded gradient (of a sum) has no features side by side
         dy = torch.empty_like(y)
         gq, gk, gv = layer.split(dy)
-        dqn, dkn = layer.positioned_backward(dq, dk, q, k, q_norm, k_norm, ctx.positions, (gq, gk))
+        dqn, dkn = layer.positioned_backward(dq, dk, q, k, q_norm, k_norm, positions, (gq, gk))
         gv.copy_(dv)
         g, gs, gt, gts = mx.block128_quantize(dy, cols=True)
         dx = mx.block128_gemm(g, gs, wt, wts)

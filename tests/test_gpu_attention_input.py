@@ -101,3 +101,16 @@ def test_a_layer_of_inference_tensors():
         x = torch.randn(9, 256, device="cuda").bfloat16()
         for a, b in zip(layer(x), layer(x)):
             assert torch.equal(a, b)
+
+
+def test_positions_changed_between_the_passes():
+    """autograd notices, as for any tensor that a backward pass needs."""
+    import torch
+
+    import attention_input
+    layer = attention_input.AttentionInput(256, 2, 1, 64, 64)
+    x, at = torch.randn(9, 256, device="cuda").bfloat16(), torch.arange(9, device="cuda")
+    out = layer(x, at)
+    at.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out[0].sum().backward()
