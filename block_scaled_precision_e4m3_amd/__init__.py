@@ -539,8 +539,11 @@ class _Torch:
         import torch
         try:
             from . import _bind
-        except ImportError:  # a library built without torch at hand: every call goes through the checks below
+        except ImportError as e:  # a library built without torch at hand: every call goes through the checks below
             _bind = None
+            if os.path.exists(os.path.join(_PKG_DIR, "_bind.so")):
+                import warnings
+                warnings.warn(f"_bind.so does not load, calls take more host time: {e}", RuntimeWarning, stacklevel=3)
         else:
             _bind.on_status(_raise)
         self.torch, self.fast = torch, _bind

@@ -46,7 +46,10 @@ def hipcc():
 
 
 def build_bind(verbose=False):
-    """Compile _bind.so against torch and the built library; without torch there is nothing for it to serve."""
+    """Compile _bind.so against torch and the built library; without torch there is nothing for it to serve.
+
+    The wrappers work without it, at more host time per call: where it cannot be compiled (no g++, other headers), that is
+    said and the library stands by itself.  One of an earlier build does not stay beside the new library."""
     import importlib.util
     import sysconfig
     spec = importlib.util.find_spec("torch")
@@ -61,11 +64,18 @@ def build_bind(verbose=False):
            "-L" + PKG_DIR, "-l:libmxgemm.so", "-L" + os.path.join(rocm, "lib"), "-lamdhip64", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("g++ failed on bind.cpp:\n" + res.stdout + res.stderr)
-    os.replace(BIND + ".tmp", BIND)
-    return BIND
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        failed = res.stdout + res.stderr if res.returncode != 0 else None
+    except OSError as e:
+        failed = str(e)
+    if failed is None:
+        os.replace(BIND + ".tmp", BIND)
+        return BIND
+    if os.path.exists(BIND):
+        os.remove(BIND)
+    print("g++ failed on bind.cpp; torch calls take the longer way through ctypes:\n" + failed, file=sys.stderr, flush=True)
+    return None
 
 
 def build(verbose=False, extra_flags=(), jobs=None):
