@@ -293,3 +293,27 @@ def test_offsets_past_32_bits(lib):
     y = lib.rope(x, cos, sin, out=x)
     ref, mag = R.rotate(f64(keep), f64(cos), f64(sin), "half")
     close(y, ref, mag, 3, torch.bfloat16)
+
+
+@pytest.mark.parametrize("D,pad,rot,off", [(128, 8, 64, 0), (64, 1, 64, 0), (192, 0, 64, 128), (128, 3, 128, 0), (100, 1, 30, 5)])
+def test_strides_do_not_change_results(lib, D, pad, rot, off):
+    """Heads of any spacing and alignment, in and out, go through the same arithmetic as contiguous ones: equal bits."""
+    T, Hq, Hk = 19, 4, 2
+    for dtype in DT.values():
+        for layout in LAYOUTS:
+            q, k, wq, wk, cos, sin, pos, _, _ = norm_case(lib, T, Hq, Hk, D, rot, off, layout, dtype, dtype, 3)
+            args = (cos, sin, pos, 1e-6, layout, off)
+            g = normal((T, Hq + Hk, D + pad), 9, dtype).cuda()
+            gq, gk = g[:, :Hq, :D], g[:, Hq:, :D]
+            qc, kc, gqc, gkc = (t.contiguous() for t in (q, k, gq, gk))
+            wide = torch.full((T, Hq + Hk + 1, D + pad), 3.0, dtype=dtype, device="cuda")
+            out = wide[:, :Hq, :D], wide[:, Hq + 1:, :D]
+            lib.qk_norm_rope(q, k, wq, wk, *args, out=out)
+            for a, b in zip(out, lib.qk_norm_rope(qc, kc, wq, wk, *args)):
+                assert torch.equal(a, b)
+            got = lib.qk_norm_rope_backward(gq, gk, q, k, wq, wk, *args, out=out)
+            for a, b in zip(got, lib.qk_norm_rope_backward(gqc, gkc, qc, kc, wq, wk, *args)):
+                assert torch.equal(a, b)
+            for transpose in (False, True):
+                lib.rope(gq, cos, sin, pos, layout, off, transpose, out=out[0])
+                assert torch.equal(out[0], lib.rope(gqc, cos, sin, pos, layout, off, transpose))
