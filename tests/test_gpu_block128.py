@@ -398,3 +398,83 @@ def test_quantize_ties(lib, dtype, exponent):
     for fmt in (0, 1):
         for square in (False, True):
             check_quantize(lib, x, fmt, True, True, square, False)
+
+
+# every tile shape and the kernel for few rows, as sizes choose them
+NORMWISE = [(1, 7168, 2048), (4, 7168, 7168), (32, 4000, 1024), (128, 7168, 2048), (512, 4096, 7168), (1024, 4096, 7168),
+            (2048, 4096, 4096), (4096, 4096, 2048), (40, 520, 7168)]
+
+
+@pytest.mark.parametrize("b_block", [128, 1])
+@pytest.mark.parametrize("m,n,k", NORMWISE)
+def test_gemm_error_in_the_mean(lib, m, n, k, b_block):
+    """Rounding to nearest of values spread evenly over a binade is off by ulp / sqrt(12) in the root mean square, 1.5e-3
+    of theirs with 8 significant bits and 1.9e-4 with 11; truncation by twice that, and by 0.7 ulp / 2 in the mean, where
+    nearest gives none.  Float32 sums of n terms in one order: about sqrt(K) 2^-25.  The 8-bit products of a 16-bit C add
+    1.4e-5.  The bounds are a third above, and for the mean five standard deviations of 7168 roundings."""
+    print(f"gemm {m}x{n}x{k} blocks of {b_block}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    a, sa, _, _ = lib.block128_quantize(torch.randn(m, k, device="cuda", generator=g))
+    b, sb, _, _ = lib.block128_quantize(torch.randn(n, k, device="cuda", generator=g) / k ** 0.5, square=b_block == 128)
+    da = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :k]
+    db = b.double() * (sb.double().t() if b_block == 1 else sb.double().repeat_interleave(128, 0)[:n]).repeat_interleave(128, 1)[:, :k]
+    ref = da @ db.t().contiguous()
+    for dtype, rms, mean in ((torch.bfloat16, 2.0e-3, 1e-4), (torch.float16, 2.6e-4, 2.5e-5), (torch.float32, 5e-6, 1e-6)):
+        e = lib.block128_gemm(a, sa, b, sb, b_block=b_block, c_dtype=dtype).double() - ref
+        assert float(e.norm() / ref.norm()) < rms, dtype
+        assert abs(float((e * ref.sign()).sum() / ref.abs().sum())) < mean, dtype
+
+
+@pytest.mark.parametrize("b_block", [128, 1])
+def test_gemm_batches_with_divided_k(lib, b_block):
+    """Batches whose K is divided, into rows of a wider C, and added to a float32 one."""
+    L, m, n, k = 2, 40, 130, 4112
+    one = [operands(m, n, k, 0, 0, b_block, 20 + i) for i in range(L)]
+    ops = upload(*[np.stack([o[j] for o in one]) for j in range(4)], 0, 0)
+    c0 = np.random.default_rng(2).standard_normal((L, m, n)).astype(np.float32)
+    for dtype in DT.values():
+        assert lib._lib.mxgemm_block128_workspace_bytes(m, n, k, L, lib._torch().dt[dtype]) > 0
+        for add in (False, True) if dtype == torch.float32 else (False,):
+            wide = torch.full((L, m, n + 6), 7.0, dtype=dtype, device="cuda")
+            c = wide[..., :n]
+            if add:
+                c.copy_(torch.from_numpy(c0))
+            lib.block128_gemm(*ops, b_block=b_block, c=c, accumulate=add)
+            assert torch.all(wide[..., n:] == 7).item()
+            for i in range(L):
+                ref, s = B.gemm(*one[i], 0, 0, b_block)
+                if add:
+                    ref, s = ref + c0[i], s + np.abs(c0[i])
+                assert (np.abs(c[i].double().cpu().numpy() - ref) <= bound(s, ref, k, dtype)).all()
+
+
+def test_host_threads(lib):
+    """Calls from several host threads, each on a stream of its own, give what one thread gets."""
+    import threading
+    jobs = []
+    for i, (m, n, k) in enumerate(((3, 200, 272), (64, 512, 4112), (300, 260, 528), (40, 130, 4112))):
+        ops = upload(*operands(m, n, k, 0, 0, 128, i), 0, 0)
+        x = values((m, k), i, torch.bfloat16).cuda()
+        jobs.append((ops, x, lib.block128_gemm(*ops), lib.block128_quantize(x, cols=True)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            ops, x, c, codes = jobs[i]
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    ok = torch.equal(lib.block128_gemm(*ops), c)
+                    for got, want in zip(lib.block128_quantize(x, cols=True), codes):
+                        ok = ok and torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+                    if not ok:
+                        wrong.append(i)
+        except Exception as e:  # noqa: BLE001  a thread's error is the test's
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
