@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../include/mxgemm.h"
@@ -16,7 +17,7 @@ namespace host {
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
-  int checked = 0;   // 0 unknown, 1 gfx950, -1 other
+  std::atomic<int> checked{0};  // 0 unknown, 1 gfx950, -1 other; set after cus
   int cus = 0;
 };
 
