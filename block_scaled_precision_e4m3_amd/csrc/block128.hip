@@ -13,16 +13,8 @@ namespace {
 
 using namespace mxg::host;
 
-// Takes MXG_TRUSTED_POINTERS out of a call's flags.
-bool take_trust(unsigned* flags) {
-  const bool trusted = (*flags & MXG_TRUSTED_POINTERS) != 0;
-  *flags &= ~(unsigned)MXG_TRUSTED_POINTERS;
-  return trusted;
-}
 using mxg::b128::GemmParams;
 using mxg::b128::QuantParams;
-
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 

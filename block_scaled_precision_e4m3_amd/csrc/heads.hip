@@ -12,12 +12,6 @@ namespace {
 
 using namespace mxg::host;
 
-// Takes MXG_TRUSTED_POINTERS out of a call's flags.
-bool take_trust(unsigned* flags) {
-  const bool trusted = (*flags & MXG_TRUSTED_POINTERS) != 0;
-  *flags &= ~(unsigned)MXG_TRUSTED_POINTERS;
-  return trusted;
-}
 using mxg::heads::Params;
 using mxg::heads::Tensor;
 
@@ -43,8 +37,6 @@ int check(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t off
   }
   return MXG_OK;
 }
-
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 void layouts(Params* p, int layout, bool transpose) {
   const bool in = layout == MXG_ROPE_HALF, out = layout != MXG_ROPE_INTERLEAVED;

@@ -29,6 +29,14 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool fits_i32(int64_t v) { return v >= 0 && v <= 0x7FFFFFFFLL; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Takes MXG_TRUSTED_POINTERS out of a call's flags.
+inline bool take_trust(unsigned* flags) {
+  const bool trusted = (*flags & MXG_TRUSTED_POINTERS) != 0;
+  *flags &= ~(unsigned)MXG_TRUSTED_POINTERS;
+  return trusted;
+}
 
 // launch(first, count) for `blocks` workgroups in runs of 2^22 at most, for kernels of up to 512 threads.  A launch has
 // fewer than 2^32 work items in a dimension; one of more is not refused but runs the remainder by 2^32 alone.  (Two
