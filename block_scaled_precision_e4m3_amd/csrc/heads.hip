@@ -38,6 +38,12 @@ int check(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t off
   return MXG_OK;
 }
 
+// Whether rows of an output surely lie on each other: neighbouring tokens or heads nearer than a row, or the same distance
+// for both.
+bool overlap(int64_t T, int64_t H, int64_t D, const int64_t* s) {
+  return T > 0 && H > 0 && ((T > 1 && s[0] < D) || (H > 1 && s[1] < D) || (T > 1 && H > 1 && s[0] == s[1]));
+}
+
 void layouts(Params* p, int layout, bool transpose) {
   const bool in = layout == MXG_ROPE_HALF, out = layout != MXG_ROPE_INTERLEAVED;
   p->halves_in = transpose ? out : in;
@@ -129,6 +135,7 @@ int mxgemm_rope(const void* X, void* Y, const float* cos, const float* sin, cons
   int st = check(T, H, 0, D, rot, rot_offset, table_rows, positions != nullptr, layout, dtype, dtype, flags,
                  MXG_ROPE_TRANSPOSE | MXG_ROPE_POS64, strides, 2);
   if (st != MXG_OK) return st;
+  if (overlap(T, H, D, strides + 2)) return MXG_ERR_SHAPE;
   if (T == 0 || H == 0) return MXG_OK;
   if (!X || !Y || (rot > 0 && (!cos || !sin))) return MXG_ERR_NULL;
   const size_t e = mxg::elem_bytes(dtype), pe = (flags & MXG_ROPE_POS64) ? 8 : 4;
@@ -167,6 +174,7 @@ int mxgemm_qk_norm_rope(const void* Q, const void* K, void* YQ, void* YK, const 
   int st = check(T, Hq, Hk, D, rot, rot_offset, table_rows, positions != nullptr, layout, dtype, w_dtype, flags,
                  MXG_ROPE_POS64, strides, 4);
   if (st != MXG_OK) return st;
+  if (overlap(T, Hq, D, strides + 4) || overlap(T, Hk, D, strides + 6)) return MXG_ERR_SHAPE;
   if (T == 0 || Hq + Hk == 0) return MXG_OK;
   if ((Hq > 0 && (!Q || !YQ || !WQ)) || (Hk > 0 && (!K || !YK || !WK)) || (rot > 0 && (!cos || !sin)))
     return MXG_ERR_NULL;
@@ -230,6 +238,7 @@ int mxgemm_qk_norm_rope_backward(const void* GQ, const void* GK, const void* Q, 
   int st = check(T, Hq, Hk, D, rot, rot_offset, table_rows, positions != nullptr, layout, dtype, w_dtype, flags,
                  MXG_ROPE_POS64, strides, 6);
   if (st != MXG_OK) return st;
+  if (overlap(T, Hq, D, strides + 8) || overlap(T, Hk, D, strides + 10)) return MXG_ERR_SHAPE;
   const bool empty = T == 0 || Hq + Hk == 0;
   if (!DWQ || (Hk > 0 && !DWK) || !workspace) return MXG_ERR_NULL;
   if (!empty && ((Hq > 0 && (!GQ || !Q || !DQ || !WQ)) || (Hk > 0 && (!GK || !K || !DK || !WK)) ||

@@ -577,8 +577,9 @@ enum {
  *               rotary features of a token whose position lies outside the
  *               tables become NaN.
  * Errors (before any work): MXG_ERR_SHAPE (negative sizes, D not 1..1024, rot
- * odd or rot_offset + rot > D, sizes or strides too large, T > table_rows
- * without positions), MXG_ERR_FMT (dtype, layout), MXG_ERR_FLAGS,
+ * odd or rot_offset + rot > D, sizes or strides too large, rows of Y nearer to
+ * each other than D or tokens as far apart as heads, T > table_rows without
+ * positions), MXG_ERR_FMT (dtype, layout), MXG_ERR_FLAGS,
  * MXG_ERR_NULL, MXG_ERR_ALIGN (a pointer not aligned to its elements),
  * MXG_ERR_DEVICE, MXG_ERR_LAUNCH.  T or H == 0 queues nothing.  Asynchronous,
  * allocates nothing.

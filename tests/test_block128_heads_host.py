@@ -243,3 +243,22 @@ def test_missing_weights_and_scales(lib):
         with pytest.raises(lib.MxgemmValueError) as e:
             bad()
         assert e.value.status == lib.MXG_ERR_NULL
+
+
+def test_outputs_whose_rows_lie_on_each_other(lib):
+    """An expanded output would be written by many rows at once; inputs may be expanded."""
+    rope, norm, back = lib._lib.mxgemm_rope, lib._lib.mxgemm_qk_norm_rope, lib._lib.mxgemm_qk_norm_rope_backward
+    good = [512, 128]
+    arr = lambda s: (ctypes.c_int64 * len(s))(*s)  # noqa: E731
+
+    def call(x, y, T=4, H=4):
+        return (rope(GOOD, GOOD, GOOD, GOOD, GOOD, arr(x + y), T, H, 128, 64, 0, 4, 0, 1, 0, None),
+                norm(*[GOOD] * 9, arr(x + x + good + y), T, 4, H, 128, 64, 0, 4, 1e-6, 0, 1, 1, 0, None),
+                norm(*[GOOD] * 9, arr(x + x + y + good), T, H, 4, 128, 64, 0, 4, 1e-6, 0, 1, 1, 0, None),
+                back(*[GOOD] * 13, arr(x * 4 + good + y), T, 4, H, 128, 64, 0, 4, 1e-6, 0, 1, 1, 0, GOOD, 1 << 30, None),
+                back(*[GOOD] * 13, arr(x * 4 + y + good), T, H, 4, 128, 64, 0, 4, 1e-6, 0, 1, 1, 0, GOOD, 1 << 30, None))
+    for y in ([0, 128], [512, 0], [127, 1024], [512, 127], [128, 128]):
+        assert call(good, y) == (lib.MXG_ERR_SHAPE,) * 5, y
+    for x, y, T, H in (([0, 0], good, 4, 4), (good, [128, 512], 4, 4), (good, [0, 128], 1, 4), (good, [512, 0], 4, 1),
+                       (good, [0, 0], 1, 1), (good, [128, 4096], 4, 4)):
+        assert call(x, y, T, H) == (lib.MXG_ERR_DEVICE,) * 5, (x, y)
