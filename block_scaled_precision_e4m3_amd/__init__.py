@@ -745,6 +745,10 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
     float32, bfloat16 (the default) or float16.  c: the output, whose rows may be further apart than N; accumulate
     adds to a float32 c.
 
+    A float32 c is exact up to float32 rounding.  A 16-bit c is made on the 8-bit matrix cores, which drop a little inside
+    groups of 8 K elements (include/mxgemm.h): far less than c's own rounding on ordinary data, but more where large terms
+    cancel; take a float32 c and round it where that matters.
+
     The product has no history for autograd: codes have no gradient (see block128_quantize)."""
     e = _env or _torch()
     if stream is None and workspace is None and e.fast is not None:

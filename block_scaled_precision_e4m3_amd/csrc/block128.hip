@@ -112,8 +112,10 @@ Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
   // a rows workgroup reads A once for its columns, so more columns are better as long as they leave enough
   // workgroups (7168 columns: 32 at a time 4.9 us, 16 5.1 us; 4096: 7.3 and 5.8 us; K = 2048 and 4096)
   // Up to 32 rows too, unless there are more workgroups than compute units (32x24576x1536: 11.7 us, tiles 9.7) or, for
-  // a 16-bit C, K is long (32x7168x2048: 6.8 us, tiles 7.0; 32x6144x4096: 10.4 and 9.7; float32 C: 7.1 and 9.4, 11.0
-  // and 14.7).  With 64 rows tiles are as fast or faster (64x7168x2048: 9.2 us, tiles 7.2; float32 C: 9.5 and 9.6).
+  // a 16-bit C, K is long (32x7168x2048: 6.9 us, tiles 7.0; 32x6144x4096: 10.8 and 10.1; float32 C: 7.3 and 9.8, 11.3
+  // and 14.0).  Where the two cross moves with rows and columns: 32 rows at K = 2560 from 6144 columns on and past 4096
+  // below that (32x4096x4096: 8.9 us, tiles 10.0), 24 rows at 3328, 17 rows past 6144 (17x7168x4096: 9.4 and 10.0);
+  // 2048 is on the safe side of all of them.  With 64 rows tiles are as fast or faster (64x7168x2048: 9.2 us, tiles 7.2; float32 C: 9.5 and 9.6).
   if (M <= 16 || (M <= 32 && L * cdiv(N, 32) <= kUnits && (exact || K <= 2048))) return {L * cdiv(N, 32) >= kUnits * 3 / 4 ? 32 : 16, 16, 0, 1, 1};
   struct Size {
     int bm, bn, kb;

@@ -243,9 +243,9 @@ __device__ __forceinline__ int first_tile_of(const GemmParams& p) {
 // cycles, under which the four multiply-adds per lane of an earlier one run.
 // VALU instructions reach only ordinary registers, so the accumulators live
 // there and a wave holds 128 x 64 of them, eight waves a 256 x 256 tile.
-// 8192 x 24576 x 1536 takes 292 us (2.1 PFLOP/s), 8192^3 460 (2.4), with the
-// matrix cores busy 58% of the cycles and no LDS bank conflicts; the clock, about
-// 2 GHz, is what power leaves.
+// 8192 x 24576 x 1536 takes 290 to 300 us (2.1 PFLOP/s), of which the C stores
+// are 43, 8192^3 460 (2.4), with the matrix cores busy 56% and 63% of the cycles at
+// a clock of 1.7 to 2 GHz and no LDS bank conflicts.
 //
 // B is the MFMA's first operand: lane (r = lane % 16, g = lane / 16) owns output
 // row r of a 16-row block and the MFMA's columns 4g .. 4g + 3.  Which tile

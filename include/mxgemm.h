@@ -486,7 +486,8 @@ enum {
  *        the transpose of Q's codes.
  * Q and S, or QT and ST, may both be NULL (not wanted); X is read once either
  * way.  A block that holds a NaN or an infinity gets a scale that is not
- * finite, so everything it touches in the product is NaN.
+ * finite and NaN codes (those past K and M in it too), so everything it touches
+ * in the product is NaN.
  *
  * Asynchronous on `stream`, allocates nothing; outputs must not overlap X.
  * Errors (before any work): MXG_ERR_SHAPE (negative or too large sizes, ldx <
@@ -523,9 +524,12 @@ enum {
  * Accuracy.  A float32 C takes exact products: codes are widened to bfloat16
  * (exact) and the sums are float32.  A 16-bit C takes the matrix cores' 8-bit
  * products, whose sums inside a group of 8 K elements drop what lies 2^-13
- * below the largest (measured 1.4e-5 of the result in 2-norm on normal data,
- * against 1.6e-3 and 2e-4 that the rounding to bfloat16 / float16 costs); sums
- * across groups and blocks are float32.
+ * below the largest: 1.4e-5 of the result in 2-norm on normal data (measured),
+ * against 1.6e-3 and 2e-4 that the rounding to bfloat16 / float16 costs, but in
+ * the worst case 2^-10 of sum |A||B|, which where terms cancel is more than
+ * that rounding.  Where this matters, take a float32 C and round it.  Sums
+ * across groups and blocks are float32.  SA SB is rounded to float32 before it
+ * multiplies a block's sum, so it should lie in float32's normal range.
  *
  * Workspace: device memory of at least mxgemm_block128_workspace_bytes, 16-byte
  * aligned, overwritten; NULL where that is 0.
