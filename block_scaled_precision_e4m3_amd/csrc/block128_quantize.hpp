@@ -77,8 +77,11 @@ __device__ __forceinline__ Scale block_scale(unsigned bits, bool pow2) {
     const int e = quant::block_exponent<FMT>(a);
     return {__uint_as_float((unsigned)(127 + e) << 23), __uint_as_float((unsigned)(127 - e) << 23), 0.f};
   }
-  const float hi = kMax / a;  // correctly rounded; an infinity or NaN makes every code NaN
-  return {a / kMax, hi, __builtin_fmaf(-hi, a, kMax) / a};
+  const float near = kMax / a;  // correctly rounded; an infinity or NaN makes every code NaN
+  const float rest = __builtin_fmaf(-near, a, kMax) / a;
+  // hi is the quotient rounded down, so that lo is not negative: x hi + x lo then keeps the sign of a zero
+  const float hi = rest < 0.f ? __int_as_float(__float_as_int(near) - 1) : near;
+  return {a / kMax, hi, rest + (near - hi)};
 }
 
 __device__ __forceinline__ float scaled(float x, const Scale& s) { return __builtin_fmaf(x, s.hi, x * s.lo); }

@@ -478,3 +478,18 @@ def test_host_threads(lib):
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_quantize_signed_zeros(lib, dtype):
+    """A zero keeps its sign, as a value that rounds to zero does, whatever the block's scale."""
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((300, 260)).astype(np.float32)
+    x[rng.random(x.shape) < 0.3] = -0.0
+    x[rng.random(x.shape) < 0.3] = 0.0
+    x[:40] = -0.0
+    x = torch.from_numpy(x).to(DT[dtype])
+    for fmt in (0, 1):
+        for square in (False, True):
+            for pow2 in (False, True):
+                check_quantize(lib, x, fmt, True, True, square, pow2)
