@@ -50,6 +50,14 @@ MXG_ROPE_INTERLEAVED_TO_HALF = 2
 MXG_ROPE_TRANSPOSE = 1
 MXG_ROPE_POS64 = 2
 MXG_TRUSTED_POINTERS = 1073741824
+MXG_ACT_NONE = 0
+MXG_ACT_RELU = 1
+MXG_ACT_SILU = 2
+MXG_ACT_GELU = 3
+MXG_ACT_GELU_TANH = 4
+MXG_GROUP_OFFSETS64 = 256
+MXG_GROUP_ZERO_REST = 512
+MXG_GROUP_ZERO_PREACT = 1024
 
 MXG_OK = 0
 MXG_ERR_NULL = -1
@@ -69,7 +77,9 @@ EXPORTED = ("mxgemm_amax", "mxgemm_amax_ex", "mxgemm_amax_reset", "mxgemm_check_
             "mxgemm_proj_rope_mxfp8", "mxgemm_gemm_rope_mxfp8", "mxgemm_projection_workspace_bytes",
             "mxgemm_projection_mxfp8", "mxgemm_projection_mxfp8_noalloc", "mxgemm_block128_quantize", "mxgemm_block128",
             "mxgemm_block128_workspace_bytes", "mxgemm_rope", "mxgemm_qk_norm_rope", "mxgemm_qk_norm_rope_backward",
-            "mxgemm_qk_norm_rope_backward_workspace_bytes")
+            "mxgemm_qk_norm_rope_backward_workspace_bytes", "mxgemm_block128_linear", "mxgemm_activation_backward",
+            "mxgemm_activation_backward_workspace_bytes", "mxgemm_group_blocks", "mxgemm_block128_quantize_grouped",
+            "mxgemm_block128_grouped", "mxgemm_block128_grouped_weight_gradient")
 
 
 class MxgemmError(Exception):
@@ -84,6 +94,13 @@ class MxgemmValueError(MxgemmError, ValueError):
 
 class MxgemmRuntimeError(MxgemmError, RuntimeError):
     pass
+
+
+class _Ends(ctypes.Structure):
+    """mxgemm_ends_t"""
+    _fields_ = [("bias", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("preact", ctypes.c_void_p), ("ldgate", ctypes.c_int64), ("ldresidual", ctypes.c_int64),
+                ("ldpreact", ctypes.c_int64), ("activation", ctypes.c_int), ("bias_dtype", ctypes.c_int)]
 
 
 def _load():
@@ -144,6 +161,21 @@ def _load():
     lib.mxgemm_qk_norm_rope_backward.restype = ci
     lib.mxgemm_qk_norm_rope_backward_workspace_bytes.argtypes = [i64, i64]
     lib.mxgemm_qk_norm_rope_backward_workspace_bytes.restype = cz
+    ends = ctypes.POINTER(_Ends)
+    lib.mxgemm_block128_linear.argtypes = [vp] * 5 + [i64] * 4 + [ci, ci, ci, ends, cu, vp, cz, vp]
+    lib.mxgemm_block128_linear.restype = ci
+    lib.mxgemm_activation_backward.argtypes = [vp] * 6 + [strides, i64, i64, ci, ci, cu, vp, cz, vp]
+    lib.mxgemm_activation_backward.restype = ci
+    lib.mxgemm_activation_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.mxgemm_activation_backward_workspace_bytes.restype = cz
+    lib.mxgemm_group_blocks.argtypes = [i64, i64]
+    lib.mxgemm_group_blocks.restype = i64
+    lib.mxgemm_block128_quantize_grouped.argtypes = [vp, i64] + [vp] * 5 + [i64] * 3 + [ci, ci, cu, vp]
+    lib.mxgemm_block128_quantize_grouped.restype = ci
+    lib.mxgemm_block128_grouped.argtypes = [vp] * 6 + [i64] * 5 + [ci, ci, ci, ends, cu, vp]
+    lib.mxgemm_block128_grouped.restype = ci
+    lib.mxgemm_block128_grouped_weight_gradient.argtypes = [vp] * 6 + [i64] * 5 + [ci, ci, cu, vp]
+    lib.mxgemm_block128_grouped_weight_gradient.restype = ci
     return lib
 
 
@@ -673,7 +705,8 @@ def _matrix_rows(t, name):
     return lead, l, m, k, ld
 
 
-def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, pow2=False, out=None, stream=None):
+def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, pow2=False, out=None, stream=None,
+                      offsets=None):
     """C-ABI mxgemm_block128_quantize: 8-bit codes of x with one float32 scale per block of 128.
 
     x is (M, K) or (L, M, K) float32, bfloat16 or float16, K contiguous (rows may be further apart).  Returns
@@ -687,8 +720,15 @@ def block128_quantize(x, fmt=MXG_FMT_E4M3, rows=True, cols=False, square=False, 
 
     pow2: scales are powers of two.  out: those four tensors preallocated (None where not wanted).
 
+    offsets (E + 1), int32 or int64: the rows of x (T, K) lie in E groups, group e from offsets[e] to offsets[e + 1] (see
+    block128_grouped_gemm), and with cols the blocks along the rows start anew at each group's first row: qt (K, 128 G)
+    and st (G, K) with G = group_blocks(T, E), group after group and zero behind the last one; rows as above.
+    The operand of block128_grouped_weight_gradient.  Not with square, which such blocks are not.
+
     Codes and scales have no gradient; a layer that trains through them defines its own (examples/attention_input.py)."""
     e = _env or _torch()
+    if offsets is not None:
+        return _quantize_grouped(e, x, offsets, fmt, rows, cols, square, pow2, out, stream)
     if out is None and stream is None and e.fast is not None:
         done = e.fast.quantize(x, fmt, rows, cols, square, pow2)
         if done is not None:
@@ -805,6 +845,321 @@ def block128_gemm(a, sa, b, sb, b_block=128, c_dtype=None, c=None, accumulate=Fa
                               fa, fb, ct, (MXG_B128_B_ROWS if b_block == 1 else 0)
                               | (MXG_B128_ACCUMULATE if accumulate else 0) | MXG_TRUSTED_POINTERS, _ptr(workspace), given,
                               _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    if not own:
+        _changed(e, c)
+    return c
+
+
+# --- what follows a product, and rows in groups ----------------------------------------
+
+_ACTIVATIONS = {None: MXG_ACT_NONE, "relu": MXG_ACT_RELU, "silu": MXG_ACT_SILU, "gelu": MXG_ACT_GELU,
+                "gelu_tanh": MXG_ACT_GELU_TANH}
+
+
+def _activation(name):
+    if name is not None and not isinstance(name, str) or name not in _ACTIVATIONS:
+        _refuse(MXG_ERR_FMT, "activation must be None, relu, silu, gelu or gelu_tanh")
+    return _ACTIVATIONS[name]
+
+
+def _no_history(e, *tensors):
+    """Refuses tensors whose gradient would be lost without a word."""
+    if e.torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        _refuse(MXG_ERR_FLAGS, "the call has no history for autograd: call under torch.no_grad(), and define the layer's "
+                               "gradients with activation_backward")
+
+
+def _beside(t, shape, dtype, name):
+    """Row distance of a (M, N) tensor with contiguous columns."""
+    if t is None:
+        return 0
+    if t.shape != shape:
+        _refuse(MXG_ERR_SHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        _refuse(MXG_ERR_FMT, f"{name} must be {dtype}, got {t.dtype}")
+    m, n = shape
+    ld = t.stride(0) if m > 1 else n
+    if (n > 1 and t.stride(1) != 1) or ld < n:
+        _refuse(MXG_ERR_ALIGN, f"{name} must have contiguous columns and rows at least {n} elements apart")
+    return ld
+
+
+def _operands(e, a, sa, b, sb, lead):
+    """(rows, K, N, formats) of a (rows, K) with sa, and of b lead + (N, K) in blocks of 128 x 128 with sb."""
+    fa, fb = e.fmt.get(a.dtype), e.fmt.get(b.dtype)
+    if fa is None or fb is None:
+        _refuse(MXG_ERR_FMT, "a and b must be float8_e4m3fn or float8_e5m2")
+    if a.dim() != 2 or b.dim() != 2 + len(lead) or tuple(b.shape[:-2]) != lead:
+        _refuse(MXG_ERR_SHAPE, "a must be (rows, K) and b (N, K)" if not lead else f"a must be (rows, K) and b ({lead[0]}, N, K)")
+    (m, k), n = a.shape, b.shape[-2]
+    if b.shape[-1] != k:
+        _refuse(MXG_ERR_SHAPE, f"a and b disagree on K: {k} and {b.shape[-1]}")
+    if sa is None or sb is None:
+        _refuse(MXG_ERR_NULL, "sa and sb must be given")
+    kb = -(-k // 128)
+    _expect(sa, (kb, m), e.f32, "sa")
+    _expect(sb, lead + (-(-n // 128), kb), e.f32, "sb")
+    if not a.is_contiguous() or not b.is_contiguous():
+        _refuse(MXG_ERR_ALIGN, "a and b must be contiguous")
+    return m, k, n, fa, fb
+
+
+def _product_out(e, m, n, c, c_dtype, preact, device, stream):
+    """(c, its row distance, whether it is the caller's, preact, MXG_DT_*)."""
+    own = c is None
+    if own:
+        c_dtype = e.bf16 if c_dtype is None else c_dtype
+    else:
+        c_dtype = c.dtype if c_dtype is None else c_dtype
+    ct = e.dt.get(c_dtype)
+    if ct is None:
+        _refuse(MXG_ERR_FMT, "c must be float32, bfloat16 or float16")
+    ldc = n if own else _beside(c, (m, n), c_dtype, "c")
+    if own:
+        c = _empty(e, (m, n), c_dtype, device, stream)
+    z = _empty(e, (m, n), c_dtype, device, stream) if preact else None
+    return c, ldc, own, z, ct
+
+
+def _ends(e, act, bias, gate, residual, z, m, n, dtype):
+    """mxgemm_ends_t of a product (m, n) of that type."""
+    ends = _Ends(activation=act, ldgate=_beside(gate, (m, n), dtype, "gate"),
+                 ldresidual=_beside(residual, (m, n), dtype, "residual"), ldpreact=n)
+    if bias is not None:
+        if bias.shape != (n,):
+            _refuse(MXG_ERR_SHAPE, f"bias must have {n} elements")
+        if bias.dtype not in (dtype, e.f32):
+            _refuse(MXG_ERR_FMT, "bias must be float32 or of c's dtype")
+        if not bias.is_contiguous():
+            _refuse(MXG_ERR_ALIGN, "bias must be contiguous")
+        ends.bias_dtype = e.dt[bias.dtype]
+    ends.bias, ends.gate, ends.residual, ends.preact = _ptr(bias), _ptr(gate), _ptr(residual), _ptr(z)
+    return ends
+
+
+def block128_linear(a, sa, b, sb, bias=None, activation=None, gate=None, residual=None, preact=False, c_dtype=None, c=None,
+                    workspace=None, stream=None):
+    """C-ABI mxgemm_block128_linear: the product of block128_gemm with what a layer does to it, in the same pass:
+
+        z = a b^T + bias,  c = act(z) * gate + residual
+
+    a (M, K) codes with sa (ceil(K/128), M), b (N, K) codes with sb (ceil(N/128), ceil(K/128)): blocks of 128 x 128.
+    activation: None, "relu", "silu", "gelu" or "gelu_tanh"; bias (N) float32 or of c's dtype; gate and residual (M, N)
+    of c's dtype, rows possibly further apart; each may be None.  c: the output, new by default; it may be residual or gate
+    itself.  c_dtype, accuracy and workspace as of block128_gemm.  Returns c, or (c, z) with preact: z in c's dtype, from
+    which activation_backward makes the gradients.
+
+    Not differentiable (codes have no gradient): a layer defines its own, as examples/feed_forward.py does, and inputs
+    that require gradients are refused outside torch.no_grad()."""
+    e = _env or _torch()
+    if stream is None and workspace is None and e.fast is not None:
+        done = e.fast.linear(a, sa, b, sb, bias, activation, gate, residual, preact, c_dtype, c)
+        if done is not None:
+            return done
+    m, k, n, fa, fb = _operands(e, a, sa, b, sb, ())
+    act = _activation(activation)
+    _no_history(e, bias, gate, residual, c)
+    _here(a.get_device(), sa, b, sb, bias, gate, residual, c, workspace)
+    given = 0 if workspace is None else _workspace_bytes(workspace)
+    c, ldc, own, z, ct = _product_out(e, m, n, c, c_dtype, preact, a.device, stream)
+    ends = _ends(e, act, bias, gate, residual, z, m, n, c.dtype)
+    need = _lib.mxgemm_block128_workspace_bytes(m, n, k, 1, ct)
+    if need and workspace is None:
+        workspace, given = _empty(e, (need,), e.u8, a.device, stream, True), need
+    st = _lib.mxgemm_block128_linear(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), c.data_ptr(), ldc, m, n, k,
+                                     fa, fb, ct, ctypes.byref(ends), MXG_TRUSTED_POINTERS, _ptr(workspace), given,
+                                     _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    if not own:
+        _changed(e, c)
+    return (c, z) if preact else c
+
+
+def activation_backward(dy, z, activation=None, gate=None, bias=False, out=None, workspace=None, stream=None):
+    """C-ABI mxgemm_activation_backward: from the gradient dy of y = act(z) * gate + residual and what block128_linear or
+    block128_grouped_gemm kept as z, (dz, dgate, dbias): dz = dy * gate * act'(z), dgate = dy * act(z) (None without a gate)
+    and, with bias, dbias (N) float32, dz's sum over rows (else None).
+
+    dz is the product's gradient; the residual's is dy.  dy, z and gate are (M, N) of one dtype, rows possibly further
+    apart.  out: the pair (dz, dgate), which may be any of dy, z and gate."""
+    e = _env or _torch()
+    if out is None and stream is None and workspace is None and e.fast is not None:
+        done = e.fast.activation_backward(dy, z, activation, gate, bias)
+        if done is not None:
+            return done
+    act = _activation(activation)
+    dt = e.dt.get(dy.dtype)
+    if dt is None:
+        _refuse(MXG_ERR_FMT, "dy must be float32, bfloat16 or float16")
+    if dy.dim() != 2:
+        _refuse(MXG_ERR_SHAPE, "dy must be (M, N)")
+    shape = m, n = tuple(dy.shape)
+    dz = dgate = None
+    if out is not None:
+        dz, dgate = out
+        if dz is None or (dgate is None) != (gate is None):
+            _refuse(MXG_ERR_NULL, "out must hold dz, and dgate with a gate")
+    lds = [_beside(t, shape, dy.dtype, name) for t, name in ((dy, "dy"), (z, "z"), (gate, "gate"), (dz, "dz"), (dgate, "dgate"))]
+    _no_history(e, dy, z, gate, dz, dgate)
+    _here(dy.get_device(), z, gate, dz, dgate, workspace)
+    given = 0 if workspace is None else _workspace_bytes(workspace)
+    if out is None:
+        dz = _empty(e, shape, dy.dtype, dy.device, stream)
+        lds[3] = lds[4] = n
+        if gate is not None:
+            dgate = _empty(e, shape, dy.dtype, dy.device, stream)
+    dbias = _empty(e, (n,), e.f32, dy.device, stream) if bias else None
+    need = _lib.mxgemm_activation_backward_workspace_bytes(m, n) if bias else 0
+    if need and workspace is None:
+        workspace, given = _empty(e, (need,), e.u8, dy.device, stream, True), need
+    st = _lib.mxgemm_activation_backward(dy.data_ptr(), z.data_ptr(), _ptr(gate), dz.data_ptr(), _ptr(dgate), _ptr(dbias),
+                                         (ctypes.c_int64 * 5)(*lds), m, n, act, dt, MXG_TRUSTED_POINTERS, _ptr(workspace),
+                                         given, _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    if out is not None:
+        _changed(e, dz, dgate)
+    return dz, dgate, dbias
+
+
+def group_blocks(rows, groups):
+    """C-ABI mxgemm_group_blocks: the blocks of 128 along the rows that so many groups of so many rows in all can have."""
+    return _lib.mxgemm_group_blocks(rows, groups)
+
+
+def _groups(e, offsets):
+    """(groups, flags) of the offsets of rows in groups."""
+    if offsets is None:
+        _refuse(MXG_ERR_NULL, "offsets must be given")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        _refuse(MXG_ERR_SHAPE, "offsets must be (groups + 1)")
+    if offsets.dtype not in (e.i32, e.i64):
+        _refuse(MXG_ERR_FMT, "offsets must be int32 or int64")
+    if not offsets.is_contiguous():
+        _refuse(MXG_ERR_ALIGN, "offsets must be contiguous")
+    return offsets.shape[0] - 1, MXG_TRUSTED_POINTERS | (MXG_GROUP_OFFSETS64 if offsets.dtype == e.i64 else 0)
+
+
+def _quantize_grouped(e, x, offsets, fmt, rows, cols, square, pow2, out, stream):
+    """block128_quantize of rows in groups."""
+    if not cols or square:
+        _refuse(MXG_ERR_FLAGS, "offsets matter to blocks along the rows: they go with cols and without square")
+    if out is None and stream is None and e.fast is not None:
+        done = e.fast.quantize_grouped(x, offsets, fmt, rows, pow2)
+        if done is not None:
+            return done
+    dt, f8 = e.dt.get(x.dtype), e.code.get(fmt)
+    if dt is None:
+        _refuse(MXG_ERR_FMT, "x must be float32, bfloat16 or float16")
+    if f8 is None:
+        _refuse(MXG_ERR_FMT, "fmt must be MXG_FMT_E4M3 or MXG_FMT_E5M2")
+    if x.dim() != 2:
+        _refuse(MXG_ERR_SHAPE, "x must be (T, K)")
+    groups, flags = _groups(e, offsets)
+    _, _, t, k, ldx = _matrix_rows(x, "x")
+    blocks, kb = _lib.mxgemm_group_blocks(t, groups), -(-k // 128)
+    shapes = (((t, -(-k // 16) * 16), f8, "q"), ((kb, t), e.f32, "s"), ((k, 128 * blocks), f8, "qt"), ((blocks, k), e.f32, "st"))
+    wanted = (rows, rows, True, True)
+    _here(x.get_device(), offsets, *(out or ()))
+    if out is None:
+        made = tuple(_empty(e, shape, dtype, x.device, stream) if w else None for (shape, dtype, _), w in zip(shapes, wanted))
+    else:
+        made = tuple(out)
+        for given, (shape, dtype, name), w in zip(made, shapes, wanted):
+            if (given is not None) != bool(w):
+                _refuse(MXG_ERR_NULL, f"{name} given but not asked for, or the reverse")
+            if w:
+                _expect(given, shape, dtype, name)
+    q, s, qt, st = made
+    status = _lib.mxgemm_block128_quantize_grouped(_ptr(x), ldx, _ptr(offsets), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), t,
+                                                   groups, k, dt, fmt, flags | (MXG_QUANT_POW2 if pow2 else 0),
+                                                   _stream(stream))
+    if status != MXG_OK:
+        _raise(status)
+    if out is not None:
+        _changed(e, *made)
+    return made
+
+
+def block128_grouped_gemm(a, sa, b, sb, offsets, activation=None, gate=None, preact=False, c_dtype=None, c=None, stream=None):
+    """C-ABI mxgemm_block128_grouped: products of rows in groups (tokens in order of their experts), each group with a b of
+    its own: with e the group of row t,
+
+        z[t] = a[t] b[e]^T,  c[t] = act(z[t]) * gate[t]
+
+    a (T, K) codes with sa (ceil(K/128), T), b (E, N, K) codes with sb (E, ceil(N/128), ceil(K/128)).  offsets (E + 1),
+    int32 or int64 on the device: group e is rows offsets[e] to offsets[e + 1], which must not decrease; the sizes are read by the
+    kernel and need not be known on the host.  Groups may be empty.  Rows before the first group and behind the last one
+    are left as they were in a given c, and zero in a new one and in z.  E is at most 1024, T at most 2^24.
+
+    activation, gate, preact, c_dtype and the refusal of inputs that require gradients as in block128_linear.  The input's
+    gradient is the same call with b's transposed codes; the weights' is block128_grouped_weight_gradient."""
+    e = _env or _torch()
+    if stream is None and e.fast is not None:
+        done = e.fast.grouped(a, sa, b, sb, offsets, activation, gate, preact, c_dtype, c)
+        if done is not None:
+            return done
+    groups, flags = _groups(e, offsets)
+    m, k, n, fa, fb = _operands(e, a, sa, b, sb, (groups,))
+    act = _activation(activation)
+    _no_history(e, gate, c)
+    _here(a.get_device(), sa, b, sb, offsets, gate, c)
+    c, ldc, own, z, ct = _product_out(e, m, n, c, c_dtype, preact, a.device, stream)
+    ends = _ends(e, act, None, gate, None, z, m, n, c.dtype)
+    st = _lib.mxgemm_block128_grouped(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), offsets.data_ptr(),
+                                      c.data_ptr(), ldc, m, groups, n, k, fa, fb, ct, ctypes.byref(ends),
+                                      flags | MXG_GROUP_ZERO_PREACT | (MXG_GROUP_ZERO_REST if own else 0),
+                                      _stream(stream))
+    if st != MXG_OK:
+        _raise(st)
+    if not own:
+        _changed(e, c)
+    return (c, z) if preact else c
+
+
+def block128_grouped_weight_gradient(a, sa, b, sb, offsets, c=None, accumulate=False, stream=None):
+    """C-ABI mxgemm_block128_grouped_weight_gradient: one product over the rows of each group, c (E, M, N) float32, from the
+    operands that block128_quantize(..., cols=True, offsets=offsets) makes: a (M, 128 G) codes with sa (G, M) and b
+    (N, 128 G) with sb (G, N).  With a of the output's gradient and b of the input it is the weights' gradient.  Zero
+    for a group without rows.  c: the output, whose rows may be further apart than N; accumulate adds to it.  Exact up to
+    float32 rounding."""
+    e = _env or _torch()
+    if stream is None and e.fast is not None:
+        done = e.fast.grouped_weight_gradient(a, sa, b, sb, offsets, c, accumulate)
+        if done is not None:
+            return done
+    groups, flags = _groups(e, offsets)
+    fa, fb = e.fmt.get(a.dtype), e.fmt.get(b.dtype)
+    if fa is None or fb is None:
+        _refuse(MXG_ERR_FMT, "a and b must be float8_e4m3fn or float8_e5m2")
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1] or a.shape[1] % 128:
+        _refuse(MXG_ERR_SHAPE, "a and b must be (M, 128 G) and (N, 128 G)")
+    m, n, blocks = a.shape[0], b.shape[0], a.shape[1] // 128
+    if sa is None or sb is None:
+        _refuse(MXG_ERR_NULL, "sa and sb must be given")
+    _expect(sa, (blocks, m), e.f32, "sa")
+    _expect(sb, (blocks, n), e.f32, "sb")
+    if not a.is_contiguous() or not b.is_contiguous():
+        _refuse(MXG_ERR_ALIGN, "a and b must be contiguous")
+    if accumulate and c is None:
+        _refuse(MXG_ERR_NULL, "accumulate needs c")
+    own, ldc = c is None, n
+    if not own:
+        _no_history(e, c)
+        if c.shape != (groups, m, n):
+            _refuse(MXG_ERR_SHAPE, f"c must have shape {(groups, m, n)}, got {tuple(c.shape)}")
+        if c.dtype != e.f32:
+            _refuse(MXG_ERR_FMT, "c must be float32")
+        ldc = _matrix_rows(c, "c")[4]
+    _here(a.get_device(), sa, b, sb, offsets, c)
+    if own:
+        c = _empty(e, (groups, m, n), e.f32, a.device, stream)
+    st = _lib.mxgemm_block128_grouped_weight_gradient(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(),
+                                                      offsets.data_ptr(), c.data_ptr(), ldc, blocks, groups, m, n, fa, fb,
+                                                      flags | (MXG_B128_ACCUMULATE if accumulate else 0), _stream(stream))
     if st != MXG_OK:
         _raise(st)
     if not own:
@@ -1081,4 +1436,7 @@ __all__ = [
     "MXG_DT_F32", "MXG_DT_BF16", "MXG_DT_F16", "MXG_QUANT_SQUARE", "MXG_QUANT_POW2", "MXG_B128_B_ROWS",
     "MXG_B128_ACCUMULATE", "MXG_ROPE_HALF", "MXG_ROPE_INTERLEAVED", "MXG_ROPE_INTERLEAVED_TO_HALF",
     "MXG_ROPE_TRANSPOSE", "MXG_ROPE_POS64", "MXG_TRUSTED_POINTERS",
+    "block128_linear", "activation_backward", "group_blocks", "block128_grouped_gemm", "block128_grouped_weight_gradient",
+    "MXG_ACT_NONE", "MXG_ACT_RELU", "MXG_ACT_SILU", "MXG_ACT_GELU", "MXG_ACT_GELU_TANH", "MXG_GROUP_OFFSETS64",
+    "MXG_GROUP_ZERO_REST", "MXG_GROUP_ZERO_PREACT",
 ]

@@ -20,7 +20,11 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mxgemm.hip", "launch_t256_bf16_f32.h
                                            "launch_t128_mj.hip", "probes.hip", "block128.hip", "block128_tile256.hip",
                                            "block128_tile128x256.hip", "block128_tile128.hip",
                                            "block128_tile64x128.hip", "block128_tile64.hip",
-                                           "block128_exact.hip", "block128_rows.hip", "heads.hip")]
+                                           "block128_exact.hip", "block128_rows.hip", "block128_more256.hip",
+                                           "block128_more128x256.hip", "block128_more128.hip", "block128_more64x128.hip",
+                                           "block128_more64.hip", "block128_more_exact_large.hip",
+                                           "block128_more_exact_small.hip", "block128_more_rows.hip",
+                                           "block128_grouped.hip", "activation.hip", "heads.hip")]
 LIB = os.path.join(PKG_DIR, "libmxgemm.so")
 # The torch wrappers' short way into the library (host code only, against torch's headers).
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")

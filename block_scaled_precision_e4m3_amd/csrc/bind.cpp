@@ -228,6 +228,187 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return THPVariable_Wrap(c);
 }
 
+// The number of an activation's name; -1 for another.
+int activation_of(PyObject* o) {
+  if (o == Py_None) return MXG_ACT_NONE;
+  if (!PyUnicode_Check(o)) return -1;
+  static const char* const names[] = {nullptr, "relu", "silu", "gelu", "gelu_tanh"};
+  for (int i = 1; i < 5; ++i)
+    if (PyUnicode_CompareWithASCIIString(o, names[i]) == 0) return i;
+  return -1;
+}
+
+// A (M, N) tensor with contiguous columns and its row distance: as the wrapper has it.
+bool beside(const Tensor* t, int64_t m, int64_t n, at::ScalarType type, int dev, int64_t* ld) {
+  *ld = n;
+  if (!t) return true;
+  if (t->dim() != 2 || t->size(0) != m || t->size(1) != n || t->scalar_type() != type || !on(*t, dev)) return false;
+  if (m > 1) *ld = t->stride(0);
+  return (n <= 1 || t->stride(1) == 1) && *ld >= n;
+}
+
+// Offsets of rows in groups.
+bool groups_of(const Tensor* t, int dev, int64_t* groups, unsigned* flags) {
+  if (!t || t->dim() != 1 || t->size(0) < 1 || !t->is_contiguous() || !on(*t, dev)) return false;
+  if (t->scalar_type() == at::kLong) *flags |= MXG_GROUP_OFFSETS64;
+  else if (t->scalar_type() != at::kInt) return false;
+  *groups = t->size(0) - 1;
+  return true;
+}
+
+// What linear and grouped share: the operands (groups < 0: one b), C and preact, and what follows the product.
+struct Product {
+  const Tensor *a, *sa, *b, *sb, *given;
+  int dev, fa, fb, ct;
+  int64_t m, n, k, ldc;
+  Tensor c, z;
+  mxgemm_ends_t ends{};
+};
+bool product(PyObject* a, PyObject* sa, PyObject* b, PyObject* sb, PyObject* bias, PyObject* act, PyObject* gate,
+             PyObject* residual, PyObject* preact, PyObject* c_dtype, PyObject* c, int64_t groups, Product* p) {
+  bool other = false;
+  p->a = tensor(a, &other);
+  p->sa = tensor(sa, &other);
+  p->b = tensor(b, &other);
+  p->sb = tensor(sb, &other);
+  p->given = tensor(c, &other);
+  const Tensor *tb = bias ? tensor(bias, &other) : nullptr, *tg = tensor(gate, &other),
+               *tr = residual ? tensor(residual, &other) : nullptr;
+  if (other || !p->a || !p->sa || !p->b || !p->sb) return false;
+  const int64_t nd = groups < 0 ? 2 : 3;
+  const Tensor &A = *p->a, &B = *p->b;
+  p->fa = fmt_of(A.scalar_type());
+  p->fb = fmt_of(B.scalar_type());
+  p->dev = A.is_cuda() ? A.get_device() : -1;
+  if (p->fa < 0 || p->fb < 0 || A.dim() != 2 || B.dim() != nd || (groups >= 0 && B.size(0) != groups) || !current(p->dev) ||
+      !on(A, p->dev) || !on(B, p->dev) || !A.is_contiguous() || !B.is_contiguous())
+    return false;
+  p->m = A.size(0);
+  p->k = A.size(1);
+  p->n = B.size(nd - 2);
+  if (B.size(nd - 1) != p->k) return false;
+  const int64_t kb = cdiv(p->k, 128), want[3] = {groups, cdiv(p->n, 128), kb};
+  if (!floats(*p->sa, {kb, p->m}, p->dev) || !floats(*p->sb, {want + 3 - nd, (size_t)nd}, p->dev)) return false;
+  if (history({tb, tg, tr, p->given})) return false;
+  at::ScalarType type = p->given ? p->given->scalar_type() : at::kBFloat16;
+  if (c_dtype != Py_None) {
+    if (!THPDtype_Check(c_dtype)) return false;
+    const at::ScalarType asked = reinterpret_cast<THPDtype*>(c_dtype)->scalar_type;
+    if (p->given && asked != type) return false;
+    type = asked;
+  }
+  p->ct = dt_of(type);
+  p->ends.activation = activation_of(act);
+  if (p->ct < 0 || p->ends.activation < 0 || !beside(p->given, p->m, p->n, type, p->dev, &p->ldc) ||
+      !beside(tg, p->m, p->n, type, p->dev, &p->ends.ldgate) || !beside(tr, p->m, p->n, type, p->dev, &p->ends.ldresidual))
+    return false;
+  if (tb) {
+    p->ends.bias_dtype = dt_of(tb->scalar_type());
+    if (tb->dim() != 1 || tb->size(0) != p->n || !tb->is_contiguous() || !on(*tb, p->dev) ||
+        (tb->scalar_type() != type && tb->scalar_type() != at::kFloat))
+      return false;
+    p->ends.bias = tb->data_ptr();
+  }
+  if (tg) p->ends.gate = tg->data_ptr();
+  if (tr) p->ends.residual = tr->data_ptr();
+  p->c = p->given ? *p->given : fresh({p->m, p->n}, type, A);
+  if (truth(preact)) {
+    p->z = fresh({p->m, p->n}, type, A);
+    p->ends.preact = p->z.data_ptr();
+    p->ends.ldpreact = p->n;
+  }
+  return true;
+}
+PyObject* product_out(const Product& p, PyObject* c) {
+  PyObject* first = c;
+  if (p.given) {
+    changed(*p.given);
+    Py_INCREF(c);
+  } else {
+    first = THPVariable_Wrap(p.c);
+  }
+  if (!p.z.defined() || !first) return first;
+  PyObject *second = THPVariable_Wrap(p.z), *out = second ? PyTuple_New(2) : nullptr;
+  if (!out) {
+    Py_XDECREF(second);
+    Py_DECREF(first);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(out, 0, first);
+  PyTuple_SET_ITEM(out, 1, second);
+  return out;
+}
+
+// linear(a, sa, b, sb, bias, activation, gate, residual, preact, c_dtype, c)
+PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  Product p;
+  if (n != 11 || !product(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], -1, &p)) return none();
+  Tensor ws;
+  const size_t need = mxgemm_block128_workspace_bytes(p.m, p.n, p.k, 1, p.ct);
+  if (need) ws = fresh({(int64_t)need}, at::kByte, *p.a);
+  const int status = mxgemm_block128_linear(p.a->data_ptr(), p.sa->data_ptr<float>(), p.b->data_ptr(), p.sb->data_ptr<float>(),
+                                            p.c.data_ptr(), p.ldc, p.m, p.n, p.k, p.fa, p.fb, p.ct, &p.ends, kTrusted,
+                                            need ? ws.data_ptr() : nullptr, need, stream_of(p.dev));
+  if (status != MXG_OK) return refused(status);
+  return product_out(p, v[10]);
+}
+
+// grouped(a, sa, b, sb, offsets, activation, gate, preact, c_dtype, c)
+PyObject* grouped(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (n != 10) return none();
+  bool other = false;
+  const Tensor *a = tensor(v[0], &other), *offsets = tensor(v[4], &other);
+  int64_t groups = 0;
+  unsigned flags = kTrusted | MXG_GROUP_ZERO_PREACT;
+  Product p;
+  if (!a || !a->is_cuda() || !groups_of(offsets, a->get_device(), &groups, &flags) ||
+      !product(v[0], v[1], v[2], v[3], nullptr, v[5], v[6], nullptr, v[7], v[8], v[9], groups, &p))
+    return none();
+  if (!p.given) flags |= MXG_GROUP_ZERO_REST;
+  const int status = mxgemm_block128_grouped(p.a->data_ptr(), p.sa->data_ptr<float>(), p.b->data_ptr(), p.sb->data_ptr<float>(),
+                                             offsets->data_ptr(), p.c.data_ptr(), p.ldc, p.m, groups, p.n, p.k, p.fa, p.fb,
+                                             p.ct, &p.ends, flags, stream_of(p.dev));
+  if (status != MXG_OK) return refused(status);
+  return product_out(p, v[9]);
+}
+
+// grouped_weight_gradient(a, sa, b, sb, offsets, c, accumulate)
+PyObject* grouped_weight_gradient(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (n != 7) return none();
+  bool other = false;
+  const Tensor *a = tensor(v[0], &other), *sa = tensor(v[1], &other), *b = tensor(v[2], &other), *sb = tensor(v[3], &other),
+               *offsets = tensor(v[4], &other), *given = tensor(v[5], &other);
+  const bool accumulate = truth(v[6]);
+  if (other || !a || !sa || !b || !sb || (accumulate && !given) || history({given})) return none();
+  const int fa = fmt_of(a->scalar_type()), fb = fmt_of(b->scalar_type()), dev = a->is_cuda() ? a->get_device() : -1;
+  int64_t groups = 0;
+  unsigned flags = kTrusted | (accumulate ? MXG_B128_ACCUMULATE : 0u);
+  if (fa < 0 || fb < 0 || a->dim() != 2 || b->dim() != 2 || a->size(1) != b->size(1) || a->size(1) % 128 != 0 || !current(dev) ||
+      !on(*a, dev) || !on(*b, dev) || !a->is_contiguous() || !b->is_contiguous() || !groups_of(offsets, dev, &groups, &flags))
+    return none();
+  const int64_t rows = a->size(0), cols = b->size(0), blocks = a->size(1) / 128;
+  if (!floats(*sa, {blocks, rows}, dev) || !floats(*sb, {blocks, cols}, dev)) return none();
+  int64_t ldc = cols;
+  if (given) {
+    const Rows r = rows_of(*given);
+    if (!r.ok || given->dim() != 3 || r.l != groups || r.m != rows || r.k != cols || given->scalar_type() != at::kFloat ||
+        !on(*given, dev))
+      return none();
+    ldc = r.ld;
+  }
+  const Tensor c = given ? *given : fresh({groups, rows, cols}, at::kFloat, *a);
+  const int status = mxgemm_block128_grouped_weight_gradient(a->data_ptr(), sa->data_ptr<float>(), b->data_ptr(),
+                                                             sb->data_ptr<float>(), offsets->data_ptr(), c.data_ptr<float>(),
+                                                             ldc, blocks, groups, rows, cols, fa, fb, flags, stream_of(dev));
+  if (status != MXG_OK) return refused(status);
+  if (given) {
+    changed(*given);
+    Py_INCREF(v[5]);
+    return v[5];
+  }
+  return THPVariable_Wrap(c);
+}
+
 // Heads (T, H, D) with contiguous features.
 bool heads(const Tensor& t, int dev) { return t.dim() == 3 && (t.size(2) <= 1 || t.stride(2) == 1) && on(t, dev); }
 
@@ -399,6 +580,66 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return pack({&xq, k_out, &dwq, s.k ? &dwk : nullptr});
 }
 
+// quantize_grouped(x, offsets, fmt, rows, pow2)
+PyObject* quantize_grouped(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (n != 5) return none();
+  bool other = false;
+  const Tensor *x = tensor(v[0], &other), *offsets = tensor(v[1], &other);
+  int64_t fmt = 0, groups = 0;
+  if (!x || !integer(v[2], &fmt) || (fmt != MXG_FMT_E4M3 && fmt != MXG_FMT_E5M2)) return none();
+  const bool rows = truth(v[3]), pow2 = truth(v[4]);
+  const int dt = dt_of(x->scalar_type()), dev = x->is_cuda() ? x->get_device() : -1;
+  unsigned flags = kTrusted | (pow2 ? MXG_QUANT_POW2 : 0u);
+  if (dt < 0 || x->dim() != 2 || !current(dev) || !on(*x, dev) || !groups_of(offsets, dev, &groups, &flags)) return none();
+  const Rows r = rows_of(*x);
+  if (!r.ok) return none();
+  const int64_t blocks = mxgemm_group_blocks(r.m, groups);
+  const at::ScalarType f8 = fmt == MXG_FMT_E4M3 ? at::kFloat8_e4m3fn : at::kFloat8_e5m2;
+  Tensor q, s;
+  if (rows) {
+    q = fresh({r.m, cdiv(r.k, 16) * 16}, f8, *x);
+    s = fresh({cdiv(r.k, 128), r.m}, at::kFloat, *x);
+  }
+  const Tensor qt = fresh({r.k, 128 * blocks}, f8, *x), st = fresh({blocks, r.k}, at::kFloat, *x);
+  const int status = mxgemm_block128_quantize_grouped(
+      x->data_ptr(), r.ld, offsets->data_ptr(), rows ? q.data_ptr() : nullptr, rows ? s.data_ptr<float>() : nullptr,
+      qt.data_ptr(), st.data_ptr<float>(), r.m, groups, r.k, dt, (int)fmt, flags, stream_of(dev));
+  if (status != MXG_OK) return refused(status);
+  return pack({rows ? &q : nullptr, rows ? &s : nullptr, &qt, &st});
+}
+
+// activation_backward(dy, z, activation, gate, bias)
+PyObject* activation_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (n != 5) return none();
+  bool other = false;
+  const Tensor *dy = tensor(v[0], &other), *z = tensor(v[1], &other), *gate = tensor(v[3], &other);
+  const int act = activation_of(v[2]);
+  const bool bias = truth(v[4]);
+  if (other || !dy || !z || act < 0 || dy->dim() != 2 || history({dy, z, gate})) return none();
+  const int dt = dt_of(dy->scalar_type()), dev = dy->is_cuda() ? dy->get_device() : -1;
+  const int64_t m = dy->size(0), cols = dy->size(1);
+  const at::ScalarType type = dy->scalar_type();
+  int64_t strides[5] = {cols, cols, cols, cols, cols};
+  if (dt < 0 || !current(dev) || !beside(dy, m, cols, type, dev, strides) || !beside(z, m, cols, type, dev, strides + 1) ||
+      !beside(gate, m, cols, type, dev, strides + 2))
+    return none();
+  const Tensor dz = fresh({m, cols}, type, *dy);
+  Tensor dgate, dbias, ws;
+  if (gate) dgate = fresh({m, cols}, type, *dy);
+  size_t need = 0;
+  if (bias) {
+    dbias = fresh({cols}, at::kFloat, *dy);
+    need = mxgemm_activation_backward_workspace_bytes(m, cols);
+    if (need) ws = fresh({(int64_t)need}, at::kByte, *dy);
+  }
+  const int status = mxgemm_activation_backward(dy->data_ptr(), z->data_ptr(), data(gate), dz.data_ptr(),
+                                                gate ? dgate.data_ptr() : nullptr, bias ? dbias.data_ptr<float>() : nullptr,
+                                                strides, m, cols, act, dt, kTrusted, need ? ws.data_ptr() : nullptr, need,
+                                                stream_of(dev));
+  if (status != MXG_OK) return refused(status);
+  return pack({&dz, gate ? &dgate : nullptr, bias ? &dbias : nullptr});
+}
+
 // C++ exceptions (an allocation that fails) become Python's.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -418,6 +659,11 @@ PyMethodDef methods[] = {
     {"on_status", on_status, METH_O, nullptr},
     {"quantize", (PyCFunction)(void*)guarded<quantize>, METH_FASTCALL, nullptr},
     {"gemm", (PyCFunction)(void*)guarded<gemm>, METH_FASTCALL, nullptr},
+    {"linear", (PyCFunction)(void*)guarded<linear>, METH_FASTCALL, nullptr},
+    {"activation_backward", (PyCFunction)(void*)guarded<activation_backward>, METH_FASTCALL, nullptr},
+    {"quantize_grouped", (PyCFunction)(void*)guarded<quantize_grouped>, METH_FASTCALL, nullptr},
+    {"grouped", (PyCFunction)(void*)guarded<grouped>, METH_FASTCALL, nullptr},
+    {"grouped_weight_gradient", (PyCFunction)(void*)guarded<grouped_weight_gradient>, METH_FASTCALL, nullptr},
     {"rope", (PyCFunction)(void*)guarded<rope>, METH_FASTCALL, nullptr},
     {"qk_norm_rope", (PyCFunction)(void*)guarded<qk_norm_rope>, METH_FASTCALL, nullptr},
     {"qk_norm_rope_backward", (PyCFunction)(void*)guarded<qk_norm_rope_backward>, METH_FASTCALL, nullptr},

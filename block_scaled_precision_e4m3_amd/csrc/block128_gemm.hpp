@@ -8,11 +8,19 @@
 // by the product of its two scales, which are float32 and cannot ride on the
 // matrix cores' power-of-two scales.  Few rows of A go through a third kernel
 // that reads B straight from memory.
+//
+// The same kernels take four forms (Form): the plain product; one with bias,
+// activation, gate and residual before C is stored; rows of A in groups, each
+// with a B of its own; and groups along K, a product for each.  In the last two
+// a workgroup first adds up the groups' tiles or blocks from the offsets in
+// device memory and keeps the table in LDS.
 #pragma once
 
 #include <type_traits>
 
 #include "dtypes.hpp"
+#include "ends.hpp"
+#include "groups.hpp"
 
 namespace mxg {
 namespace b128 {
@@ -34,6 +42,22 @@ struct GemmParams {
   bool b_rows, accumulate;
   bool c_vec;        // base, ldc and N in multiples of 16 bytes: every store of C is a whole one
 };
+
+enum Form {
+  kPlain,
+  kEnds,        // C = act(product + bias) gate + residual
+  kRowGroups,   // A (M, K), B (E, N, K): C's rows of group e from B[e]; with kEnds' activation and gate
+  kDeepGroups,  // A (M, K), B (N, K), scales in rows of blocks: C[e] (E, M, N) over the blocks of K that are group e's
+};
+struct MoreParams : GemmParams {
+  ends::Ends ends;
+  groups::Groups groups;
+  bool zero_c, zero_z;  // kRowGroups: rows of no group become zero (or are left alone), in C and in what is kept of z
+};
+template <Form FORM>
+using params_t = std::conditional_t<FORM == kPlain, GemmParams, MoreParams>;
+constexpr bool has_ends(Form f) { return f == kEnds || f == kRowGroups; }
+constexpr bool has_groups(Form f) { return f == kRowGroups || f == kDeepGroups; }
 
 // 16 bytes where an element of C may lie: gfx950 takes 16-byte accesses at any alignment.
 typedef v4u v4u_at2 __attribute__((aligned(2)));
@@ -73,29 +97,65 @@ __device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t rs, unsigned voff
 #pragma clang diagnostic pop
 
 struct TileAt {
-  int l, m0, n0;
+  int l, m0, n0;  // batch or group, first row and column
+  int rows;       // rows of the tile that there are
 };
 struct Part {
-  int at, count;  // first step and number of steps
+  int at, count;  // first block of K and number of steps
+  int end;        // block of K behind the last (kDeepGroups; elsewhere K ends the last block)
 };
-template <class T>
-__device__ __forceinline__ Part part_of(const GemmParams& p, int item) {
-  if (!T::kParts || p.splits == 1) return {0, p.steps};
-  const int at = __builtin_amdgcn_readfirstlane(item / p.num_tiles * p.per);
-  return {at, min(p.per, p.steps - at)};
-}
-// Tile t: batches, then groups of kGroupM tile rows walked column by column.  A work item is a tile and a part of
-// its K; items of one part follow each other.
-template <class T>
-__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
-  constexpr int bm = T::kBM, bn = T::kBN;
-  if (T::kParts && p.splits > 1) t %= p.num_tiles;
-  const int per = p.tilesM * p.tilesN, l = t / per, r = t - l * per;
-  const int group = kGroupM * p.tilesN, g = r / group, first = g * kGroupM;
-  const int rows = min(p.tilesM - first, kGroupM), rg = r - g * group;
-  return {__builtin_amdgcn_readfirstlane(l), __builtin_amdgcn_readfirstlane((first + rg % rows) * bm),
-          __builtin_amdgcn_readfirstlane(rg / rows * bn)};
-}
+
+// What a kernel walks over: its parameters, and for groups the table of them and the group met last (items only grow).
+template <class T, Form FORM>
+struct Walk {
+  const params_t<FORM>& p;
+  const groups::Table* table;
+  int lane;
+  int group = 0;
+
+  __device__ __forceinline__ int items() const {
+    if constexpr (FORM == kRowGroups) return __builtin_amdgcn_readfirstlane(table->units[p.groups.E]) * p.tilesN;
+    else return T::kParts && FORM == kPlain ? p.num_tiles * p.splits : p.num_tiles;
+  }
+  __device__ __forceinline__ Part part(int item) {
+    if constexpr (FORM == kDeepGroups) {
+      // a group without rows takes one step in which everything reads as zero
+      const int e = item / (p.tilesM * p.tilesN);
+      const int from = __builtin_amdgcn_readfirstlane(table->units[e]);
+      const int to = __builtin_amdgcn_readfirstlane(table->units[e + 1]);
+      return {from, max(1, (to - from + T::kKB - 1) / T::kKB), to};
+    } else {
+      if (!T::kParts || FORM != kPlain || p.splits == 1) return {0, p.steps, 0};
+      const int at = __builtin_amdgcn_readfirstlane(item / p.num_tiles * p.per);
+      return {T::kKB * at, min(p.per, p.steps - at), 0};
+    }
+  }
+  // Tile t: batches, then groups of kGroupM tile rows walked column by column.  A work item is a tile and a part of
+  // its K; items of one part follow each other.
+  __device__ __forceinline__ TileAt tile(int t) {
+    constexpr int bm = T::kBM, bn = T::kBN;
+    if (T::kParts && FORM == kPlain && p.splits > 1) t %= p.num_tiles;
+    int l, r, rows_of_tiles = p.tilesM, m_at = 0, m_end = p.M;
+    if constexpr (FORM == kRowGroups) {
+      l = group = groups::lookup(table, p.groups.E, t / p.tilesN, group, lane);
+      const int before = __builtin_amdgcn_readfirstlane(table->units[l]);
+      rows_of_tiles = __builtin_amdgcn_readfirstlane(table->units[l + 1]) - before;
+      m_at = __builtin_amdgcn_readfirstlane(table->start[l]);
+      m_end = __builtin_amdgcn_readfirstlane(table->start[l + 1]);
+      r = t - before * p.tilesN;
+    } else {
+      const int per = p.tilesM * p.tilesN;
+      l = t / per;
+      r = t - l * per;
+    }
+    const int group_items = kGroupM * p.tilesN, g = r / group_items, first = g * kGroupM;
+    const int rows = min(rows_of_tiles - first, kGroupM), rg = r - g * group_items;
+    TileAt at = {__builtin_amdgcn_readfirstlane(l), __builtin_amdgcn_readfirstlane(m_at + (first + rg % rows) * bm),
+                 __builtin_amdgcn_readfirstlane(rg / rows * bn), 0};
+    at.rows = min(m_end - at.m0, bm);
+    return at;
+  }
+};
 
 // The workgroup's stream of K steps, tile after tile.  A step is one scale
 // block: 128 bytes of every row of A and B and the scales beside them, by
@@ -107,9 +167,10 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
 // patterns); the swizzles let each pass cover all 64 banks.  Rows past the
 // matrix fall past the resource and chunks past K get an offset that does:
 // both read as zero.
-template <class T, bool BROWS, int (*SwA)(int), int (*SwB)(int)>
+template <class T, bool BROWS, int (*SwA)(int), int (*SwB)(int), Form FORM>
 struct Stream {
-  const GemmParams& p;
+  const params_t<FORM>& p;
+  Walk<T, FORM> walk;
   const int wave, G, items;
   int item, left = 0;       // of the next step to fetch: its work item and the steps that are left of it
   unsigned k;               // and its first K
@@ -119,9 +180,11 @@ struct Stream {
   unsigned sc_bytes, sc_voff;
   int64_t sc_inc;           // bytes from one block's scales to the next one's: past 32 bits for 2^30 rows
   unsigned base, va[T::kKB], vb[T::kKB];  // of the step being fetched
+  unsigned end_k = 0;       // kDeepGroups: where the group's blocks end
 
-  __device__ __forceinline__ Stream(const GemmParams& p_, const uint8_t* lds, int lane, int wave_, int first)
-      : p(p_), wave(wave_), G((int)gridDim.x), items(T::kParts ? p_.num_tiles * p_.splits : p_.num_tiles), item(first) {
+  __device__ __forceinline__ Stream(const params_t<FORM>& p_, const Walk<T, FORM>& walk_, const uint8_t* lds, int lane,
+                                    int wave_, int first)
+      : p(p_), walk(walk_), wave(wave_), G((int)gridDim.x), items(walk_.items()), item(first) {
     lds0 = lds_addr(lds);
     const int row = 8 * wave + (lane >> 3);
     chunk_a = (unsigned)((lane & 7) ^ SwA(row)) * 16;
@@ -136,40 +199,50 @@ struct Stream {
     open();
   }
   __device__ __forceinline__ void open() {
-    TileAt f{0, 0, 0};
+    TileAt f{0, 0, 0, 0};
     unsigned mv = 0, nv = 0;
     int at = 0;
     left = 0x7FFFFFFF;
     if (item < items) {
-      f = tile_at<T>(p, item);
-      mv = (unsigned)min(p.M - f.m0, T::kBM);
+      f = walk.tile(item);
+      mv = (unsigned)f.rows;
       nv = (unsigned)min(p.N - f.n0, T::kBN);
-      const Part part = part_of<T>(p, item);
-      at = T::kKB * part.at;
+      const Part part = walk.part(item);
+      at = part.at;
       left = part.count;
+      if constexpr (FORM == kDeepGroups) {
+        end_k = min(128u * (unsigned)part.end, (unsigned)p.K);
+        if (part.end <= part.at) mv = nv = 0;
+      }
     }
+    // batches of A and B: of one, groups share A or both
+    const int la = has_groups(FORM) ? 0 : f.l, lb = FORM == kDeepGroups ? 0 : f.l;
     k = 128u * (unsigned)at;
-    ra = make_rsrc(p.A + ((int64_t)f.l * p.M + f.m0) * p.K, mv * (unsigned)p.K);
-    rb = make_rsrc(p.B + ((int64_t)f.l * p.N + f.n0) * p.K, nv * (unsigned)p.K);
+    ra = make_rsrc(p.A + ((int64_t)la * p.M + f.m0) * p.K, mv * (unsigned)p.K);
+    rb = make_rsrc(p.B + ((int64_t)lb * p.N + f.n0) * p.K, nv * (unsigned)p.K);
     if (wave < T::kBM / 64) {
-      sc_at = (const char*)(p.SA + ((int64_t)f.l * p.Kb + at) * p.M + f.m0);
+      sc_at = (const char*)(p.SA + ((int64_t)la * p.Kb + at) * p.M + f.m0);
       sc_bytes = 4 * mv;
     } else if constexpr (BROWS) {
-      sc_at = (const char*)(p.SB + ((int64_t)f.l * p.Kb + at) * p.N + f.n0);
+      sc_at = (const char*)(p.SB + ((int64_t)lb * p.Kb + at) * p.N + f.n0);
       sc_bytes = 4 * nv;
     } else {
       const int nb = min(p.Nb - f.n0 / 128, (T::kBN + 127) / 128);
-      sc_at = (const char*)(p.SB + ((int64_t)f.l * p.Nb + f.n0 / 128) * p.Kb + at);
+      sc_at = (const char*)(p.SB + ((int64_t)lb * p.Nb + f.n0 / 128) * p.Kb + at);
       sc_bytes = nv ? 4u * (unsigned)((nb - 1) * p.Kb + 1) : 0u;
     }
     if (wave >= T::kBM / 64 + T::kBN / 64) sc_bytes = 0;
+  }
+  __device__ __forceinline__ unsigned past() const {
+    if constexpr (FORM == kDeepGroups) return end_k;
+    else return (unsigned)p.K;
   }
   __device__ __forceinline__ void begin(int stage) {
     base = lds0 + (unsigned)(stage * T::kStage) + 1024 * (unsigned)wave;
 #pragma unroll
     for (int b = 0; b < T::kKB; ++b) {
-      va[b] = k + 128 * b + chunk_a < (unsigned)p.K ? row_k + k + 128 * b + chunk_a : kOob;
-      vb[b] = k + 128 * b + chunk_b < (unsigned)p.K ? row_k + k + 128 * b + chunk_b : kOob;
+      va[b] = k + 128 * b + chunk_a < past() ? row_k + k + 128 * b + chunk_a : kOob;
+      vb[b] = k + 128 * b + chunk_b < past() ? row_k + k + 128 * b + chunk_b : kOob;
     }
   }
   // One of the step's kIssued DMA instructions (every wave issues as many, some on an empty resource, so that
@@ -181,7 +254,7 @@ struct Stream {
     else if (q < T::kDa + T::kDb) dma16_at(rb, vb[b] + (q - T::kDa) * next_k, to + T::kOffB + 1024 * T::kDmaWaves * (q - T::kDa));
     else {
       const bool any = wave < T::kBM / 64 + T::kBN / 64;
-      const bool in = T::kKB == 1 || k + 128 * b < (unsigned)p.K;  // a step's last blocks may lie past K
+      const bool in = T::kKB == 1 || k + 128 * b < past();  // a step's last blocks may lie past K
       dma4_at(make_rsrc(sc_at + (in ? b : 0) * sc_inc, in ? sc_bytes : 0u), sc_voff,
               any ? to + T::kOffSA - 768 * (unsigned)wave : lds0 + T::kStages * T::kStage);
     }
@@ -218,18 +291,58 @@ __device__ __forceinline__ void wait_step(bool stores_fixed, bool stores_behind)
 // A wave that only moves operands: it meets the computing waves at their barrier of every step, when its DMA of that
 // step has landed, and then refills the stage they have left.  A wave whose DMA instruction finds the queue full
 // issues nothing until it drains, which these waves can afford.
-template <class T, class S>
-__device__ __forceinline__ void produce(const GemmParams& p, S& in, int item, int items) {
+template <class T, class S, class W>
+__device__ __forceinline__ void produce(S& in, W& walk, int item, int items) {
   for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
   int stage = 0;
   for (; item < items; item += (int)gridDim.x)
-    for (int n = part_of<T>(p, item).count; n > 0; --n) {
+    for (int n = walk.part(item).count; n > 0; --n) {
       wait_vm<(T::kStages - 2) * T::kIssued>();
       barrier();
       in.all(stage == 0 ? T::kStages - 1 : stage - 1);
       stage = stage + 1 == T::kStages ? 0 : stage + 1;
     }
   wait_vm<0>();  // no DMA may land after the workgroup's LDS is handed on
+}
+
+// The table of a kernel's groups, filled by its first wave: rows in tiles of kBM, or blocks of 128.
+template <class T, Form FORM>
+__device__ __forceinline__ const groups::Table* group_table(const params_t<FORM>& p, int lane, int wave) {
+  if constexpr (has_groups(FORM)) {
+    __shared__ groups::Table table;
+    if (wave == 0) groups::fill(&table, p.groups, lane, FORM == kRowGroups ? T::kBM : 128, FORM == kRowGroups ? p.tilesM : p.Kb);
+    __syncthreads();
+    return &table;
+  } else {
+    return nullptr;
+  }
+}
+
+// The kernel's arguments, to be read where they are used: those of a tile's end are not to be kept in registers through
+// its K loop.
+template <Form FORM>
+__device__ __forceinline__ const __attribute__((address_space(4))) params_t<FORM>* late_params() {
+  auto p = (const __attribute__((address_space(4))) params_t<FORM>*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// Zeros in the rows of no group of C and of what is kept of z: those before the first group and behind the last one.
+// Thread `at` of `all` takes every all-th element.
+template <int CT>
+__device__ __forceinline__ void zero_rest(const MoreParams& p, int64_t at, int64_t all) {
+  using E = elem_t<CT>;
+  const bool of_c = p.zero_c, of_z = p.zero_z && p.ends.Z;
+  if (!of_c && !of_z) return;
+  const int head = groups::offset(p.groups, 0), tail = groups::offset(p.groups, p.groups.E);
+  const int64_t rows = head + (int64_t)(p.groups.T - tail);
+  if (rows <= 0) return;
+  E *c = static_cast<E*>(p.C), *z = static_cast<E*>(p.ends.Z);
+  for (int64_t i = at; i < rows * p.N; i += all) {
+    const int64_t row = i / p.N, n = i - row * p.N, m = row < head ? row : row - head + tail;
+    if (of_c) c[m * p.ldc + n] = (E)0.f;
+    if (of_z) z[m * p.ends.ldz + n] = (E)0.f;
+  }
 }
 
 __device__ __forceinline__ int first_tile_of(const GemmParams& p) {
@@ -257,8 +370,8 @@ __device__ __forceinline__ int first_tile_of(const GemmParams& p) {
 __device__ __forceinline__ int swizzle_a16(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swizzle_b16(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 
-template <class T, int FA, int FB, int CT, bool BROWS>
-__global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void block128_tile_kernel(GemmParams p) {
+template <class T, int FA, int FB, int CT, bool BROWS, Form FORM>
+__global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void block128_tile_kernel(params_t<FORM> p) {
   static_assert(CT != 0, "16-bit C");
   constexpr int kMt = T::kTM / 16, kNt = T::kTN / 16, kPairs = kNt / 2;
   constexpr int kStores = kMt * kPairs;                     // C store instructions per lane and tile
@@ -271,11 +384,12 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
   const int r = lane & 15, g = lane >> 4;
   const int G = (int)gridDim.x;
   int item = first_tile_of(p);
-  const int items = T::kParts ? p.num_tiles * p.splits : p.num_tiles;
-  Stream<T, BROWS, swizzle_a16, swizzle_b16> in(p, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
+  Walk<T, FORM> walk{p, group_table<T, FORM>(p, lane, wave), lane};
+  const int items = walk.items();
+  Stream<T, BROWS, swizzle_a16, swizzle_b16, FORM> in(p, walk, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
   if constexpr (T::kProducers > 0) {
     if (wave >= T::kWaves) {
-      produce<T>(p, in, item, items);
+      produce<T>(in, walk, item, items);
       return;
     }
   }
@@ -291,7 +405,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 
   if constexpr (T::kProducers == 0)
     for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
-  int step = 0, stage = 0, count = item < items ? part_of<T>(p, item).count : 0;
+  int step = 0, stage = 0, count = item < items ? walk.part(item).count : 0;
   bool stored = false;
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
   v4f acc[kMt][kNt];
@@ -373,9 +487,9 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
     if (++step == count) {
       step = 0;
       stored = true;
-      const TileAt at = tile_at<T>(p, item);
-      const int rows = min(p.M - at.m0, T::kBM);
-      if (T::kParts && p.splits > 1) {
+      const TileAt at = walk.tile(item);
+      const int rows = at.rows;
+      if (T::kParts && FORM == kPlain && p.splits > 1) {
         // a part's sums, four columns at a time (ldw is a multiple of 4)
         float* w = p.sums + (((int64_t)(item / p.num_tiles) * p.L + at.l) * p.M + at.m0) * p.ldw + at.n0;
 #pragma unroll
@@ -386,19 +500,18 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
             if (m < rows && at.n0 + n < p.ldw) *reinterpret_cast<v4f*>(w + (int64_t)m * p.ldw + n) = acc[mt][nt];
           }
         item += G;
-        count = item < items ? part_of<T>(p, item).count : 0;
+        count = item < items ? walk.part(item).count : 0;
         continue;
       }
       item += G;
-      count = item < items ? part_of<T>(p, item).count : 0;
+      count = item < items ? walk.part(item).count : 0;
       using E = elem_t<CT>;
-      E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
+      const int cols = min(p.N - at.n0, T::kBN);
       const bool odd = (r & 1) != 0;
       // stores 8 columns to a call; non-temporal: C is not read here, and keeping it would push A and B out of the
       // caches (8192 x 24576 x 1536: 341 -> 318 us)
-      auto put = [&](auto store) {
-#pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
+      auto put_row = [&](int mt, auto store) {
+        {
           v4u u[kPairs];
 #pragma unroll
           for (int h = 0; h < kPairs; ++h) {
@@ -433,22 +546,17 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
           }
         }
       };
-      if (p.c_vec) {
-        // N and ldc are multiples of 8 here: a lane's 8 columns lie inside or outside N together
-        int ldc = (int)p.ldc;
-        // with 16 scales more to a lane, the stores' offsets are made here, not kept in registers through the K loop
-        if constexpr (BROWS) asm volatile("" : "+s"(ldc));
-        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * ldc + min(p.N - at.n0, T::kBN)));
-        put([&](const v4u& u, int m, int n) {
+      // row mt of MFMAs to c, rows ldc apart.  Whole: N and ldc are multiples of 8, so a lane's 8 columns lie inside or
+      // outside N together.  Else 16-byte stores at any alignment but for the last columns of a row (8192 x 8191 x 1024:
+      // 184 us element by element).
+      auto whole = [&](int mt, __amdgpu_buffer_rsrc_t rc, int ldc) {
+        put_row(mt, [&](const v4u& u, int m, int n) {
           const unsigned off = m < rows && at.n0 + n < p.N ? 2u * (unsigned)(m * ldc + n) : kOob;
           __builtin_amdgcn_raw_buffer_store_b128(u, rc, (int)off, 0, 2);
         });
-      } else {
-        // 16-byte stores at any alignment but for the last columns of a row (8192 x 8191 x 1024: 184 us element by
-        // element)
-        int64_t ldc = p.ldc;
-        asm volatile("" : "+s"(ldc));  // as above
-        put([&](const v4u& u, int m, int n) {
+      };
+      auto pieces = [&](int mt, E* c, int64_t ldc) {
+        put_row(mt, [&](const v4u& u, int m, int n) {
           const int left = p.N - at.n0 - n;
           E* to = c + m * ldc + n;
           if (m < rows && left >= 8) {
@@ -459,10 +567,118 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
               if (e < left) to[e] = __builtin_bit_cast(E, (unsigned short)(u[e >> 1] >> (16 * (e & 1))));
           }
         });
+      };
+      if constexpr (!has_ends(FORM)) {
+        E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
+        if (p.c_vec) {
+          int ldc = (int)p.ldc;
+          // with 16 scales more to a lane, the stores' offsets are made here, not kept in registers through the K loop
+          if constexpr (BROWS) asm volatile("" : "+s"(ldc));
+          const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * ldc + cols));
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) whole(mt, rc, ldc);
+        } else {
+          int64_t ldc = p.ldc;
+          asm volatile("" : "+s"(ldc));  // as above
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) pieces(mt, c, ldc);
+        }
+      } else {
+        // One row of MFMAs after the other, and the tensors beside C asked for one row ahead: all at once would not fit
+        // the registers, which hold the sums of all rows.
+        const auto* q = late_params<FORM>();
+        const int64_t row0 = (FORM == kRowGroups ? 0 : (int64_t)at.l * q->M) + at.m0;
+        const bool vec = q->c_vec, gated = q->ends.gate != nullptr, residual = FORM == kEnds && q->ends.residual != nullptr;
+        const bool kept = q->ends.Z != nullptr;
+        const int ldc = (int)q->ldc, ldz = (int)q->ends.ldz, ldg = (int)q->ends.ldg, ldr = (int)q->ends.ldr;
+        E* c = static_cast<E*>(q->C) + row0 * ldc + at.n0;
+        E* z = static_cast<E*>(q->ends.Z) + row0 * ldz + at.n0;
+        const E* gate = static_cast<const E*>(q->ends.gate) + row0 * ldg + at.n0;
+        const E* more = static_cast<const E*>(q->ends.residual) + row0 * ldr + at.n0;
+        const int n_lane = T::kTN * wn + 8 * g;
+        struct Row {
+          Raw8<CT> at[kPairs];
+        };
+        auto load = [&](const E* from, int ld, int mt) {
+          Row w;
+          const int m = a_row + 16 * mt;
+          if (vec) {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, 2u * (unsigned)((rows - 1) * ld + cols));
+#pragma unroll
+            for (int h = 0; h < kPairs; ++h) {
+              const unsigned off = m < rows && n_lane + 32 * h < cols ? 2u * (unsigned)(m * ld + n_lane + 32 * h) : kOob;
+              w.at[h].w[0] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, 0, 0);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < kPairs; ++h)
+              w.at[h] = load_chunk<CT>(from + (int64_t)m * ld + n_lane + 32 * h, m < rows ? cols - n_lane - 32 * h : 0);
+          }
+          return w;
+        };
+        v4f bias[kNt];
+        if (q->ends.bias) {
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int n = n_lane + 32 * (nt >> 1) + 4 * (nt & 1) + i;
+              bias[nt][i] = n < cols ? ends::bias_at<CT>(q->ends.bias, q->ends.bias_f32, at.n0 + n) : 0.f;
+            }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) bias[nt] = zero;
+        }
+        const int act = q->ends.act;
+        Row gates[2], mores[2];
+        if (gated) gates[0] = load(gate, ldg, 0);
+        if (residual) mores[0] = load(more, ldr, 0);
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          if (mt + 1 < kMt) {
+            if (gated) gates[(mt + 1) & 1] = load(gate, ldg, mt + 1);
+            if (residual) mores[(mt + 1) & 1] = load(more, ldr, mt + 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (FORM == kEnds) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] += bias[nt];
+          }
+          if (kept) {
+            if (vec) whole(mt, make_rsrc(z, 2u * (unsigned)((rows - 1) * ldz + cols)), ldz);
+            else pieces(mt, z, ldz);
+          }
+          ends::with_activation<true>(act, [&](auto f) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[mt][nt][i] = f(acc[mt][nt][i]);
+          });
+          if (gated) {
+#pragma unroll
+            for (int h = 0; h < kPairs; ++h) {
+              const v8f v = widen8<CT>(gates[mt & 1].at[h]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) acc[mt][2 * h + (i >> 2)][i & 3] *= v[i];
+            }
+          }
+          if (residual) {
+#pragma unroll
+            for (int h = 0; h < kPairs; ++h) {
+              const v8f v = widen8<CT>(mores[mt & 1].at[h]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) acc[mt][2 * h + (i >> 2)][i & 3] += v[i];
+            }
+          }
+          if (vec) whole(mt, make_rsrc(c, 2u * (unsigned)((rows - 1) * ldc + cols)), ldc);
+          else pieces(mt, c, ldc);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   }
   wait_vm<0>();  // no DMA may land after the workgroup's LDS is handed on
+  if constexpr (FORM == kRowGroups) zero_rest<CT>(p, (int64_t)blockIdx.x * 64 * T::kWaves + threadIdx.x, (int64_t)G * 64 * T::kWaves);
 }
 
 // --- float32 C: codes widened to bfloat16 -----------------------------------------
@@ -481,8 +697,8 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 __device__ __forceinline__ int swizzle_a32(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swizzle_b32(int row) { return ((row >> 1) & 1) | ((row >> 3) & 2) | (row & 4); }
 
-template <class T, int FA, int FB, bool BROWS>
-__global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void block128_exact_kernel(GemmParams p) {
+template <class T, int FA, int FB, bool BROWS, Form FORM>
+__global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void block128_exact_kernel(params_t<FORM> p) {
   constexpr int kMt = T::kTM / 32, kNt = T::kTN / 32;  // a wave's MFMA blocks
   constexpr int kStores = 4 * kMt * kNt;               // C store instructions per lane and tile
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
@@ -492,11 +708,12 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
   const int r = lane & 31, h = lane >> 5;
   const int G = (int)gridDim.x;
   int item = first_tile_of(p);
-  const int items = T::kParts ? p.num_tiles * p.splits : p.num_tiles;
-  Stream<T, BROWS, swizzle_a32, swizzle_b32> in(p, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
+  Walk<T, FORM> walk{p, group_table<T, FORM>(p, lane, wave), lane};
+  const int items = walk.items();
+  Stream<T, BROWS, swizzle_a32, swizzle_b32, FORM> in(p, walk, lds, lane, T::kProducers ? wave - T::kWaves : wave, item);
   if constexpr (T::kProducers > 0) {
     if (wave >= T::kWaves) {
-      produce<T>(p, in, item, items);
+      produce<T>(in, walk, item, items);
       return;
     }
   } else {
@@ -508,7 +725,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
   const unsigned a_off = (unsigned)(a_row * 128 + 16 * (h ^ swizzle_a32(a_row)));
   const unsigned b_off = (unsigned)(T::kOffB + b_row * 128 + 16 * (h ^ swizzle_b32(b_row)));
 
-  int step = 0, stage = 0, count = item < items ? part_of<T>(p, item).count : 0;
+  int step = 0, stage = 0, count = item < items ? walk.part(item).count : 0;
   bool stored = false;
   v16f acc[kMt][kNt];
   while (item < items) {
@@ -587,52 +804,46 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
     if (++step == count) {
       step = 0;
       stored = true;
-      const TileAt at = tile_at<T>(p, item);
+      const TileAt at = walk.tile(item);
       // a part's sums go to the workspace, which the host has described as C: (splits, L, M, ldc)
-      const int l = at.l + (T::kParts && p.splits > 1 ? item / p.num_tiles * p.L : 0);
+      const int l = at.l + (T::kParts && FORM == kPlain && p.splits > 1 ? item / p.num_tiles * p.L : 0);
       item += G;
-      count = item < items ? part_of<T>(p, item).count : 0;
-      const int rows = min(p.M - at.m0, T::kBM);
-      float* c = static_cast<float*>(p.C) + ((int64_t)l * p.M + at.m0) * p.ldc + at.n0;
+      count = item < items ? walk.part(item).count : 0;
+      const int rows = at.rows, cols = min(p.N - at.n0, T::kBN);
       // finish(v, m, n): quad q of v is columns n .. n + 3 of row m + q
-      auto quads = [&](auto finish) {
+      auto block = [&](int m, int n, auto finish) {
+        // quad q of row r (r % 4 = j) goes to lane j' = q of the four, as its quad of row j: a 4 x 4
+        // transposition in two exchanges, with lane ^ 1 and lane ^ 2
+        float v[4][4];
 #pragma unroll
-        for (int m = 0; m < kMt; ++m)
+        for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = acc[m][n][e];
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            // quad q of row r (r % 4 = j) goes to lane j' = q of the four, as its quad of row j: a 4 x 4
-            // transposition in two exchanges, with lane ^ 1 and lane ^ 2
-            float v[4][4];
+        for (int s = 1; s < 4; s <<= 1) {
+          const bool up = (r & s) != 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = acc[m][n][e];
+          for (int q = 0; q < 4; ++q) {
+            if (q & s) continue;
 #pragma unroll
-            for (int s = 1; s < 4; s <<= 1) {
-              const bool up = (r & s) != 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (q & s) continue;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const float x = v[q][w], y = v[q | s][w];
-                  const int give = __builtin_bit_cast(int, up ? x : y);
-                  const float got = __builtin_bit_cast(float, s == 1 ? __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true)
-                                                                     : __builtin_amdgcn_mov_dpp(give, 0x4E, 0xF, 0xF, true));
-                  v[q][w] = up ? got : x;
-                  v[q | s][w] = up ? y : got;
-                }
-              }
+            for (int w = 0; w < 4; ++w) {
+              const float x = v[q][w], y = v[q | s][w];
+              const int give = __builtin_bit_cast(int, up ? x : y);
+              const float got = __builtin_bit_cast(float, s == 1 ? __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true)
+                                                                 : __builtin_amdgcn_mov_dpp(give, 0x4E, 0xF, 0xF, true));
+              v[q][w] = up ? got : x;
+              v[q | s][w] = up ? y : got;
             }
-            finish(v, (a_row & ~3) + 32 * m, T::kTN * wn + 32 * n + 16 * h + 4 * (r & 3));
           }
+        }
+        finish(v, (a_row & ~3) + 32 * m, T::kTN * wn + 32 * n + 16 * h + 4 * (r & 3));
       };
-      if (p.c_vec) {
-        // N and ldc are multiples of 4 here
-        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 4u * (unsigned)((int64_t)(rows - 1) * p.ldc + min(p.N - at.n0, T::kBN)));
-        quads([&](float(&v)[4][4], int m, int n) {
+      // block (m, n) to c, rows ldc apart.  Whole: N and ldc are multiples of 4.  Else 16-byte accesses at any alignment but
+      // for the last columns of a row (8192 x 8191 x 1024: 396 us element by element).
+      auto whole = [&](int bm, int bn, __amdgpu_buffer_rsrc_t rc, int ldc) {
+        block(bm, bn, [&](float(&v)[4][4], int m, int n) {
           unsigned off[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) off[q] = m + q < rows && at.n0 + n < p.N ? 4u * (unsigned)((m + q) * (int)p.ldc + n) : kOob;
-          if (p.accumulate) {
+          for (int q = 0; q < 4; ++q) off[q] = m + q < rows && at.n0 + n < p.N ? 4u * (unsigned)((m + q) * ldc + n) : kOob;
+          if (!has_ends(FORM) && p.accumulate) {
             v4u old[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) old[q] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off[q], 0, 0);
@@ -647,16 +858,16 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
             __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 2);
           }
         });
-      } else {
-        // 16-byte accesses at any alignment but for the last columns of a row (8192 x 8191 x 1024: 396 us element by
-        // element)
-        quads([&](float(&v)[4][4], int m, int n) {
+      };
+      auto pieces = [&](int bm, int bn, float* c, int64_t ldc) {
+        block(bm, bn, [&](float(&v)[4][4], int m, int n) {
           const int left = p.N - at.n0 - n;
+          const bool add = !has_ends(FORM) && p.accumulate;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float* to = c + (int64_t)(m + q) * p.ldc + n;
+            float* to = c + (int64_t)(m + q) * ldc + n;
             if (m + q < rows && left >= 4) {
-              if (p.accumulate) {
+              if (add) {
                 const v4u old = *reinterpret_cast<const v4u_at4*>(to);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) v[q][w] += __uint_as_float(old[w]);
@@ -666,14 +877,102 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
             } else if (m + q < rows) {
 #pragma unroll
               for (int w = 0; w < 3; ++w)
-                if (w < left) to[w] = (p.accumulate ? to[w] : 0.f) + v[q][w];
+                if (w < left) to[w] = (add ? to[w] : 0.f) + v[q][w];
             }
           }
         });
+      };
+      if constexpr (!has_ends(FORM)) {
+        float* c = static_cast<float*>(p.C) + ((int64_t)l * p.M + at.m0) * p.ldc + at.n0;
+        if (p.c_vec) {
+          const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 4u * (unsigned)((int64_t)(rows - 1) * p.ldc + cols));
+#pragma unroll
+          for (int t = 0; t < kMt * kNt; ++t) whole(t / kNt, t % kNt, rc, (int)p.ldc);
+        } else {
+#pragma unroll
+          for (int t = 0; t < kMt * kNt; ++t) pieces(t / kNt, t % kNt, c, p.ldc);
+        }
+      } else {
+        // one block after the other; its part of the tensors beside C is on the way during its activation
+        const auto* q = late_params<FORM>();
+        const int64_t row0 = (FORM == kRowGroups ? 0 : (int64_t)at.l * q->M) + at.m0;
+        const bool vec = q->c_vec, gated = q->ends.gate != nullptr, residual = FORM == kEnds && q->ends.residual != nullptr;
+        const bool kept = q->ends.Z != nullptr, biased = FORM == kEnds && q->ends.bias != nullptr;
+        const int ldc = (int)q->ldc, ldz = (int)q->ends.ldz, ldg = (int)q->ends.ldg, ldr = (int)q->ends.ldr;
+        float* c = static_cast<float*>(q->C) + row0 * ldc + at.n0;
+        float* z = static_cast<float*>(q->ends.Z) + row0 * ldz + at.n0;
+        const float* gate = static_cast<const float*>(q->ends.gate) + row0 * ldg + at.n0;
+        const float* more = static_cast<const float*>(q->ends.residual) + row0 * ldr + at.n0;
+        const int act = q->ends.act;
+        struct Block {
+          v4u at[4];
+        };
+        auto load = [&](const float* from, int ld, int t) {
+          Block w;
+          const int m = a_row + 32 * (t / kNt), n = T::kTN * wn + 32 * (t % kNt) + 16 * h;
+          if (vec) {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, 4u * (unsigned)((rows - 1) * ld + cols));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const unsigned off = m < rows && n + 4 * i < cols ? 4u * (unsigned)(m * ld + n + 4 * i) : kOob;
+              w.at[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, 0, 0);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const Raw8<0> half = load_chunk<0>(from + (int64_t)m * ld + n + 8 * i, m < rows ? cols - n - 8 * i : 0);
+              w.at[2 * i] = half.w[0];
+              w.at[2 * i + 1] = half.w[1];
+            }
+          }
+          return w;
+        };
+#pragma unroll
+        for (int t = 0; t < kMt * kNt; ++t) {
+          Block gates, mores;
+          if (gated) gates = load(gate, ldg, t);
+          if (residual) mores = load(more, ldr, t);
+          __builtin_amdgcn_sched_barrier(0);
+          v16f& x = acc[t / kNt][t % kNt];
+          if (biased) {
+            const int n = T::kTN * wn + 32 * (t % kNt) + 16 * h;
+            const float* b = static_cast<const float*>(q->ends.bias) + at.n0 + n;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const Raw8<0> half = load_chunk<0>(b + 8 * i, cols - n - 8 * i);
+#pragma unroll
+              for (int w = 0; w < 8; ++w) x[8 * i + w] += __uint_as_float(half.w[w >> 2][w & 3]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          if (kept) {
+            if (vec) whole(t / kNt, t % kNt, make_rsrc(z, 4u * (unsigned)((rows - 1) * ldz + cols)), ldz);
+            else pieces(t / kNt, t % kNt, z, ldz);
+          }
+          ends::with_activation<false>(act, [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              x[i] = f(x[i]);
+              if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+          });
+          if (gated) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] *= __uint_as_float(gates.at[i >> 2][i & 3]);
+          }
+          if (residual) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(mores.at[i >> 2][i & 3]);
+          }
+          if (vec) whole(t / kNt, t % kNt, make_rsrc(c, 4u * (unsigned)((rows - 1) * ldc + cols)), ldc);
+          else pieces(t / kNt, t % kNt, c, ldc);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   }
   if constexpr (T::kProducers == 0) wait_vm<0>();
+  if constexpr (FORM == kRowGroups) zero_rest<0>(p, (int64_t)blockIdx.x * 64 * T::kWaves + threadIdx.x, (int64_t)G * 64 * T::kWaves);
 }
 
 // --- few rows of A -----------------------------------------------------------------
@@ -689,21 +988,33 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 // C the widened codes, as in the tile kernels.
 constexpr int kRowWaves = 8;
 
-template <int FA, int FB, int CT, bool BROWS, int COLS, int MT>
-__global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParams p) {
+// Groups of rows: a workgroup takes up to 16 MT rows of one group.
+template <int FA, int FB, int CT, bool BROWS, int COLS, int MT, Form FORM>
+__global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(params_t<FORM> p) {
   constexpr int W = kRowWaves;
   constexpr int NT = COLS / 16;
   __shared__ float lds[W][16 * MT][16 * NT + 4];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int item = p.first + (int)blockIdx.x, l = item / p.tilesN, n0 = item % p.tilesN * COLS;
+  const int item = p.first + (int)blockIdx.x, n0 = item % p.tilesN * COLS;
+  int l = item / p.tilesN, m0 = 0, rows = p.M;
+  if constexpr (FORM == kRowGroups) {
+    zero_rest<CT>(p, (int64_t)item * 64 * W + threadIdx.x, (int64_t)p.num_tiles * 64 * W);
+    const groups::Unit u = groups::find(p.groups, l, lane, 16 * MT, false);
+    if (u.group < 0) return;
+    l = u.group;
+    m0 = u.start + 16 * MT * u.at;
+    rows = min(u.rows - 16 * MT * u.at, 16 * MT);
+  }
+  // of rows: batches of A, of one where groups share it
+  const int la = FORM == kRowGroups ? 0 : l;
   const uint8_t* a[MT];
   const float* sa[MT];
 #pragma unroll
   for (int s = 0; s < MT; ++s) {
-    const int m = min(16 * s + r, p.M - 1);
-    a[s] = p.A + ((int64_t)l * p.M + m) * p.K + 16 * g;
-    sa[s] = p.SA + (int64_t)l * p.Kb * p.M + m;
+    const int m = m0 + min(16 * s + r, rows - 1);
+    a[s] = p.A + ((int64_t)la * p.M + m) * p.K + 16 * g;
+    sa[s] = p.SA + (int64_t)la * p.Kb * p.M + m;
   }
   const uint8_t* b[NT];
   const float* sb[NT];
@@ -803,35 +1114,41 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(GemmParam
 #pragma unroll
     for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&lds[wave][16 * s + r][16 * t + 4 * g]) = acc[s][t];
   __syncthreads();
-  elem_t<CT>* c = static_cast<elem_t<CT>*>(p.C) + (int64_t)l * p.M * p.ldc + n0;
-  for (int i = threadIdx.x; i < p.M * COLS; i += 64 * W) {
+  const int64_t row0 = (int64_t)la * p.M + m0;
+  elem_t<CT>* c = static_cast<elem_t<CT>*>(p.C) + row0 * p.ldc + n0;
+  for (int i = threadIdx.x; i < rows * COLS; i += 64 * W) {
     const int row = i / COLS, n = i % COLS;
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) sum += lds[w][row][n];
     if (n0 + n < p.N) {
       elem_t<CT>* to = c + (int64_t)row * p.ldc + n;
+      if constexpr (has_ends(FORM)) sum = ends::finish<CT>(p.ends, sum, row0 + row, n0 + n);
       if (CT == 0 && p.accumulate) sum += (float)*to;
       *to = (elem_t<CT>)sum;
     }
   }
 }
 
-// C from the parts' sums, four columns to a thread, parts added in order.
-template <int CT>
-__global__ __launch_bounds__(256) void block128_sum_kernel(GemmParams p, int splits) {
+// C from the parts' sums, four columns to a thread, parts added in order; with no parts, an empty sum's.
+template <int CT, Form FORM>
+__global__ __launch_bounds__(256) void block128_sum_kernel(params_t<FORM> p, int splits) {
   const int quads = p.ldw / 4;
   const int64_t rows = (int64_t)p.L * p.M, all = rows * quads, stride = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
     const int64_t row = i / quads;
     const int n = 4 * (int)(i - row * quads);
     const float* w = p.sums + row * p.ldw + n;
-    v4f sum = *reinterpret_cast<const v4f*>(w);
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    if (FORM == kPlain || splits > 0) sum = *reinterpret_cast<const v4f*>(w);
     for (int s = 1; s < splits; ++s) sum += *reinterpret_cast<const v4f*>(w + s * rows * p.ldw);
     elem_t<CT>* c = static_cast<elem_t<CT>*>(p.C) + row * p.ldc + n;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < p.N) c[e] = (elem_t<CT>)(CT == 0 && p.accumulate ? (float)c[e] + sum[e] : sum[e]);
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= p.N) continue;
+      if constexpr (has_ends(FORM)) sum[e] = ends::finish<CT>(p.ends, sum[e], row, n + e);
+      c[e] = (elem_t<CT>)(CT == 0 && p.accumulate ? (float)c[e] + sum[e] : sum[e]);
+    }
   }
 }
 

@@ -1,0 +1,16 @@
+// Block-128 product, float32 C, larger tiles, with what follows the product or in groups: instantiations.
+#include "block128_launch.hpp"
+
+namespace mxg {
+namespace b128 {
+
+hipError_t launch_more_exact128x256(Form form, const MoreParams& p, int fa, int fb, int, int64_t grid, hipStream_t s) {
+  return launch_more_exact<Exact128x256>(form, p, fa, fb, grid, s);
+}
+
+hipError_t launch_more_exact128(Form form, const MoreParams& p, int fa, int fb, int, int64_t grid, hipStream_t s) {
+  return launch_more_exact<Exact128>(form, p, fa, fb, grid, s);
+}
+
+}  // namespace b128
+}  // namespace mxg

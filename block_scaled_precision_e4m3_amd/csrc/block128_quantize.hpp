@@ -31,7 +31,10 @@
 // take 2.3 us, of which 1.95 are an empty launch.
 #pragma once
 
+#include <type_traits>
+
 #include "dtypes.hpp"
+#include "groups.hpp"
 #include "mx_quantize.hpp"
 
 namespace mxg {
@@ -52,6 +55,10 @@ struct QuantParams {
   int tiles_m;       // row tiles per batch
   int first;         // the launch's first tile
   bool pow2;
+};
+// Rows in groups: Mb and M16 count the blocks that the groups may take, each group's starting with one of its own.
+struct GroupQuantParams : QuantParams {
+  groups::Groups groups;
 };
 
 constexpr unsigned kTinyBits = 0x11E00000u;  // 448 * 2^-100 = 1.75 * 2^-92
@@ -161,30 +168,12 @@ __device__ __forceinline__ unsigned mag_bits(unsigned m) {
   else return half_bits<DT>(max(m & 0xFFFFu, m >> 16));
 }
 
-// 8 elements at p, those at or past `valid` as zero.
-template <int DT>
-__device__ __forceinline__ Raw8<DT> load_chunk(const elem_t<DT>* p, int valid) {
-  if (valid >= 8) return load8<DT>(p);
-  Raw8<DT> r;
-#pragma unroll
-  for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) r.w[i] = (v4u){0, 0, 0, 0};
-  if (valid > 0) {  // the end of a row
-#pragma unroll
-    for (int i = 0; i < 7; ++i) {
-      if constexpr (DT == 0) {
-        r.w[i >> 2][i & 3] = i < valid ? __float_as_uint(p[i]) : 0u;
-      } else {
-        const unsigned h = i < valid ? (unsigned)__builtin_bit_cast(unsigned short, p[i]) : 0u;
-        r.w[0][i >> 1] |= h << (16 * (i & 1));
-      }
-    }
-  }
-  return r;
-}
-
-template <int DT, int FMT, int RT, bool ROWS, bool COLS, bool SQUARE>
-__global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParams p) {
+// GROUPED: tile tm is block tm of the groups' blocks.  The tiles behind the last block take the rows of no group, of
+// which only ROWS has codes, and write zeros for the blocks that no group has filled.
+template <int DT, int FMT, int RT, bool ROWS, bool COLS, bool SQUARE, bool GROUPED = false>
+__global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(std::conditional_t<GROUPED, GroupQuantParams, QuantParams> p) {
   static_assert(RT == 8 || (!COLS && !SQUARE), "columns and squares need the 128 rows of a block");
+  static_assert(!GROUPED || (COLS && !SQUARE), "groups matter to blocks along the rows");
   constexpr int kRows = 16 * RT, kPitch = 132;  // LDS bytes between columns of the transposed codes
   __shared__ __attribute__((aligned(16))) uint8_t tile[COLS ? 128 * kPitch : 16];
   __shared__ unsigned colmax[COLS && !SQUARE ? 4 : 1][COLS && !SQUARE ? 128 : 4];
@@ -195,14 +184,31 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
   const int kb = b % p.Kb;
   b /= p.Kb;
   const int tm = b % p.tiles_m, l = b / p.tiles_m;
-  const int m0 = tm * kRows, k0 = kb * 128, k = k0 + 8 * c;
+  const int k0 = kb * 128, k = k0 + 8 * c;
+  int m0 = tm * kRows, rows = p.M - m0;
+  bool filled = true;  // the columns' block holds a group's rows
+  if constexpr (GROUPED) {
+    const groups::Unit u = groups::find(p.groups, tm, tid & 63, 128, false);
+    filled = u.group >= 0;
+    if (filled) {
+      m0 = u.start + 128 * u.at;
+      rows = min(u.rows - 128 * u.at, 128);
+    } else {
+      // rows before the first group, then those behind the last one
+      const int head = groups::offset(p.groups, 0), tail = groups::offset(p.groups, p.groups.E);
+      const int i = tm - u.total, before = (head + 127) / 128;
+      m0 = i < before ? 128 * i : tail + 128 * (i - before);
+      rows = min((i < before ? head : p.M) - m0, 128);
+      if (rows <= 0) m0 = rows = 0;
+    }
+  }
   const elem_t<DT>* x = static_cast<const elem_t<DT>*>(p.X) + ((int64_t)l * p.M + m0) * p.ldx + k;
 
   Raw8<DT> v[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int m = RT * g + i;
-    v[i] = load_chunk<DT>(x + (int64_t)m * p.ldx, m0 + m < p.M ? p.K - k : 0);
+    v[i] = load_chunk<DT>(x + (int64_t)m * p.ldx, m < rows ? p.K - k : 0);
   }
 
   // largest magnitudes: of the thread's rows, and of its columns
@@ -275,7 +281,7 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
       if (tid < 128) {
         const unsigned t = max(max(colmax[0][tid], colmax[1][tid]), max(colmax[2][tid], colmax[3][tid]));
         const Scale s = block_scale<FMT>(t, p.pow2);
-        if (k0 + tid < p.K) p.ST[((int64_t)l * p.Mb + tm) * p.K + k0 + tid] = s.scale;
+        if (k0 + tid < p.K && (!GROUPED || tm < p.Mb)) p.ST[((int64_t)l * p.Mb + tm) * p.K + k0 + tid] = filled ? s.scale : 0.f;
         colmax[0][tid] = __float_as_uint(s.hi);
         colmax[1][tid] = __float_as_uint(s.lo);
       }
@@ -287,7 +293,7 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
       }
     }
     if constexpr (ROWS) {
-      if (tid < kRows && m0 + tid < p.M) p.S[((int64_t)l * p.Kb + kb) * p.M + m0 + tid] = rowscale[tid];
+      if (tid < kRows && tid < rows) p.S[((int64_t)l * p.Kb + kb) * p.M + m0 + tid] = rowscale[tid];
     }
   }
 
@@ -305,7 +311,7 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int m = RT * g + i;
-      if (m0 + m < p.M && k < p.K16) *reinterpret_cast<uint2*>(q + (int64_t)m * p.K16) = u[i];
+      if (m < rows && k < p.K16) *reinterpret_cast<uint2*>(q + (int64_t)m * p.K16) = u[i];
     }
   }
   if constexpr (COLS) {
@@ -327,14 +333,16 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(QuantParam
         *reinterpret_cast<unsigned*>(tile + (8 * c + j) * kPitch + 8 * g + 4 * h) = w[j];
     }
     __syncthreads();
-    uint8_t* q = p.QT + ((int64_t)l * p.K + k0) * p.M16 + m0;
+    const int at0 = GROUPED ? 128 * tm : m0;  // the block's first column
+    uint8_t* q = p.QT + ((int64_t)l * p.K + k0) * p.M16 + at0;
     const int at = 16 * (tid & 7);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = (tid >> 3) + 32 * i;
       const unsigned* t = reinterpret_cast<const unsigned*>(tile + r * kPitch + at);
-      const v4u u = {t[0], t[1], t[2], t[3]};
-      if (k0 + r < p.K && m0 + at < p.M16) *reinterpret_cast<v4u*>(q + (int64_t)r * p.M16 + at) = u;
+      v4u u = {t[0], t[1], t[2], t[3]};
+      if (GROUPED && !filled) u = (v4u){0, 0, 0, 0};
+      if (k0 + r < p.K && at0 + at < p.M16) *reinterpret_cast<v4u*>(q + (int64_t)r * p.M16 + at) = u;
     }
   }
 }

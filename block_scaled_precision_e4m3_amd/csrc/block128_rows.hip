@@ -10,11 +10,11 @@ template <int FA, int FB, int CT, bool BROWS>
 void launch(const GemmParams& p, int cols, unsigned grid, hipStream_t s) {
   const dim3 g(grid), b(64 * kRowWaves);
   if (p.M <= 16) {
-    if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 1>), g, b, 0, s, p);
-    else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 1>), g, b, 0, s, p);
+    if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 1, kPlain>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 1, kPlain>), g, b, 0, s, p);
   } else {
-    if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 2>), g, b, 0, s, p);
-    else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 2>), g, b, 0, s, p);
+    if (cols == 16) hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 16, 2, kPlain>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((block128_rows_kernel<FA, FB, CT, BROWS, 32, 2, kPlain>), g, b, 0, s, p);
   }
 }
 

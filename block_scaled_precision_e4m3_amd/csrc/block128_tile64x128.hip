@@ -5,7 +5,7 @@ namespace mxg {
 namespace b128 {
 
 hipError_t launch_tile64x128(const GemmParams& p, int fa, int fb, int ct, int64_t grid, hipStream_t s) {
-  return launch_tile<Tile64x128>(p, fa, fb, ct, grid, s);
+  return launch_tile<Tile64x128, kPlain, true>(p, fa, fb, ct, grid, s);
 }
 
 }  // namespace b128

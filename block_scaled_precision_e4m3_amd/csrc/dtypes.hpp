@@ -66,6 +66,36 @@ __device__ __forceinline__ void store8(elem_t<DT>* p, const v8f& f) {
   reinterpret_cast<Raw8At<DT>*>(p)->v = r;
 }
 
+// 8 elements at p, those at or past `valid` as zero.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_chunk(const elem_t<DT>* p, int valid) {
+  if (valid >= 8) return load8<DT>(p);
+  Raw8<DT> r;
+#pragma unroll
+  for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) r.w[i] = (v4u){0, 0, 0, 0};
+  if (valid > 0) {  // the end of a row
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      if constexpr (DT == 0) {
+        r.w[i >> 2][i & 3] = i < valid ? __float_as_uint(p[i]) : 0u;
+      } else {
+        const unsigned h = i < valid ? (unsigned)__builtin_bit_cast(unsigned short, p[i]) : 0u;
+        r.w[0][i >> 1] |= h << (16 * (i & 1));
+      }
+    }
+  }
+  return r;
+}
+
+// The first `valid` (1..8) of 8 elements, rounded as above.
+template <int DT>
+__device__ __forceinline__ void store_chunk(elem_t<DT>* p, const v8f& f, int valid) {
+  if (valid >= 8) return store8<DT>(p, f);
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < valid) p[i] = (elem_t<DT>)f[i];
+}
+
 // The number of bytes of one element on the host.
 inline int elem_bytes(int dt) { return dt == 0 ? 4 : 2; }
 

@@ -547,6 +547,156 @@ int mxgemm_block128(const void* A, const float* SA, const void* B, const float* 
                     size_t workspace_bytes, void* stream);
 size_t mxgemm_block128_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int c_dtype);
 
+/* activations */
+enum {
+  MXG_ACT_NONE = 0,
+  MXG_ACT_RELU = 1,      /* max(z, 0)                                          */
+  MXG_ACT_SILU = 2,      /* z s(z), s(u) = 1 / (1 + e^-u)                      */
+  MXG_ACT_GELU = 3,      /* z P(z), P the normal distribution                  */
+  MXG_ACT_GELU_TANH = 4  /* z s(2 sqrt(2/pi) (z + 0.044715 z^3))               */
+};
+
+/*
+ * What follows a product: with p its value at (m, n),
+ *
+ *   z = p + bias[n],   y = act(z) * gate[m,n] + residual[m,n]
+ *
+ * in float32, y and z rounded once each.  Every tensor may be NULL (not there):
+ *   bias     : (N), of C's type, or float32 with bias_dtype = MXG_DT_F32.
+ *   gate, residual : (M, N) of C's type, rows ldgate / ldresidual >= N elements
+ *              apart.  Either may be C itself with C's row distance.
+ *   preact   : (M, N) of C's type, rows ldpreact >= N apart: receives z, from
+ *              which mxgemm_activation_backward makes the gradients.
+ * No row distance exceeds 2^21.  Other overlaps of outputs with anything are
+ * not allowed.
+ */
+typedef struct {
+  const void* bias;
+  const void* gate;
+  const void* residual;
+  void* preact;
+  int64_t ldgate, ldresidual, ldpreact;
+  int activation, bias_dtype;
+} mxgemm_ends_t;
+
+/*
+ * mxgemm_block128_linear -- C = y of the product of mxgemm_block128 (one batch,
+ * B in blocks of 128 x 128) and what follows it, in one pass where K is not
+ * divided.  Arguments, accuracy of the product and errors as there; ends must
+ * not be NULL; flags: none of mxgemm_block128's.  Workspace:
+ * mxgemm_block128_workspace_bytes(M, N, K, 1, c_dtype).  Errors besides:
+ * MXG_ERR_FMT (activation, bias_dtype), MXG_ERR_SHAPE (a row distance),
+ * MXG_ERR_ALIGN (a tensor not aligned to its elements).  K == 0 takes p = 0.
+ */
+int mxgemm_block128_linear(const void* A, const float* SA, const void* B, const float* SB, void* C, int64_t ldc, int64_t M,
+                           int64_t N, int64_t K, int a_fmt, int b_fmt, int c_dtype, const mxgemm_ends_t* ends, unsigned flags,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mxgemm_activation_backward -- the gradients of y = act(z) gate + residual,
+ * z = p + bias, from that of y: with act' the activation's derivative (relu's 0
+ * at 0),
+ *
+ *   dz = dy * gate * act'(z),  dgate = dy * act(z),  dbias[n] = sum_m dz[m,n]
+ *
+ * in float32, dz and dgate rounded once, dbias from dz before its rounding.
+ * (dp is dz, and the residual's gradient is dy.)
+ *   DY, Z, GATE, DZ, DGATE : (M, N) of `dtype`, rows strides[0..4] >= N elements
+ *            apart.  GATE and DGATE may both be NULL (no gate).  DZ and DGATE may each
+ *            be one of DY, Z, GATE with the same row distance; no other overlap.
+ *   DBIAS : (N) float32, overwritten, or NULL.  Summed in a fixed order: equal
+ *            calls give equal bits.
+ *   workspace : device memory of at least
+ *            mxgemm_activation_backward_workspace_bytes(M, N), 16-byte aligned,
+ *            overwritten; needed for DBIAS only, NULL where that is 0.
+ * Asynchronous, allocates nothing.  Errors (before any work): MXG_ERR_SHAPE
+ * (sizes, a row distance, a short workspace), MXG_ERR_FMT (activation, dtype),
+ * MXG_ERR_FLAGS, MXG_ERR_NULL, MXG_ERR_ALIGN, MXG_ERR_DEVICE, MXG_ERR_LAUNCH.
+ * M == 0 makes DBIAS zero; N == 0 queues nothing.
+ */
+int mxgemm_activation_backward(const void* DY, const void* Z, const void* GATE, void* DZ, void* DGATE, float* DBIAS,
+                               const int64_t* strides, int64_t M, int64_t N, int activation, int dtype, unsigned flags,
+                               void* workspace, size_t workspace_bytes, void* stream);
+size_t mxgemm_activation_backward_workspace_bytes(int64_t M, int64_t N);
+
+/* flags of the entry points on rows in groups */
+enum {
+  MXG_GROUP_OFFSETS64 = 256u,  /* offsets are int64 instead of int32                */
+  MXG_GROUP_ZERO_REST = 512u,  /* mxgemm_block128_grouped: zeros in C's rows of no group */
+  MXG_GROUP_ZERO_PREACT = 1024u /* the same in preact                               */
+};
+
+/*
+ * Rows in groups.  T rows lie in order of the E groups (experts) they belong
+ * to: group e holds rows offsets[e] <= t < offsets[e + 1].  offsets (E + 1), int32 or
+ * int64 (MXG_GROUP_OFFSETS64), is device memory that the kernels read: no size is known to the
+ * host.  A group may have no rows; rows before offsets[0] and behind offsets[E]
+ * belong to none.  Offsets must not decrease and lie within 0 .. T; others give
+ * wrong results, not accesses out of bounds.  E <= 1024, T <= 2^24.
+ *
+ * Along the rows each group has blocks of 128 of its own, the last one filled
+ * up with zeros.  mxgemm_group_blocks(T, E) is the number of blocks that E groups
+ * of T rows in all can have, (T + 127 min(T, E)) / 128 rounded down (0 for E = 0): group
+ * e's blocks follow those of the groups before it, and what is behind the last
+ * group's is zero.
+ */
+int64_t mxgemm_group_blocks(int64_t T, int64_t E);
+
+/*
+ * mxgemm_block128_quantize_grouped -- mxgemm_block128_quantize with blocks along
+ * the rows that start at each group's first row.
+ *   X  : (T, K) of x_dtype, rows ldx apart.
+ *   Q, S : codes (T, K16) and scales (ceil(K/128), T) in blocks of 1 x 128, of all
+ *        rows; both may be NULL (not wanted).
+ *   QT : (K, 128 G) codes of the transpose, G = mxgemm_group_blocks(T, E); ST: (G, K)
+ *        scales.  Codes and scales of blocks that no group has are zero.
+ * flags: MXG_QUANT_POW2, MXG_GROUP_OFFSETS64.  Errors as there, and
+ * MXG_ERR_SHAPE for E or T past their limits, MXG_ERR_NULL without offsets, QT
+ * or ST.  T or K == 0 queues nothing.
+ */
+int mxgemm_block128_quantize_grouped(const void* X, int64_t ldx, const void* offsets, void* Q, float* S, void* QT, float* ST,
+                                     int64_t T, int64_t E, int64_t K, int x_dtype, int fmt, unsigned flags, void* stream);
+
+/*
+ * mxgemm_block128_grouped -- the product of every group's rows with the group's
+ * own B, and what follows it: for rows t of group e
+ *
+ *   p[t,n] = sum_j SA[j,t] SB[e,n/128,j] sum_{k in block j} dec(A[t,k]) dec(B[e,n,k])
+ *
+ *   A  : (T, K) codes, SA: (ceil(K/128), T); B: (E, N, K) codes, SB: (E,
+ *        ceil(N/128), ceil(K/128)); contiguous, K % 16 == 0, K > 0.
+ *   C  : (T, N) of c_dtype, rows ldc >= N apart.  Rows of no group are left as
+ *        they were, or made zero with MXG_GROUP_ZERO_REST (in preact with
+ *        MXG_GROUP_ZERO_PREACT).
+ *   ends : NULL, or activation, gate and preact (bias and residual must be
+ *        NULL: MXG_ERR_FLAGS).
+ * Accuracy as of mxgemm_block128.  Needs no workspace.  flags: MXG_GROUP_*.
+ * Errors as of mxgemm_block128_linear, and MXG_ERR_SHAPE for E or T past their
+ * limits and for K == 0.  T or N == 0 queues nothing.
+ */
+int mxgemm_block128_grouped(const void* A, const float* SA, const void* B, const float* SB, const void* offsets, void* C,
+                            int64_t ldc, int64_t T, int64_t E, int64_t N, int64_t K, int a_fmt, int b_fmt, int c_dtype,
+                            const mxgemm_ends_t* ends, unsigned flags, void* stream);
+
+/*
+ * mxgemm_block128_grouped_weight_gradient -- one product over the rows of each
+ * group, of two operands that mxgemm_block128_quantize_grouped has made along
+ * the rows with the same offsets:
+ *
+ *   C[e,m,n] = sum over e's blocks j of SA[j,m] SB[j,n] sum_{t in block j} dec(A[m,t]) dec(B[n,t])
+ *
+ *   A  : (M, 128 blocks) codes (QT), SA: (blocks, M) (ST); B: (N, 128 blocks), SB:
+ *        (blocks, N); blocks = mxgemm_group_blocks(T, E) < 2^16.
+ *   C  : (E, M, N) float32, rows ldc >= N apart, groups M * ldc apart; zero for
+ *        a group without rows.  MXG_B128_ACCUMULATE: C += product.
+ * Products and sums as in a float32 C of mxgemm_block128.  Needs no workspace.
+ * flags: MXG_GROUP_OFFSETS64, MXG_B128_ACCUMULATE.  Errors as there.  E, M or N
+ * == 0 queues nothing; blocks == 0 makes C zero (leaves it with ACCUMULATE).
+ */
+int mxgemm_block128_grouped_weight_gradient(const void* A, const float* SA, const void* B, const float* SB, const void* offsets,
+                                            float* C, int64_t ldc, int64_t blocks, int64_t E, int64_t M, int64_t N,
+                                            int a_fmt, int b_fmt, unsigned flags, void* stream);
+
 /* layouts of the rotary features inside a head */
 enum {
   MXG_ROPE_HALF = 0,                /* pairs (i, i + rot/2)                          */

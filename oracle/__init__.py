@@ -28,6 +28,8 @@ in float64, where every decoded product is exact.  Modules:
                    the product of two such operands.
 * ``rope_heads`` -- rotary positions and the per-head norm of queries and
                    keys, forward and backward.
+* ``feed_forward`` -- activations with their slopes, and the block-128 quantiser
+                   on rows in groups.
 
 Every function has a pin in ``tests/test_oracle_*.py``; see each module's
 header for which pin covers it.
@@ -40,7 +42,7 @@ from .gemm_amax import (dequantize, gemm_amax, gemm_amax_loops, gemm_rows, gemm_
                         gemm_row_blocks, amax_of)
 from .mx_quantize import mx_quantize, block_max, block_exponent, encode_rne, place_scales, pack_e2m1
 from .proj_rope import rope, proj_rope_mxfp8
-from . import block128, rope_heads
+from . import block128, feed_forward, rope_heads
 
 __all__ = [
     "decode", "decode_e4m3", "decode_e5m2", "decode_e8m0", "decode_e2m1", "unpack_e2m1", "element_codes",
@@ -48,5 +50,5 @@ __all__ = [
     "sf_physical_shape", "sf_logical_shape", "sf_logical_view", "expand_scales",
     "dequantize", "gemm_amax", "gemm_amax_loops", "gemm_rows", "gemm_entries", "gemm_row_blocks", "amax_of",
     "mx_quantize", "block_max", "block_exponent", "encode_rne", "place_scales", "pack_e2m1",
-    "rope", "proj_rope_mxfp8", "block128", "rope_heads",
+    "rope", "proj_rope_mxfp8", "block128", "rope_heads", "feed_forward",
 ]
