@@ -63,6 +63,13 @@ constexpr bool has_groups(Form f) { return f == kRowGroups || f == kDeepGroups; 
 typedef v4u v4u_at2 __attribute__((aligned(2)));
 typedef v4u v4u_at4 __attribute__((aligned(4)));
 
+// Whether rows of a tile start on 128-byte lines, as its stores then fill whole ones.  Only those are non-temporal: parts of
+// lines written past the caches reach memory one by one (50 products 5427 x 356 in float32: 240 us, and 102 through them).
+template <class E>
+__device__ __forceinline__ bool whole_lines(const E* c, int ld) {
+  return (((unsigned)reinterpret_cast<uintptr_t>(c) | (unsigned)ld * (unsigned)sizeof(E)) & 127u) == 0;
+}
+
 constexpr unsigned kOob = 0x80000000u;  // an offset past every resource: reads as zero, is not stored
 
 // A tile of BM x BN outputs by WM x WN waves, operands in a ring of NST stages of KB blocks of K each, moved by the
@@ -83,7 +90,7 @@ struct TileShape {
   static_assert(BM % 64 == 0 && BN % 64 == 0 && BM / 64 + BN / 64 <= kDmaWaves, "one scale DMA per wave");
   static_assert(kTN % 32 == 0 && 128 % kTN == 0, "one 128-column block per wave");
   static constexpr int kLds = NST * kStage + 256;        // and where waves without scales to fetch write zeros
-  static_assert(kLds <= 160 * 1024, "LDS");
+  static_assert(kLds + (int)sizeof(groups::Table) <= 160 * 1024, "LDS");
 };
 
 // As dma16_at, 4 bytes per lane to m0 + 4 * lane.
@@ -405,275 +412,287 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 
   if constexpr (T::kProducers == 0)
     for (int s = 0; s < T::kStages - 1; ++s) in.all(s);
-  int step = 0, stage = 0, count = item < items ? walk.part(item).count : 0;
+  int stage = 0;
   bool stored = false;
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
   v4f acc[kMt][kNt];
-  while (item < items) {
-    if constexpr (T::kProducers == 0) wait_step<T, kStores>(p.c_vec, stored && step < T::kStages - 1);
-    barrier();
-    const uint8_t* st = lds + stage * T::kStage;
-    const uint8_t *a_lo = st + a_off, *a_hi = st + (a_off ^ 64), *b_lo = st + b_off, *b_hi = st + (b_off ^ 64);
-    const float* ssa = reinterpret_cast<const float*>(st + T::kOffSA) + a_row;
-    const float* ssb = reinterpret_cast<const float*>(st + T::kOffSB) + (BROWS ? T::kTN * wn + 8 * g : T::kTN * wn / 128);
-    // row t of MFMAs is row t % kMt of block t / kMt; A's fragments are read two rows ahead of their use
-    auto a_frag = [&](int t) { return frag(a_lo, a_hi, t / kMt * T::kBlock + 2048 * (t % kMt)); };
-    v8i b[T::kKB][kNt], a[3];
-    a[0] = a_frag(0);
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) b[0][nt] = frag(b_lo, b_hi, 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
-    a[1] = a_frag(1);
-    float sa[T::kKB][kMt];
-    v4f sb[T::kKB][BROWS ? kNt : 1];
-#pragma unroll
-    for (int kb = 0; kb < T::kKB; ++kb) {
-      if (kb > 0) {
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) b[kb][nt] = frag(b_lo, b_hi, kb * T::kBlock + 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
-      }
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt) sa[kb][mt] = ssa[kb * (T::kBlock / 4) + 16 * mt];
-      if constexpr (BROWS) {
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt)
-          sb[kb][nt] = *reinterpret_cast<const v4f*>(ssb + kb * (T::kBlock / 4) + 32 * (nt >> 1) + 4 * (nt & 1));
-      } else {
-        sb[kb][0][0] = ssb[kb * (T::kBlock / 4)];
+  // The last tile of a group is seldom full.  The waves of one column strip share a SIMD, so where the lower one has no
+  // rows it leaves the matrix core to the other (16384 rows in 32 groups, 4096 x 7168: 602 us, 638 without).
+  constexpr bool kSkips = FORM == kRowGroups && T::kProducers == 0;
+  for (; item < items; item += G) {
+    const int count = walk.part(item).count;
+    const TileAt at = walk.tile(item);
+    if constexpr (kSkips) {
+      if (at.rows <= T::kTM * wm) {
+        for (int step = 0; step < count; ++step) {
+          wait_step<T, kStores>(p.c_vec, stored && step < T::kStages - 1);
+          barrier();
+          in.all(stage == 0 ? T::kStages - 1 : stage - 1);
+          stage = stage + 1 == T::kStages ? 0 : stage + 1;
+        }
+        stored = false;
+        continue;
       }
     }
-    if (step == 0) {
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] = zero;
+    for (int step = 0; step < count; ++step) {
+      if constexpr (T::kProducers == 0) wait_step<T, kStores>(p.c_vec, stored && step < T::kStages - 1);
+      barrier();
+      const uint8_t* st = lds + stage * T::kStage;
+      const uint8_t *a_lo = st + a_off, *a_hi = st + (a_off ^ 64), *b_lo = st + b_off, *b_hi = st + (b_off ^ 64);
+      const float* ssa = reinterpret_cast<const float*>(st + T::kOffSA) + a_row;
+      const float* ssb = reinterpret_cast<const float*>(st + T::kOffSB) + (BROWS ? T::kTN * wn + 8 * g : T::kTN * wn / 128);
+      // row t of MFMAs is row t % kMt of block t / kMt; A's fragments are read two rows ahead of their use
+      auto a_frag = [&](int t) { return frag(a_lo, a_hi, t / kMt * T::kBlock + 2048 * (t % kMt)); };
+      v8i b[T::kKB][kNt], a[3];
+      a[0] = a_frag(0);
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) b[0][nt] = frag(b_lo, b_hi, 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
+      a[1] = a_frag(1);
+      float sa[T::kKB][kMt];
+      v4f sb[T::kKB][BROWS ? kNt : 1];
+#pragma unroll
+      for (int kb = 0; kb < T::kKB; ++kb) {
+        if (kb > 0) {
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) b[kb][nt] = frag(b_lo, b_hi, kb * T::kBlock + 128 * (32 * (nt >> 1) + 4 * (nt & 1)));
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) sa[kb][mt] = ssa[kb * (T::kBlock / 4) + 16 * mt];
+        if constexpr (BROWS) {
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+            sb[kb][nt] = *reinterpret_cast<const v4f*>(ssb + kb * (T::kBlock / 4) + 32 * (nt >> 1) + 4 * (nt & 1));
+        } else {
+          sb[kb][0][0] = ssb[kb * (T::kBlock / 4)];
+        }
+      }
+      v4f part[kNt];
+      auto fold = [&](int t, int nt) {
+        const int kb = t / kMt, mt = t % kMt;
+        const v4f pt = part[nt];
+        const float s0 = BROWS ? sa[kb][mt] : sa[kb][mt] * sb[kb][0][0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = __builtin_fmaf(pt[e], BROWS ? s0 * sb[kb][nt][e] : s0, acc[mt][nt][e]);
+        // keeps the multiply-adds here: moved past the step's branches, all parts would have to be kept
+        asm volatile("" : "+v"(acc[mt][nt]));
+      };
+      // Each MFMA's result goes into the accumulators right before the MFMA of the next row that overwrites it, one
+      // between two MFMAs: a wave that issues a row's MFMAs and then all its multiply-adds leaves the matrix core idle
+      // under most of them (8192 x 24576 x 1536: 319 -> 295 us, 1024 x 4096 x 7168: 41.3 -> 36.5 us).
+      // The stage the step before used takes the DMA that is furthest ahead, issued between the rows of MFMAs.
+      if constexpr (T::kProducers == 0) in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
+#pragma unroll
+      for (int t = 0; t < kRows; ++t) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          if (t > 0) fold(t - 1, nt);
+          part[nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[t / kMt][nt], a[t % 3], zero, FB, FA, 0, 0, 0, 0);
+          if (T::kProducers > 0 && nt == 0 && t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (T::kProducers == 0) {
+          if (t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
+#pragma unroll
+          for (int q = 0; q < T::kIssued; ++q)
+            if (q / kPerRow == t) in.one(q);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) fold(kRows - 1, nt);
+      if constexpr (T::kProducers == 0) in.end();
+      stage = stage + 1 == T::kStages ? 0 : stage + 1;
+    }
+
+    stored = true;
+    const int rows = at.rows;
+    if (T::kParts && FORM == kPlain && p.splits > 1) {
+      // a part's sums, four columns at a time (ldw is a multiple of 4)
+      float* w = p.sums + (((int64_t)(item / p.num_tiles) * p.L + at.l) * p.M + at.m0) * p.ldw + at.n0;
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] = zero;
-    }
-    v4f part[kNt];
-    auto fold = [&](int t, int nt) {
-      const int kb = t / kMt, mt = t % kMt;
-      const v4f pt = part[nt];
-      const float s0 = BROWS ? sa[kb][mt] : sa[kb][mt] * sb[kb][0][0];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[mt][nt][e] = __builtin_fmaf(pt[e], BROWS ? s0 * sb[kb][nt][e] : s0, acc[mt][nt][e]);
-      // keeps the multiply-adds here: moved past the step's branches, all parts would have to be kept
-      asm volatile("" : "+v"(acc[mt][nt]));
-    };
-    // Each MFMA's result goes into the accumulators right before the MFMA of the next row that overwrites it, one
-    // between two MFMAs: a wave that issues a row's MFMAs and then all its multiply-adds leaves the matrix core idle
-    // under most of them (8192 x 24576 x 1536: 319 -> 295 us, 1024 x 4096 x 7168: 41.3 -> 36.5 us).
-    // The stage the step before used takes the DMA that is furthest ahead, issued between the rows of MFMAs.
-    if constexpr (T::kProducers == 0) in.begin(stage == 0 ? T::kStages - 1 : stage - 1);
-#pragma unroll
-    for (int t = 0; t < kRows; ++t) {
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        if (t > 0) fold(t - 1, nt);
-        part[nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[t / kMt][nt], a[t % 3], zero, FB, FA, 0, 0, 0, 0);
-        if (T::kProducers > 0 && nt == 0 && t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (T::kProducers == 0) {
-        if (t + 2 < kRows) a[(t + 2) % 3] = a_frag(t + 2);
-#pragma unroll
-        for (int q = 0; q < T::kIssued; ++q)
-          if (q / kPerRow == t) in.one(q);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) fold(kRows - 1, nt);
-    if constexpr (T::kProducers == 0) in.end();
-    stage = stage + 1 == T::kStages ? 0 : stage + 1;
-
-    if (++step == count) {
-      step = 0;
-      stored = true;
-      const TileAt at = walk.tile(item);
-      const int rows = at.rows;
-      if (T::kParts && FORM == kPlain && p.splits > 1) {
-        // a part's sums, four columns at a time (ldw is a multiple of 4)
-        float* w = p.sums + (((int64_t)(item / p.num_tiles) * p.L + at.l) * p.M + at.m0) * p.ldw + at.n0;
-#pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            const int m = a_row + 16 * mt, n = T::kTN * wn + 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
-            if (m < rows && at.n0 + n < p.ldw) *reinterpret_cast<v4f*>(w + (int64_t)m * p.ldw + n) = acc[mt][nt];
-          }
-        item += G;
-        count = item < items ? walk.part(item).count : 0;
-        continue;
-      }
-      item += G;
-      count = item < items ? walk.part(item).count : 0;
-      using E = elem_t<CT>;
-      const int cols = min(p.N - at.n0, T::kBN);
-      const bool odd = (r & 1) != 0;
-      // stores 8 columns to a call; non-temporal: C is not read here, and keeping it would push A and B out of the
-      // caches (8192 x 24576 x 1536: 341 -> 318 us)
-      auto put_row = [&](int mt, auto store) {
-        {
-          v4u u[kPairs];
-#pragma unroll
-          for (int h = 0; h < kPairs; ++h) {
-            const v8f v = __builtin_shufflevector(acc[mt][2 * h], acc[mt][2 * h + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-            if constexpr (CT == 1) u[h] = __builtin_bit_cast(v4u, __builtin_convertvector(v, v8bf));
-            else u[h] = __builtin_bit_cast(v4u, __builtin_convertvector(v, v8h));
-          }
-          const int m = a_row + 16 * mt, n = T::kTN * wn + 8 * g;
-          if constexpr (kPairs % 2 == 0) {
-#pragma unroll
-            for (int h = 0; h < kPairs; h += 2) {
-              // even lanes take columns 0..31 of their row and the next, odd lanes 32..63 of theirs and the one before
-              v4u got, mine;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                got[w] = (unsigned)__builtin_amdgcn_mov_dpp((int)(odd ? u[h][w] : u[h + 1][w]), 0xB1, 0xF, 0xF, true);
-                mine[w] = odd ? u[h + 1][w] : u[h][w];
-              }
-              const int nn = n + 32 * h + (odd ? 32 : 0);
-              v4u first, second;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                first[w] = odd ? got[w] : mine[w];
-                second[w] = odd ? mine[w] : got[w];
-              }
-              store(first, m & ~1, nn);
-              store(second, m | 1, nn);
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < kPairs; ++h) store(u[h], m, n + 32 * h);
-          }
+        for (int nt = 0; nt < kNt; ++nt) {
+          const int m = a_row + 16 * mt, n = T::kTN * wn + 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
+          if (m < rows && at.n0 + n < p.ldw) *reinterpret_cast<v4f*>(w + (int64_t)m * p.ldw + n) = acc[mt][nt];
         }
-      };
-      // row mt of MFMAs to c, rows ldc apart.  Whole: N and ldc are multiples of 8, so a lane's 8 columns lie inside or
-      // outside N together.  Else 16-byte stores at any alignment but for the last columns of a row (8192 x 8191 x 1024:
-      // 184 us element by element).
-      auto whole = [&](int mt, __amdgpu_buffer_rsrc_t rc, int ldc) {
-        put_row(mt, [&](const v4u& u, int m, int n) {
-          const unsigned off = m < rows && at.n0 + n < p.N ? 2u * (unsigned)(m * ldc + n) : kOob;
-          __builtin_amdgcn_raw_buffer_store_b128(u, rc, (int)off, 0, 2);
-        });
-      };
-      auto pieces = [&](int mt, E* c, int64_t ldc) {
-        put_row(mt, [&](const v4u& u, int m, int n) {
-          const int left = p.N - at.n0 - n;
-          E* to = c + m * ldc + n;
-          if (m < rows && left >= 8) {
-            __builtin_nontemporal_store(u, reinterpret_cast<v4u_at2*>(to));
-          } else if (m < rows) {
+      continue;
+    }
+    using E = elem_t<CT>;
+    const int cols = min(p.N - at.n0, T::kBN);
+    const bool odd = (r & 1) != 0;
+    // stores 8 columns to a call; non-temporal: C is not read here, and keeping it would push A and B out of the
+    // caches (8192 x 24576 x 1536: 341 -> 318 us)
+    auto put_row = [&](int mt, auto store) {
+      v4u u[kPairs];
 #pragma unroll
-            for (int e = 0; e < 7; ++e)
-              if (e < left) to[e] = __builtin_bit_cast(E, (unsigned short)(u[e >> 1] >> (16 * (e & 1))));
+      for (int h = 0; h < kPairs; ++h) {
+        const v8f v = __builtin_shufflevector(acc[mt][2 * h], acc[mt][2 * h + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+        if constexpr (CT == 1) u[h] = __builtin_bit_cast(v4u, __builtin_convertvector(v, v8bf));
+        else u[h] = __builtin_bit_cast(v4u, __builtin_convertvector(v, v8h));
+      }
+      const int m = a_row + 16 * mt, n = T::kTN * wn + 8 * g;
+      if constexpr (kPairs % 2 == 0) {
+#pragma unroll
+        for (int h = 0; h < kPairs; h += 2) {
+          // even lanes take columns 0..31 of their row and the next, odd lanes 32..63 of theirs and the one before
+          v4u got, mine;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            got[w] = (unsigned)__builtin_amdgcn_mov_dpp((int)(odd ? u[h][w] : u[h + 1][w]), 0xB1, 0xF, 0xF, true);
+            mine[w] = odd ? u[h + 1][w] : u[h][w];
           }
-        });
-      };
-      if constexpr (!has_ends(FORM)) {
-        E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
-        if (p.c_vec) {
-          int ldc = (int)p.ldc;
-          // with 16 scales more to a lane, the stores' offsets are made here, not kept in registers through the K loop
-          if constexpr (BROWS) asm volatile("" : "+s"(ldc));
-          const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * ldc + cols));
+          const int nn = n + 32 * h + (odd ? 32 : 0);
+          v4u first, second;
 #pragma unroll
-          for (int mt = 0; mt < kMt; ++mt) whole(mt, rc, ldc);
-        } else {
-          int64_t ldc = p.ldc;
-          asm volatile("" : "+s"(ldc));  // as above
-#pragma unroll
-          for (int mt = 0; mt < kMt; ++mt) pieces(mt, c, ldc);
+          for (int w = 0; w < 4; ++w) {
+            first[w] = odd ? got[w] : mine[w];
+            second[w] = odd ? mine[w] : got[w];
+          }
+          store(first, m & ~1, nn);
+          store(second, m | 1, nn);
         }
       } else {
-        // One row of MFMAs after the other, and the tensors beside C asked for one row ahead: all at once would not fit
-        // the registers, which hold the sums of all rows.
-        const auto* q = late_params<FORM>();
-        const int64_t row0 = (FORM == kRowGroups ? 0 : (int64_t)at.l * q->M) + at.m0;
-        const bool vec = q->c_vec, gated = q->ends.gate != nullptr, residual = FORM == kEnds && q->ends.residual != nullptr;
-        const bool kept = q->ends.Z != nullptr;
-        const int ldc = (int)q->ldc, ldz = (int)q->ends.ldz, ldg = (int)q->ends.ldg, ldr = (int)q->ends.ldr;
-        E* c = static_cast<E*>(q->C) + row0 * ldc + at.n0;
-        E* z = static_cast<E*>(q->ends.Z) + row0 * ldz + at.n0;
-        const E* gate = static_cast<const E*>(q->ends.gate) + row0 * ldg + at.n0;
-        const E* more = static_cast<const E*>(q->ends.residual) + row0 * ldr + at.n0;
-        const int n_lane = T::kTN * wn + 8 * g;
-        struct Row {
-          Raw8<CT> at[kPairs];
-        };
-        auto load = [&](const E* from, int ld, int mt) {
-          Row w;
-          const int m = a_row + 16 * mt;
-          if (vec) {
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, 2u * (unsigned)((rows - 1) * ld + cols));
 #pragma unroll
-            for (int h = 0; h < kPairs; ++h) {
-              const unsigned off = m < rows && n_lane + 32 * h < cols ? 2u * (unsigned)(m * ld + n_lane + 32 * h) : kOob;
-              w.at[h].w[0] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, 0, 0);
-            }
-          } else {
+        for (int h = 0; h < kPairs; ++h) store(u[h], m, n + 32 * h);
+      }
+    };
+    // row mt of MFMAs to c, rows ldc apart.  Whole: N and ldc are multiples of 8, so a lane's 8 columns lie inside or
+    // outside N together.  Else 16-byte stores at any alignment but for the last columns of a row (8192 x 8191 x 1024:
+    // 184 us element by element).
+    auto whole = [&](int mt, __amdgpu_buffer_rsrc_t rc, int ldc, bool lines) {
+      put_row(mt, [&](const v4u& u, int m, int n) {
+        const unsigned off = m < rows && at.n0 + n < p.N ? 2u * (unsigned)(m * ldc + n) : kOob;
+        if (lines) __builtin_amdgcn_raw_buffer_store_b128(u, rc, (int)off, 0, 2);
+        else __builtin_amdgcn_raw_buffer_store_b128(u, rc, (int)off, 0, 0);
+      });
+    };
+    auto pieces = [&](int mt, E* c, int64_t ldc) {
+      put_row(mt, [&](const v4u& u, int m, int n) {
+        const int left = p.N - at.n0 - n;
+        E* to = c + m * ldc + n;
+        if (m < rows && left >= 8) {
+          *reinterpret_cast<v4u_at2*>(to) = u;
+        } else if (m < rows) {
 #pragma unroll
-            for (int h = 0; h < kPairs; ++h)
-              w.at[h] = load_chunk<CT>(from + (int64_t)m * ld + n_lane + 32 * h, m < rows ? cols - n_lane - 32 * h : 0);
+          for (int e = 0; e < 7; ++e)
+            if (e < left) to[e] = __builtin_bit_cast(E, (unsigned short)(u[e >> 1] >> (16 * (e & 1))));
+        }
+      });
+    };
+    if constexpr (!has_ends(FORM)) {
+      E* c = static_cast<E*>(p.C) + ((int64_t)at.l * p.M + at.m0) * p.ldc + at.n0;
+      if (p.c_vec) {
+        int ldc = (int)p.ldc;
+        // with 16 scales more to a lane, the stores' offsets are made here, not kept in registers through the K loop
+        if constexpr (BROWS) asm volatile("" : "+s"(ldc));
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((int64_t)(rows - 1) * ldc + cols));
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) whole(mt, rc, ldc, whole_lines(c, ldc));
+      } else {
+        int64_t ldc = p.ldc;
+        asm volatile("" : "+s"(ldc));  // as above
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) pieces(mt, c, ldc);
+      }
+    } else {
+      // One row of MFMAs after the other, and the tensors beside C asked for one row ahead: all at once would not fit
+      // the registers, which hold the sums of all rows.
+      const auto* q = late_params<FORM>();
+      const int64_t row0 = (FORM == kRowGroups ? 0 : (int64_t)at.l * q->M) + at.m0;
+      const bool vec = q->c_vec, gated = q->ends.gate != nullptr, residual = FORM == kEnds && q->ends.residual != nullptr;
+      const bool kept = q->ends.Z != nullptr;
+      const int ldc = (int)q->ldc, ldz = (int)q->ends.ldz, ldg = (int)q->ends.ldg, ldr = (int)q->ends.ldr;
+      E* c = static_cast<E*>(q->C) + row0 * ldc + at.n0;
+      E* z = static_cast<E*>(q->ends.Z) + row0 * ldz + at.n0;
+      const E* gate = static_cast<const E*>(q->ends.gate) + row0 * ldg + at.n0;
+      const E* more = static_cast<const E*>(q->ends.residual) + row0 * ldr + at.n0;
+      const int n_lane = T::kTN * wn + 8 * g;
+      struct Row {
+        Raw8<CT> at[kPairs];
+      };
+      auto load = [&](const E* from, int ld, int mt) {
+        Row w;
+        const int m = a_row + 16 * mt;
+        if (vec) {
+          const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, 2u * (unsigned)((rows - 1) * ld + cols));
+#pragma unroll
+          for (int h = 0; h < kPairs; ++h) {
+            const unsigned off = m < rows && n_lane + 32 * h < cols ? 2u * (unsigned)(m * ld + n_lane + 32 * h) : kOob;
+            w.at[h].w[0] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, 0, 0);
           }
-          return w;
-        };
-        v4f bias[kNt];
-        if (q->ends.bias) {
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = n_lane + 32 * (nt >> 1) + 4 * (nt & 1) + i;
-              bias[nt][i] = n < cols ? ends::bias_at<CT>(q->ends.bias, q->ends.bias_f32, at.n0 + n) : 0.f;
-            }
         } else {
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) bias[nt] = zero;
+          for (int h = 0; h < kPairs; ++h)
+            w.at[h] = load_chunk<CT>(from + (int64_t)m * ld + n_lane + 32 * h, m < rows ? cols - n_lane - 32 * h : 0);
         }
-        const int act = q->ends.act;
-        Row gates[2], mores[2];
-        if (gated) gates[0] = load(gate, ldg, 0);
-        if (residual) mores[0] = load(more, ldr, 0);
+        return w;
+      };
+      v4f bias[kNt];
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
-          if (mt + 1 < kMt) {
-            if (gated) gates[(mt + 1) & 1] = load(gate, ldg, mt + 1);
-            if (residual) mores[(mt + 1) & 1] = load(more, ldr, mt + 1);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (FORM == kEnds) {
+      for (int nt = 0; nt < kNt; ++nt) bias[nt] = zero;
+      if (FORM == kEnds && q->ends.bias) {
+        const bool f32 = q->ends.bias_f32;
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] += bias[nt];
-          }
-          if (kept) {
-            if (vec) whole(mt, make_rsrc(z, 2u * (unsigned)((rows - 1) * ldz + cols)), ldz);
-            else pieces(mt, z, ldz);
-          }
-          ends::with_activation<true>(act, [&](auto f) {
+        for (int h = 0; h < kPairs; ++h) {
+          const int n = n_lane + 32 * h;
+          const v8f v = f32 ? widen8<0>(load_chunk<0>(static_cast<const float*>(q->ends.bias) + at.n0 + n, cols - n))
+                            : widen8<CT>(load_chunk<CT>(static_cast<const E*>(q->ends.bias) + at.n0 + n, cols - n));
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[mt][nt][i] = f(acc[mt][nt][i]);
-          });
-          if (gated) {
-#pragma unroll
-            for (int h = 0; h < kPairs; ++h) {
-              const v8f v = widen8<CT>(gates[mt & 1].at[h]);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) acc[mt][2 * h + (i >> 2)][i & 3] *= v[i];
-            }
-          }
-          if (residual) {
-#pragma unroll
-            for (int h = 0; h < kPairs; ++h) {
-              const v8f v = widen8<CT>(mores[mt & 1].at[h]);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) acc[mt][2 * h + (i >> 2)][i & 3] += v[i];
-            }
-          }
-          if (vec) whole(mt, make_rsrc(c, 2u * (unsigned)((rows - 1) * ldc + cols)), ldc);
-          else pieces(mt, c, ldc);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < 8; ++i) bias[2 * h + (i >> 2)][i & 3] = v[i];
         }
+      }
+      const int act = q->ends.act;
+      const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 2u * (unsigned)((rows - 1) * ldc + cols));
+      const bool lines = whole_lines(c, ldc);
+      Row gates[2], mores[2];
+      if (gated) gates[0] = load(gate, ldg, 0);
+      if (residual) mores[0] = load(more, ldr, 0);
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) {
+        if (mt + 1 < kMt) {
+          if (gated) gates[(mt + 1) & 1] = load(gate, ldg, mt + 1);
+          if (residual) mores[(mt + 1) & 1] = load(more, ldr, mt + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (FORM == kEnds) {
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) acc[mt][nt] += bias[nt];
+        }
+        if (kept) {
+          if (vec) whole(mt, make_rsrc(z, 2u * (unsigned)((rows - 1) * ldz + cols)), ldz, whole_lines(z, ldz));
+          else pieces(mt, z, ldz);
+        }
+        ends::with_activation<true>(act, [&](auto f) {
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[mt][nt][i] = f(acc[mt][nt][i]);
+            if (nt & 1) __builtin_amdgcn_sched_barrier(0);  // eight at a time: more do not fit the registers
+          }
+        });
+        if (gated) {
+#pragma unroll
+          for (int h = 0; h < kPairs; ++h) {
+            const v8f v = widen8<CT>(gates[mt & 1].at[h]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[mt][2 * h + (i >> 2)][i & 3] *= v[i];
+          }
+        }
+        if (residual) {
+#pragma unroll
+          for (int h = 0; h < kPairs; ++h) {
+            const v8f v = widen8<CT>(mores[mt & 1].at[h]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[mt][2 * h + (i >> 2)][i & 3] += v[i];
+          }
+        }
+        if (vec) whole(mt, rc, ldc, lines);
+        else pieces(mt, c, ldc);
       }
     }
   }
@@ -838,7 +857,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
       };
       // block (m, n) to c, rows ldc apart.  Whole: N and ldc are multiples of 4.  Else 16-byte accesses at any alignment but
       // for the last columns of a row (8192 x 8191 x 1024: 396 us element by element).
-      auto whole = [&](int bm, int bn, __amdgpu_buffer_rsrc_t rc, int ldc) {
+      auto whole = [&](int bm, int bn, __amdgpu_buffer_rsrc_t rc, int ldc, bool lines) {
         block(bm, bn, [&](float(&v)[4][4], int m, int n) {
           unsigned off[4];
 #pragma unroll
@@ -855,7 +874,8 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const v4u out = {__float_as_uint(v[q][0]), __float_as_uint(v[q][1]), __float_as_uint(v[q][2]), __float_as_uint(v[q][3])};
-            __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 2);
+            if (lines) __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 2);
+            else __builtin_amdgcn_raw_buffer_store_b128(out, rc, (int)off[q], 0, 0);
           }
         });
       };
@@ -873,7 +893,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
                 for (int w = 0; w < 4; ++w) v[q][w] += __uint_as_float(old[w]);
               }
               const v4u out = {__float_as_uint(v[q][0]), __float_as_uint(v[q][1]), __float_as_uint(v[q][2]), __float_as_uint(v[q][3])};
-              __builtin_nontemporal_store(out, reinterpret_cast<v4u_at4*>(to));
+              *reinterpret_cast<v4u_at4*>(to) = out;
             } else if (m + q < rows) {
 #pragma unroll
               for (int w = 0; w < 3; ++w)
@@ -887,7 +907,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
         if (p.c_vec) {
           const __amdgpu_buffer_rsrc_t rc = make_rsrc(c, 4u * (unsigned)((int64_t)(rows - 1) * p.ldc + cols));
 #pragma unroll
-          for (int t = 0; t < kMt * kNt; ++t) whole(t / kNt, t % kNt, rc, (int)p.ldc);
+          for (int t = 0; t < kMt * kNt; ++t) whole(t / kNt, t % kNt, rc, (int)p.ldc, whole_lines(c, (int)p.ldc));
         } else {
 #pragma unroll
           for (int t = 0; t < kMt * kNt; ++t) pieces(t / kNt, t % kNt, c, p.ldc);
@@ -946,7 +966,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
             }
           }
           if (kept) {
-            if (vec) whole(t / kNt, t % kNt, make_rsrc(z, 4u * (unsigned)((rows - 1) * ldz + cols)), ldz);
+            if (vec) whole(t / kNt, t % kNt, make_rsrc(z, 4u * (unsigned)((rows - 1) * ldz + cols)), ldz, whole_lines(z, ldz));
             else pieces(t / kNt, t % kNt, z, ldz);
           }
           ends::with_activation<false>(act, [&](auto f) {
@@ -964,7 +984,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(mores.at[i >> 2][i & 3]);
           }
-          if (vec) whole(t / kNt, t % kNt, make_rsrc(c, 4u * (unsigned)((rows - 1) * ldc + cols)), ldc);
+          if (vec) whole(t / kNt, t % kNt, make_rsrc(c, 4u * (unsigned)((rows - 1) * ldc + cols)), ldc, whole_lines(c, ldc));
           else pieces(t / kNt, t % kNt, c, ldc);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -1000,7 +1020,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void block128_rows_kernel(params_t<
   int l = item / p.tilesN, m0 = 0, rows = p.M;
   if constexpr (FORM == kRowGroups) {
     zero_rest<CT>(p, (int64_t)item * 64 * W + threadIdx.x, (int64_t)p.num_tiles * 64 * W);
-    const groups::Unit u = groups::find(p.groups, l, lane, 16 * MT, false);
+    const groups::Unit u = groups::find(p.groups, l, lane, 16 * MT);
     if (u.group < 0) return;
     l = u.group;
     m0 = u.start + 16 * MT * u.at;

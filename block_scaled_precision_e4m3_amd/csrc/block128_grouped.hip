@@ -176,12 +176,12 @@ int mxgemm_block128_grouped(const void* A, const float* SA, const void* B, const
   const int64_t some = std::min(T, E);  // groups that can have rows
   if (ch.rows) {
     p.tilesN = (int)cdiv(N, ch.rows);
-    const int64_t chunks = (T + 15 * some) / 16;
+    const int64_t chunks = (T + (ch.bm - 1) * some) / ch.bm;
     p.num_tiles = (int)(chunks * p.tilesN);
     hipError_t e = hipSuccess;
     launch_runs(p.num_tiles, [&](int64_t first, unsigned count) {
       p.first = (int)first;
-      if (e == hipSuccess) e = launch_rows_more(kRowGroups, p, a_fmt, b_fmt, c_dtype, 16, ch.rows, count, s);
+      if (e == hipSuccess) e = launch_rows_more(kRowGroups, p, a_fmt, b_fmt, c_dtype, ch.bm, ch.rows, count, s);
     });
     return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
   }

@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(std::condi
   int m0 = tm * kRows, rows = p.M - m0;
   bool filled = true;  // the columns' block holds a group's rows
   if constexpr (GROUPED) {
-    const groups::Unit u = groups::find(p.groups, tm, tid & 63, 128, false);
+    const groups::Unit u = groups::find(p.groups, tm, tid & 63, 128);
     filled = u.group >= 0;
     if (filled) {
       m0 = u.start + 128 * u.at;

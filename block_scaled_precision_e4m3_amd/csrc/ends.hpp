@@ -68,27 +68,29 @@ __device__ __forceinline__ float tanh_sigmoid(float z) {
   }
 }
 
-// P(z), and e^(-z^2/2) beside it.
-struct Normal {
+// P's lower tail at -|z|, and e^(-z^2/2).
+struct Tail {
   float p, e;
 };
 template <bool FAST>
-__device__ __forceinline__ Normal normal(float z) {
-  // -z^2/2 with what its rounding loses
-  const float s = -0.5f * z, q = s * z;
-  float e = exponential<FAST>(q), t, r;
+__device__ __forceinline__ Tail tail(float z) {
   if constexpr (FAST) {
-    t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.31f, 1.f));
-    r = -0.0739273363f;
+    const float w = 0.8493218003f * z;  // w^2 is z^2/2 in powers of 2
+    const float e = __builtin_amdgcn_exp2f(-(w * w));
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(w), 0.31f / 0.8493218003f, 1.f));
+    float r = -0.0739273363f;
     r = __builtin_fmaf(r, t, 0.180445171f);
     r = __builtin_fmaf(r, t, 0.0157504037f);
     r = __builtin_fmaf(r, t, 0.133426788f);
     r = __builtin_fmaf(r, t, 0.120442029f);
     r = __builtin_fmaf(r, t, 0.12386063f);
+    return {r * t * e, e};
   } else {
-    if (q > -150.f) e = __builtin_fmaf(e, __builtin_fmaf(s, z, -q), e);
-    t = 1.f / __builtin_fmaf(fabsf(z), 0.3f, 1.f);
-    r = 0.0356745869f;
+    const float s = -0.5f * z, q = s * z;
+    float e = exponential<false>(q);
+    if (q > -150.f) e = __builtin_fmaf(e, __builtin_fmaf(s, z, -q), e);  // what q's rounding loses
+    const float t = 1.f / __builtin_fmaf(fabsf(z), 0.3f, 1.f);
+    float r = 0.0356745869f;
     r = __builtin_fmaf(r, t, -0.157202214f);
     r = __builtin_fmaf(r, t, 0.206351876f);
     r = __builtin_fmaf(r, t, -0.0536820367f);
@@ -96,9 +98,12 @@ __device__ __forceinline__ Normal normal(float z) {
     r = __builtin_fmaf(r, t, 0.0999137834f);
     r = __builtin_fmaf(r, t, 0.120753907f);
     r = __builtin_fmaf(r, t, 0.119629301f);
+    return {r * t * e, e};
   }
-  const float tail = r * t * e;
-  return {z > 0.f ? 1.f - tail : tail, e};
+}
+// z P(z) = max(z, 0) - |z| P(-|z|), |z| held finite, as the tail of an infinity is zero.  A NaN is one in the tail.
+__device__ __forceinline__ float gelu_of(float z, const Tail& t) {
+  return __builtin_fmaf(-fminf(fabsf(z), 3e38f), t.p, fmaxf(z, 0.f));
 }
 
 // f(g) with g(z) the activation of that kind: the choice stands outside of what loops over values.
@@ -106,7 +111,7 @@ template <bool FAST, class F>
 __device__ __forceinline__ void with_activation(int act, F f) {
   if (act == MXG_ACT_RELU) f([](float z) { return z < 0.f ? 0.f : z; });
   else if (act == MXG_ACT_SILU) f([](float z) { return z * sigmoid<FAST>(z); });
-  else if (act == MXG_ACT_GELU) f([](float z) { return z * normal<FAST>(z).p; });
+  else if (act == MXG_ACT_GELU) f([](float z) { return gelu_of(z, tail<FAST>(z)); });
   else if (act == MXG_ACT_GELU_TANH) f([](float z) { return z * tanh_sigmoid<FAST>(z); });
 }
 
@@ -125,8 +130,8 @@ __device__ __forceinline__ void with_slope(int act, F f) {
     });
   } else if (act == MXG_ACT_GELU) {
     f([](float z) {
-      const Normal n = normal<FAST>(z);
-      return Slope{z * n.p, __builtin_fmaf(0.3989422804f * z, n.e, n.p)};
+      const Tail t = tail<FAST>(z);
+      return Slope{gelu_of(z, t), __builtin_fmaf(0.3989422804f * z, t.e, z > 0.f ? 1.f - t.p : t.p)};
     });
   } else if (act == MXG_ACT_GELU_TANH) {
     f([](float z) {

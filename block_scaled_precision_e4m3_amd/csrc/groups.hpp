@@ -44,41 +44,56 @@ __device__ __forceinline__ int wave_sum(int v) {
   return v;
 }
 
+// Offsets i + 64 j + lane, j <= 4: asked for together, since one waits for memory as long as all of them.
+struct Ahead {
+  int at[5];
+  __device__ __forceinline__ Ahead(const Groups& g, int i, int lane) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) at[j] = offset(g, i + 64 * j + lane);
+  }
+};
+
 // Groups i .. i + 63, one to a lane: its first row, its units of `per` rows, and the units up to its end where `before`
-// lie in the groups before i.
+// lie in the groups before i.  Its offset is `start` in the lane; `next` starts with the offset behind the last lane's.
 struct Span {
   int start, rows, units, end;
 };
-__device__ __forceinline__ Span span(const Groups& g, int i, int lane, int per, int before) {
+__device__ __forceinline__ Span span(const Groups& g, int i, int lane, int per, int before, int start, int next) {
   Span s;
-  s.start = offset(g, i + lane);
-  const int next = offset(g, i + lane + 1);
-  s.rows = i + lane < g.E ? max(next - s.start, 0) : 0;
+  s.start = start;
+  const int behind = __builtin_amdgcn_readfirstlane(next);
+  const int stop = __builtin_amdgcn_update_dpp(behind, start, 0x130, 0xF, 0xF, false);  // lane + 1's
+  s.rows = i + lane < g.E ? max(stop - start, 0) : 0;
   s.units = (s.rows + per - 1) / per;
   s.end = before + wave_sum(s.units);
   return s;
 }
 
 // The unit `want` of all groups' units: its group, the group's rows, the first of them, and which of the group's units it
-// is.  group < 0: there are no more than `total`, which is known then (and with `all`).  Every lane of the wave takes part
-// and gets the answer.
+// is.  group < 0: there are no more than `total`, which is known then.  Every lane of the wave takes part and gets the
+// answer.
 struct Unit {
   int group, start, rows, at, total;
 };
-__device__ __forceinline__ Unit find(const Groups& g, int want, int lane, int per, bool all) {
+__device__ __forceinline__ Unit find(const Groups& g, int want, int lane, int per) {
   Unit u = {-1, 0, 0, 0, 0};
-  for (int i = 0; i < g.E; i += 64) {
-    const Span s = span(g, i, lane, per, u.total);
-    const uint64_t past = __ballot(s.end > want);
-    if (past && u.group < 0) {
-      const int from = __builtin_ctzll(past);
-      u.group = i + from;
-      u.start = __builtin_amdgcn_readlane(s.start, from);
-      u.rows = __builtin_amdgcn_readlane(s.rows, from);
-      u.at = want - (__builtin_amdgcn_readlane(s.end, from) - __builtin_amdgcn_readlane(s.units, from));
-      if (!all) return u;
+  for (int i = 0; i < g.E; i += 256) {
+    const Ahead a(g, i, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i + 64 * j >= g.E) break;
+      const Span s = span(g, i + 64 * j, lane, per, u.total, a.at[j], a.at[j + 1]);
+      const uint64_t past = __ballot(s.end > want);
+      if (past) {
+        const int from = __builtin_ctzll(past);
+        u.group = i + 64 * j + from;
+        u.start = __builtin_amdgcn_readlane(s.start, from);
+        u.rows = __builtin_amdgcn_readlane(s.rows, from);
+        u.at = want - (__builtin_amdgcn_readlane(s.end, from) - __builtin_amdgcn_readlane(s.units, from));
+        return u;
+      }
+      u.total = __builtin_amdgcn_readlane(s.end, 63);
     }
-    u.total = __builtin_amdgcn_readlane(s.end, 63);
   }
   return u;
 }
@@ -90,13 +105,19 @@ struct Table {
 // Filled by one wave.  No count exceeds `most`, what the groups can have at most.
 __device__ __forceinline__ void fill(Table* t, const Groups& g, int lane, int per, int most) {
   int before = 0;
-  for (int i = 0; i < g.E; i += 64) {
-    const Span s = span(g, i, lane, per, before);
-    if (i + lane < g.E) {
-      t->start[i + lane] = s.start;
-      t->units[i + lane + 1] = min(s.end, most);
+  for (int i = 0; i < g.E; i += 256) {
+    const Ahead a(g, i, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int first = i + 64 * j;
+      if (first >= g.E) break;
+      const Span s = span(g, first, lane, per, before, a.at[j], a.at[j + 1]);
+      if (first + lane < g.E) {
+        t->start[first + lane] = s.start;
+        t->units[first + lane + 1] = min(s.end, most);
+      }
+      before = __builtin_amdgcn_readlane(s.end, 63);
     }
-    before = __builtin_amdgcn_readlane(s.end, 63);
   }
   if (lane == 0) {
     t->start[g.E] = offset(g, g.E);
