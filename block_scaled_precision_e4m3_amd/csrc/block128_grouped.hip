@@ -73,7 +73,7 @@ int mxgemm_block128_quantize_grouped(const void* X, int64_t ldx, const void* off
   const int64_t tiles = Q ? (T + 127 * (std::min(T, E) + 2)) / 128 : blocks;
   if (K && tiles > 0x7FFFFFFFLL / cdiv(K, 128)) return MXG_ERR_SHAPE;
   if (T == 0 || K == 0) return MXG_OK;
-  if (!X || !offsets || !QT || !ST || (Q != nullptr) != (S != nullptr)) return MXG_ERR_NULL;
+  if (!X || !offsets || (blocks > 0 && (!QT || !ST)) || (Q != nullptr) != (S != nullptr)) return MXG_ERR_NULL;
   if (!aligned_to(X, mxg::elem_bytes(x_dtype)) || !aligned16(Q) || !aligned16(QT) || !aligned_to(S, 4) || !aligned_to(ST, 4) ||
       !offsets_aligned(offsets, flags))
     return MXG_ERR_ALIGN;

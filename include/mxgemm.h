@@ -651,8 +651,8 @@ int64_t mxgemm_group_blocks(int64_t T, int64_t E);
  *   QT : (K, 128 G) codes of the transpose, G = mxgemm_group_blocks(T, E); ST: (G, K)
  *        scales.  Codes and scales of blocks that no group has are zero.
  * flags: MXG_QUANT_POW2, MXG_GROUP_OFFSETS64.  Errors as there, and
- * MXG_ERR_SHAPE for E or T past their limits, MXG_ERR_NULL without offsets, QT
- * or ST.  T or K == 0 queues nothing.
+ * MXG_ERR_SHAPE for E or T past their limits, MXG_ERR_NULL without offsets, or QT
+ * or ST where G > 0.  T or K == 0 queues nothing.
  */
 int mxgemm_block128_quantize_grouped(const void* X, int64_t ldx, const void* offsets, void* Q, float* S, void* QT, float* ST,
                                      int64_t T, int64_t E, int64_t K, int x_dtype, int fmt, unsigned flags, void* stream);
