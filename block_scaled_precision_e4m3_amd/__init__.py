@@ -79,7 +79,8 @@ EXPORTED = ("mxgemm_amax", "mxgemm_amax_ex", "mxgemm_amax_reset", "mxgemm_check_
             "mxgemm_block128_workspace_bytes", "mxgemm_rope", "mxgemm_qk_norm_rope", "mxgemm_qk_norm_rope_backward",
             "mxgemm_qk_norm_rope_backward_workspace_bytes", "mxgemm_block128_linear", "mxgemm_activation_backward",
             "mxgemm_activation_backward_workspace_bytes", "mxgemm_group_blocks", "mxgemm_block128_quantize_grouped",
-            "mxgemm_block128_grouped", "mxgemm_block128_grouped_weight_gradient")
+            "mxgemm_block128_grouped", "mxgemm_block128_grouped_weight_gradient",
+            "mxgemm_block128_grouped_weight_gradient_workspace_bytes")
 
 
 class MxgemmError(Exception):
@@ -174,8 +175,10 @@ def _load():
     lib.mxgemm_block128_quantize_grouped.restype = ci
     lib.mxgemm_block128_grouped.argtypes = [vp] * 6 + [i64] * 5 + [ci, ci, ci, ends, cu, vp]
     lib.mxgemm_block128_grouped.restype = ci
-    lib.mxgemm_block128_grouped_weight_gradient.argtypes = [vp] * 6 + [i64] * 5 + [ci, ci, cu, vp]
+    lib.mxgemm_block128_grouped_weight_gradient.argtypes = [vp] * 6 + [i64] * 5 + [ci, ci, cu, vp, cz, vp]
     lib.mxgemm_block128_grouped_weight_gradient.restype = ci
+    lib.mxgemm_block128_grouped_weight_gradient_workspace_bytes.argtypes = [i64] * 4
+    lib.mxgemm_block128_grouped_weight_gradient_workspace_bytes.restype = cz
     return lib
 
 
@@ -1120,14 +1123,14 @@ def block128_grouped_gemm(a, sa, b, sb, offsets, activation=None, gate=None, pre
     return (c, z) if preact else c
 
 
-def block128_grouped_weight_gradient(a, sa, b, sb, offsets, c=None, accumulate=False, stream=None):
+def block128_grouped_weight_gradient(a, sa, b, sb, offsets, c=None, accumulate=False, workspace=None, stream=None):
     """C-ABI mxgemm_block128_grouped_weight_gradient: one product over the rows of each group, c (E, M, N) float32, from the
     operands that block128_quantize(..., cols=True, offsets=offsets) makes: a (M, 128 G) codes with sa (G, M) and b
     (N, 128 G) with sb (G, N).  With a of the output's gradient and b of the input it is the weights' gradient.  Zero
     for a group without rows.  c: the output, whose rows may be further apart than N; accumulate adds to it.  Exact up to
     float32 rounding."""
     e = _env or _torch()
-    if stream is None and e.fast is not None:
+    if stream is None and workspace is None and e.fast is not None:
         done = e.fast.grouped_weight_gradient(a, sa, b, sb, offsets, c, accumulate)
         if done is not None:
             return done
@@ -1154,12 +1157,17 @@ def block128_grouped_weight_gradient(a, sa, b, sb, offsets, c=None, accumulate=F
         if c.dtype != e.f32:
             _refuse(MXG_ERR_FMT, "c must be float32")
         ldc = _matrix_rows(c, "c")[4]
-    _here(a.get_device(), sa, b, sb, offsets, c)
+    given = 0 if workspace is None else _workspace_bytes(workspace)
+    _here(a.get_device(), sa, b, sb, offsets, c, workspace)
     if own:
         c = _empty(e, (groups, m, n), e.f32, a.device, stream)
+    need = _lib.mxgemm_block128_grouped_weight_gradient_workspace_bytes(blocks, groups, m, n)
+    if need and workspace is None:
+        workspace, given = _empty(e, (need,), e.u8, a.device, stream, True), need
     st = _lib.mxgemm_block128_grouped_weight_gradient(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(),
                                                       offsets.data_ptr(), c.data_ptr(), ldc, blocks, groups, m, n, fa, fb,
-                                                      flags | (MXG_B128_ACCUMULATE if accumulate else 0), _stream(stream))
+                                                      flags | (MXG_B128_ACCUMULATE if accumulate else 0),
+                                                      _ptr(workspace), given, _stream(stream))
     if st != MXG_OK:
         _raise(st)
     if not own:

@@ -397,9 +397,13 @@ PyObject* grouped_weight_gradient(PyObject*, PyObject* const* v, Py_ssize_t n) {
     ldc = r.ld;
   }
   const Tensor c = given ? *given : fresh({groups, rows, cols}, at::kFloat, *a);
+  Tensor ws;
+  const size_t need = mxgemm_block128_grouped_weight_gradient_workspace_bytes(blocks, groups, rows, cols);
+  if (need) ws = fresh({(int64_t)need}, at::kByte, *a);
   const int status = mxgemm_block128_grouped_weight_gradient(a->data_ptr(), sa->data_ptr<float>(), b->data_ptr(),
                                                              sb->data_ptr<float>(), offsets->data_ptr(), c.data_ptr<float>(),
-                                                             ldc, blocks, groups, rows, cols, fa, fb, flags, stream_of(dev));
+                                                             ldc, blocks, groups, rows, cols, fa, fb, flags,
+                                                             need ? ws.data_ptr() : nullptr, need, stream_of(dev));
   if (status != MXG_OK) return refused(status);
   if (given) {
     changed(*given);

@@ -91,18 +91,26 @@ inline Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
 // float32 columns of a row of the parts' sums
 inline int64_t sums_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
-// The best tile for `tiles(t)` tiles, as a rule not a whole number, of `blocks` blocks of K.
+// The best tile for `tiles(t)` tiles, as a rule not a whole number, of `blocks` blocks of K, which may be cut into parts
+// where values > 0 of them are then added up (as in choose).
 template <class F>
-inline Choice choose_tile(int64_t blocks, bool exact, F tiles) {
+inline Choice choose_tile(int64_t blocks, bool exact, double values, F tiles) {
   Choice best{};
   double best_time = 0;
   for (const Size& t : kSizes[exact]) {
     if (t.bm == 0) break;
-    const double all = tiles(t), rounds = std::ceil(all / kUnits), idle = 1.0 - std::min(1.0, all / kUnits);
-    const double time = rounds * (cdiv(blocks, t.kb) * t.kb * t.block * (1.0 - idle * t.gain) + t.end);
-    if (best.bm == 0 || time < best_time) {
-      best = {0, t.bm, t.bn, t.kb, 1};
-      best_time = time;
+    const double all = tiles(t);
+    const int64_t steps = cdiv(blocks, t.kb);
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (values == 0 || !t.divides || splits > steps || all * (splits - 1) >= kUnits)) break;
+      const int64_t per = cdiv(steps, splits), parts = cdiv(steps, per);
+      const double rounds = std::ceil(all * parts / kUnits), idle = 1.0 - std::min(1.0, all * parts / kUnits);
+      double time = rounds * (per * t.kb * t.block * (1.0 - idle * t.gain) + t.end);
+      if (parts > 1) time += 4.0 + 0.12 * parts + parts * values * 8 / 3e6;
+      if (best.bm == 0 || time < best_time) {
+        best = {0, t.bm, t.bn, t.kb, (int)parts};
+        best_time = time;
+      }
     }
   }
   return best;
@@ -111,21 +119,35 @@ inline Choice choose_tile(int64_t blocks, bool exact, F tiles) {
 // Rows in E groups, whose sizes the host does not know: taken as T / E and spread around it, so that a group has a tile at
 // least and half a tile more than its rows where they are more.  Forced one at a time over 48 cases of 8 to 128
 // groups of 4 to 200 rows, 512 x 2048 to 2048 x 7168, sizes e^(0.5 normal), the tiles chosen cost 2.7% more than the best.
-// The kernel for few rows, which reads a group's B once for each 16 of them, is the faster with a row or two to a group:
+//
+// The kernel for few rows, 16 or 32 of a group and 16 or 32 columns to a workgroup, divides K between its waves, which is
+// the faster where there are no more workgroups than compute units (of 16 rows and for a float32 C: twice as many)
+//   1 x 2048 x 4096, 3 rows     16 x 16 6.0 us   16 x 32 7.7   tiles 10.6   float32 6.3, 15.7
+//   2 x 2048 x 4096, 12 each    32 x 16 8.0 us   16 x 32 9.3   tiles 10.6           8.3, 15.9
+//   8 x 1024 x 4096, 3 each     16 x 32 8.4 us   16 x 16 9.2   tiles 10.6           8.6, 15.8
+//   16 x 1024 x 1024, 12 each   32 x 32 7.2 us   16 x 32 8.2   tiles  6.7           10.0, 8.1
+// and, since its workgroups ask for B at once, with a row or two to a group, whatever their number
 //   32 x 2048 x 7168     1 row 51.2 us (tiles 54.5), 4 rows 78.3 (79.6), 8 rows 88.4 (82.1)
 //   128 x 512 x 2048     1 row 17.2 us (19.4), 4 rows 26.4 (23.9)
 inline Choice choose_grouped(int64_t T, int64_t E, int64_t N, int64_t K, bool exact) {
   const int64_t groups = std::max<int64_t>(1, std::min(T, E));
-  if (T <= 2 * groups) return {32, 16, 0, 1, 1};
-  return choose_tile(cdiv(K, 128), exact, [&](const Size& t) {
-    const double rows = (double)T / groups / t.bm;
-    return groups * std::max(1.0, rows + 0.5 * std::min(1.0, rows)) * cdiv(N, t.bn);
-  });
+  // pieces of `of` rows that the groups make
+  const auto pieces = [&](int of) {
+    const double rows = (double)T / groups / of;
+    return groups * std::max(1.0, rows + 0.5 * std::min(1.0, rows));
+  };
+  if (T <= 32 * groups) {
+    const int rows = T <= 8 * groups ? 16 : 32;
+    const double units = exact && rows == 16 ? 2 * kUnits : kUnits;
+    if (pieces(rows) * cdiv(N, 16) <= kUnits) return {16, rows, 0, 1, 1};
+    if (pieces(rows) * cdiv(N, 32) <= units || T <= 2 * groups) return {32, rows, 0, 1, 1};
+  }
+  return choose_tile(cdiv(K, 128), exact, 0, [&](const Size& t) { return pieces(t.bm) * cdiv(N, t.bn); });
 }
 
-// Groups along K: E products (M, N) over their shares of all blocks.
+// Groups along K: E products (M, N) over their shares of all blocks; a group with few of them leaves parts empty.
 inline Choice choose_deep(int64_t all, int64_t E, int64_t M, int64_t N) {
-  return choose_tile(cdiv(all, E), true, [&](const Size& t) { return (double)(E * cdiv(M, t.bm) * cdiv(N, t.bn)); });
+  return choose_tile(cdiv(all, E), true, (double)E * M * N, [&](const Size& t) { return (double)(E * cdiv(M, t.bm) * cdiv(N, t.bn)); });
 }
 
 // Blocks of 128 rows that E groups of T rows in all take at most, each starting with a block of its own.

@@ -58,6 +58,7 @@ template <Form FORM>
 using params_t = std::conditional_t<FORM == kPlain, GemmParams, MoreParams>;
 constexpr bool has_ends(Form f) { return f == kEnds || f == kRowGroups; }
 constexpr bool has_groups(Form f) { return f == kRowGroups || f == kDeepGroups; }
+constexpr bool divides_k(Form f) { return f == kPlain || f == kDeepGroups; }
 
 // 16 bytes where an element of C may lie: gfx950 takes 16-byte accesses at any alignment.
 typedef v4u v4u_at2 __attribute__((aligned(2)));
@@ -122,14 +123,18 @@ struct Walk {
 
   __device__ __forceinline__ int items() const {
     if constexpr (FORM == kRowGroups) return __builtin_amdgcn_readfirstlane(table->units[p.groups.E]) * p.tilesN;
-    else return T::kParts && FORM == kPlain ? p.num_tiles * p.splits : p.num_tiles;
+    else return T::kParts && divides_k(FORM) ? p.num_tiles * p.splits : p.num_tiles;
   }
   __device__ __forceinline__ Part part(int item) {
     if constexpr (FORM == kDeepGroups) {
-      // a group without rows takes one step in which everything reads as zero
-      const int e = item / (p.tilesM * p.tilesN);
-      const int from = __builtin_amdgcn_readfirstlane(table->units[e]);
-      const int to = __builtin_amdgcn_readfirstlane(table->units[e + 1]);
+      const int s = T::kParts && p.splits > 1 ? item / p.num_tiles : 0, e = (item - s * p.num_tiles) / (p.tilesM * p.tilesN);
+      int from = __builtin_amdgcn_readfirstlane(table->units[e]), to = __builtin_amdgcn_readfirstlane(table->units[e + 1]);
+      if (T::kParts && p.splits > 1) {
+        const int steps = (to - from + T::kKB - 1) / T::kKB, per = (steps + p.splits - 1) / p.splits * T::kKB;
+        from = __builtin_amdgcn_readfirstlane(min(from + s * per, to));
+        to = __builtin_amdgcn_readfirstlane(min(from + per, to));
+      }
+      // a group or part without blocks takes one step in which everything reads as zero
       return {from, max(1, (to - from + T::kKB - 1) / T::kKB), to};
     } else {
       if (!T::kParts || FORM != kPlain || p.splits == 1) return {0, p.steps, 0};
@@ -141,7 +146,7 @@ struct Walk {
   // its K; items of one part follow each other.
   __device__ __forceinline__ TileAt tile(int t) {
     constexpr int bm = T::kBM, bn = T::kBN;
-    if (T::kParts && FORM == kPlain && p.splits > 1) t %= p.num_tiles;
+    if (T::kParts && divides_k(FORM) && p.splits > 1) t %= p.num_tiles;
     int l, r, rows_of_tiles = p.tilesM, m_at = 0, m_end = p.M;
     if constexpr (FORM == kRowGroups) {
       l = group = groups::lookup(table, p.groups.E, t / p.tilesN, group, lane);
@@ -825,7 +830,7 @@ __global__ __launch_bounds__(64 * T::kAllWaves, (T::kAllWaves + 3) / 4) void blo
       stored = true;
       const TileAt at = walk.tile(item);
       // a part's sums go to the workspace, which the host has described as C: (splits, L, M, ldc)
-      const int l = at.l + (T::kParts && FORM == kPlain && p.splits > 1 ? item / p.num_tiles * p.L : 0);
+      const int l = at.l + (T::kParts && divides_k(FORM) && p.splits > 1 ? item / p.num_tiles * p.L : 0);
       item += G;
       count = item < items ? walk.part(item).count : 0;
       const int rows = at.rows, cols = min(p.N - at.n0, T::kBN);

@@ -24,6 +24,14 @@ int check_groups(int64_t T, int64_t E) {
   return T < 0 || E < 0 || T > mxg::groups::kMaxRows || E > mxg::groups::kMaxGroups ? MXG_ERR_SHAPE : MXG_OK;
 }
 
+// Sizes of the weights' gradient.
+int check_deep(int64_t blocks, int64_t E, int64_t M, int64_t N) {
+  if (blocks < 0 || M < 0 || N < 0 || check_groups(0, E) != MXG_OK) return MXG_ERR_SHAPE;
+  if (M > kTop || N > kTop || blocks > (1 << 16) - 1) return MXG_ERR_SHAPE;
+  if (E * cdiv(M, 32) > 0x7FFFFFFFLL / std::max<int64_t>(1, cdiv(N, 32))) return MXG_ERR_SHAPE;
+  return MXG_OK;
+}
+
 bool offsets_aligned(const void* offsets, unsigned flags) {
   return aligned_to(offsets, (flags & MXG_GROUP_OFFSETS64) ? 8 : 4);
 }
@@ -195,28 +203,36 @@ int mxgemm_block128_grouped(const void* A, const float* SA, const void* B, const
   return more_launch(ch, exact)(kRowGroups, p, a_fmt, b_fmt, c_dtype, grid, s) == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 
+size_t mxgemm_block128_grouped_weight_gradient_workspace_bytes(int64_t blocks, int64_t E, int64_t M, int64_t N) {
+  if (check_deep(blocks, E, M, N) != MXG_OK || blocks == 0 || E == 0 || M == 0 || N == 0) return 0;
+  const Choice ch = choose_deep(blocks, E, M, N);
+  return ch.splits > 1 ? (size_t)(ch.splits * E * M * sums_ld(N) * 4) : 0;
+}
+
 int mxgemm_block128_grouped_weight_gradient(const void* A, const float* SA, const void* B, const float* SB, const void* offsets,
                                             float* C, int64_t ldc, int64_t blocks, int64_t E, int64_t M, int64_t N, int a_fmt,
-                                            int b_fmt, unsigned flags, void* stream) {
+                                            int b_fmt, unsigned flags, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
   const bool trusted = take_trust(&flags);
-  int st = check_groups(0, E);
+  int st = check_deep(blocks, E, M, N);
   if (st != MXG_OK) return st;
-  if (blocks < 0 || M < 0 || N < 0 || ldc < N) return MXG_ERR_SHAPE;
+  if (ldc < N || ldc > (1LL << 21)) return MXG_ERR_SHAPE;
   for (int f : {a_fmt, b_fmt})
     if (f != MXG_FMT_E4M3 && f != MXG_FMT_E5M2) return MXG_ERR_FMT;
   if (flags & ~(unsigned)(MXG_GROUP_OFFSETS64 | MXG_B128_ACCUMULATE)) return MXG_ERR_FLAGS;
-  if (M > kTop || N > kTop || blocks > (1 << 16) - 1 || ldc > (1LL << 21)) return MXG_ERR_SHAPE;
-  if (E * cdiv(M, 32) > 0x7FFFFFFFLL / std::max<int64_t>(1, cdiv(N, 32))) return MXG_ERR_SHAPE;
   if (E == 0 || M == 0 || N == 0) return MXG_OK;
   if (!C || (blocks > 0 && (!A || !SA || !B || !SB || !offsets))) return MXG_ERR_NULL;
+  const size_t need = mxgemm_block128_grouped_weight_gradient_workspace_bytes(blocks, E, M, N);
+  if (need > 0 && !workspace) return MXG_ERR_NULL;
+  if (need > workspace_bytes) return MXG_ERR_SHAPE;
   if (!aligned16(A) || !aligned16(B) || !aligned_to(SA, 4) || !aligned_to(SB, 4) || !aligned_to(C, 4) ||
-      !offsets_aligned(offsets, flags))
+      !offsets_aligned(offsets, flags) || (need > 0 && !aligned16(workspace)))
     return MXG_ERR_ALIGN;
   int dev = 0, cus = 0;
   st = device_check(&dev, &cus);
   if (st != MXG_OK) return st;
   if (!trusted)
-    for (const void* t : {A, (const void*)SA, B, (const void*)SB, offsets, (const void*)C})
+    for (const void* t : {A, (const void*)SA, B, (const void*)SB, offsets, (const void*)C, need > 0 ? (const void*)workspace : nullptr})
       if (t && !on_device(t, dev)) return MXG_ERR_DEVICE;
   MoreParams p{};
   p.A = static_cast<const uint8_t*>(A);
@@ -240,10 +256,26 @@ int mxgemm_block128_grouped_weight_gradient(const void* A, const float* SA, cons
   p.tilesM = (int)cdiv(M, ch.bm);
   p.tilesN = (int)cdiv(N, ch.bn);
   p.num_tiles = (int)(E * p.tilesM * p.tilesN);
-  p.splits = 1;
-  const int64_t grid = std::min<int64_t>(p.num_tiles, cus);
+  p.splits = ch.splits;
+  const int64_t grid = std::min<int64_t>((int64_t)p.num_tiles * p.splits, cus);
   p.xcd_remap = grid % 8 == 0;
-  return more_launch(ch, true)(kDeepGroups, p, a_fmt, b_fmt, MXG_DT_F32, grid, s) == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
+  GemmParams last = p;  // what adds the parts up
+  if (p.splits > 1) {
+    // a part's sums are a float32 C of their own
+    last.sums = static_cast<float*>(workspace);
+    last.ldw = (int)sums_ld(N);
+    p.C = workspace;
+    p.ldc = last.ldw;
+    p.c_vec = N % 4 == 0;
+    p.accumulate = false;
+  }
+  hipError_t e = more_launch(ch, true)(kDeepGroups, p, a_fmt, b_fmt, MXG_DT_F32, grid, s);
+  if (e == hipSuccess && p.splits > 1) {
+    const dim3 g((unsigned)std::min<int64_t>(cdiv(E * M * (last.ldw / 4), 256), 8LL * cus)), b(256);
+    hipLaunchKernelGGL((block128_sum_kernel<0, kPlain>), g, b, 0, s, last, p.splits);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? MXG_OK : MXG_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -689,13 +689,18 @@ int mxgemm_block128_grouped(const void* A, const float* SA, const void* B, const
  *        (blocks, N); blocks = mxgemm_group_blocks(T, E) < 2^16.
  *   C  : (E, M, N) float32, rows ldc >= N apart, groups M * ldc apart; zero for
  *        a group without rows.  MXG_B128_ACCUMULATE: C += product.
- * Products and sums as in a float32 C of mxgemm_block128.  Needs no workspace.
+ * Products and sums as in a float32 C of mxgemm_block128.
+ *   workspace : device memory of at least
+ *        mxgemm_block128_grouped_weight_gradient_workspace_bytes, 16-byte aligned,
+ *        overwritten; NULL where that is 0.
  * flags: MXG_GROUP_OFFSETS64, MXG_B128_ACCUMULATE.  Errors as there.  E, M or N
  * == 0 queues nothing; blocks == 0 makes C zero (leaves it with ACCUMULATE).
  */
 int mxgemm_block128_grouped_weight_gradient(const void* A, const float* SA, const void* B, const float* SB, const void* offsets,
                                             float* C, int64_t ldc, int64_t blocks, int64_t E, int64_t M, int64_t N,
-                                            int a_fmt, int b_fmt, unsigned flags, void* stream);
+                                            int a_fmt, int b_fmt, unsigned flags, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+size_t mxgemm_block128_grouped_weight_gradient_workspace_bytes(int64_t blocks, int64_t E, int64_t M, int64_t N);
 
 /* layouts of the rotary features inside a head */
 enum {

@@ -131,8 +131,9 @@ def test_grouped_refusals(lib):
 def test_weight_gradient_refusals(lib):
     f = lib._lib.mxgemm_block128_grouped_weight_gradient
 
-    def call(A=GOOD, SA=GOOD, B=GOOD, SB=GOOD, off=GOOD, C=GOOD, ldc=128, blocks=3, E=4, M=64, N=128, fa=0, fb=0, flags=0):
-        return f(A, SA, B, SB, off, C, ldc, blocks, E, M, N, fa, fb, flags, None)
+    def call(A=GOOD, SA=GOOD, B=GOOD, SB=GOOD, off=GOOD, C=GOOD, ldc=128, blocks=3, E=4, M=64, N=128, fa=0, fb=0, flags=0,
+             ws=GOOD, nws=1 << 40):
+        return f(A, SA, B, SB, off, C, ldc, blocks, E, M, N, fa, fb, flags, ws, nws, None)
     assert call() == lib.MXG_ERR_DEVICE and call(flags=256 | lib.MXG_B128_ACCUMULATE) == lib.MXG_ERR_DEVICE
     for bad in ({"blocks": -1}, {"E": -1}, {"M": -1}, {"N": -1, "ldc": 0}, {"ldc": 127}, {"blocks": 1 << 16}, {"E": 1025},
                 {"ldc": (1 << 21) + 1}, {"M": 1 << 31}, {"E": 1024, "M": 1 << 20, "N": 1 << 20, "ldc": 1 << 20}):
@@ -143,6 +144,10 @@ def test_weight_gradient_refusals(lib):
         assert call(**{name: None}) == lib.MXG_ERR_NULL, name
     for bad in ({"A": GOOD + 8}, {"SB": GOOD + 2}, {"C": GOOD + 2}, {"off": GOOD + 2}):
         assert call(**bad) == lib.MXG_ERR_ALIGN, bad
+    need = lib._lib.mxgemm_block128_grouped_weight_gradient_workspace_bytes(80, 1, 64, 128)
+    assert need > 0 and lib._lib.mxgemm_block128_grouped_weight_gradient_workspace_bytes(3, 4, 64, 128) == 0
+    assert call(blocks=80, E=1, ws=None) == lib.MXG_ERR_NULL and call(blocks=80, E=1, nws=need - 1) == lib.MXG_ERR_SHAPE
+    assert call(blocks=80, E=1, ws=GOOD + 8) == lib.MXG_ERR_ALIGN and call(ws=None, nws=0) == lib.MXG_ERR_DEVICE
     assert call(C=None, E=0) == lib.MXG_OK and call(C=None, M=0) == lib.MXG_OK and call(C=None, N=0, ldc=0) == lib.MXG_OK
 
 

@@ -516,7 +516,9 @@ def check_weight_gradient(lib, sizes, m, n, head=0, tail=0, fa=1, fb=0, pad=0, i
 @pytest.mark.parametrize("sizes,m,n,head,tail", [([1], 8, 16, 0, 0), ([0, 5, 0], 100, 70, 1, 1), ([128, 127, 129], 130, 300, 0, 0),
                                                  (sizes_of(900, 4, 1), 200, 300, 0, 30), (sizes_of(900, 4, 2), 1000, 1000, 5, 0),
                                                  (sizes_of(1500, 4, 3), 2000, 2001, 0, 0), (sizes_of(3000, 6, 4), 4000, 2000, 0, 0),
-                                                 (sizes_of(600, 250, 5), 40, 72, 0, 0), ([3] * 1024, 16, 24, 0, 0)])
+                                                 (sizes_of(600, 250, 5), 40, 72, 0, 0), ([3] * 1024, 16, 24, 0, 0),
+                                                 # few tiles: the blocks in parts, some of them empty
+                                                 ([4000], 70, 130, 3, 0), ([3000, 0, 200, 1], 200, 101, 0, 0), ([5000, 700], 500, 300, 0, 9)])
 def test_weight_gradient_sizes(lib, sizes, m, n, head, tail):
     check_weight_gradient(lib, sizes, m, n, head, tail)
     check_weight_gradient(lib, sizes, m, n, head, tail, pad=3, index=torch.int64, seed=5)

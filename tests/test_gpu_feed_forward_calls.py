@@ -179,6 +179,11 @@ def test_other_streams(lib):
     check_streams(lambda **kw: lib.block128_quantize(g, cols=True, offsets=off, **kw))
     _, _, q, s = lib.block128_quantize(g, cols=True, offsets=off)
     check_streams(lambda **kw: (lib.block128_grouped_weight_gradient(q, s, q, s, off, **kw),))
+    off = offsets(6000)
+    _, _, q, s = lib.block128_quantize(rand(6000, 200), cols=True, offsets=off)
+    scratch = lib._lib.mxgemm_block128_grouped_weight_gradient_workspace_bytes(q.shape[1] // 128, 1, 200, 200)
+    assert scratch > 0
+    check_streams(lambda **kw: (lib.block128_grouped_weight_gradient(q, s, q, s, off, **kw),), [scratch])
 
 
 def test_in_a_graph(lib):
