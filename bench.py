@@ -722,6 +722,67 @@ def bench_qkv(args):
         "decode_us": round(decode_ms * 1e3, 2), "decode_graph_us": round(graph_ms * 1e3, 2)}), flush=True)
 
 
+def bench_ffn(args):
+    """One JSON line for the feed-forward layers (examples/feed_forward.py) in bfloat16: a training step of the one with
+    experts (rows in order of them, sizes unequal), its forward pass, a decode step of eight rows of eight experts, called
+    as it is and replayed from a graph, and a training step of the dense one."""
+    import torch
+
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import feed_forward
+    tokens, hidden, inner, experts, dense_inner = 8192, 4096, 2048, 32, 8192
+    torch.manual_seed(5)
+    layer, dense = feed_forward.Experts(experts, hidden, inner), feed_forward.FeedForward(hidden, dense_inner)
+    share = torch.exp(0.5 * torch.randn(experts, generator=torch.Generator().manual_seed(5)))
+    who = torch.multinomial(share, tokens, replacement=True, generator=torch.Generator().manual_seed(6))
+    sizes = torch.bincount(who, minlength=experts)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), sizes.cumsum(0)]).int().cuda()
+    few = torch.cat([torch.zeros(1, dtype=torch.int64), (torch.arange(experts) % 4 == 0).long().cumsum(0)]).int().cuda()
+    x = torch.randn(tokens, hidden, device="cuda").bfloat16().requires_grad_()
+    dy, one = torch.randn_like(x), x[:8].detach()
+
+    def step(of, *rest):
+        return torch.autograd.grad(of(x, *rest), (x, of.gate, of.up, of.down), dy)
+
+    def forward(rows, where):
+        with torch.no_grad():
+            return layer(rows, where)
+
+    def timed(f, steps):
+        for _ in range(args.warmup):
+            f()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for _ in range(steps):
+            f()
+        torch.cuda.synchronize()
+        return (time.perf_counter() - t0) * 1e3 / steps
+
+    ms = timed(lambda: step(layer, offsets), args.steps)
+    forward_ms, dense_ms = timed(lambda: forward(x, offsets), args.steps), timed(lambda: step(dense), args.steps)
+    decode_ms = timed(lambda: forward(one, few), 10 * args.steps)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        forward(one, few)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        forward(one, few)
+    graph_ms = timed(graph.replay, 10 * args.steps)
+    flops, dense_flops = 6.0 * tokens * hidden * inner, 6.0 * tokens * hidden * dense_inner
+    print(json.dumps({
+        "metric": "feed-forward layer with experts, forward and backward, TFLOP/s (its nine products' flops over the whole step)",
+        "value": round(3 * flops / (ms * 1e-3) / 1e12, 2), "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(ms, 4), "higher_is_better": True, "scaling": "weak",
+        "vs_baseline": None, "dtype": "bf16 in and out, e4m3 codes with float32 scales per 128", "data": "synthetic (seeded normal)",
+        "config": {"workload": "feed-forward with experts", "tokens": tokens, "hidden": hidden, "inner": inner,
+                   "experts": experts, "largest_expert": int(sizes.max()), "dense_inner": dense_inner},
+        "forward_ms": round(forward_ms, 4), "forward_tflops": round(flops / (forward_ms * 1e-3) / 1e12, 1),
+        "decode_us": round(decode_ms * 1e3, 2), "decode_graph_us": round(graph_ms * 1e3, 2),
+        "dense_ms_per_step": round(dense_ms, 4), "dense_tflops": round(3 * dense_flops / (dense_ms * 1e-3) / 1e12, 1)}), flush=True)
+
+
 def bench_probe(args):
     """One JSON line of hardware ceilings measured on this GPU (include/mxgemm_probe.h): the dense MFMA
     rate and shader clock with all CUs busy (bf16 32x32x16 and scaled FP8 32x32x64), the global->LDS
@@ -801,11 +862,12 @@ def main():
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--workload", type=int, default=5)
-    ap.add_argument("--op", choices=["gemm", "quantize", "proj", "qkv", "probe"], default="gemm",
+    ap.add_argument("--op", choices=["gemm", "quantize", "proj", "qkv", "ffn", "probe"], default="gemm",
                     help="gemm: the GEMM + amax step (default); quantize: the MX quantisation of the "
                          "workload's float32 operands; proj: the projection pipeline (row-wise scales -> GEMM -> "
                          "RoPE + dual-direction MXFP8) at the projection workload's shape; qkv: the input half of "
-                         "an attention layer on block-128 codes, forward and backward; probe: hardware "
+                         "an attention layer on block-128 codes, forward and backward; ffn: a feed-forward layer "
+                         "on them, with experts and dense; probe: hardware "
                          "ceilings (MFMA rate and clock, global->LDS path, HBM bandwidth)")
     ap.add_argument("--fp8-mfma", action="store_true", help="time the reduced-precision FP8 MFMA path")
     ap.add_argument("--fp4", action="store_true",
@@ -847,6 +909,9 @@ def main():
         return
     if args.op == "qkv":
         bench_qkv(args)
+        return
+    if args.op == "ffn":
+        bench_ffn(args)
         return
     if args.op == "probe":
         bench_probe(args)
