@@ -92,7 +92,9 @@ inline Choice choose(int64_t M, int64_t N, int64_t K, int64_t L, bool exact) {
 inline int64_t sums_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
 // The best tile for `tiles(t)` tiles, as a rule not a whole number, of `blocks` blocks of K, which may be cut into parts
-// where values > 0 of them are then added up (as in choose).
+// where values > 0 of them are then added up (as in choose).  A last round with few tiles costs less than a whole one
+// where many came before: the units have drifted apart by then, and groups differ in length.  Tiles of
+// 64 rows, which read B most often, lose against the larger ones the longer the chip is full (up to 15% from 1 to 8 rounds).
 template <class F>
 inline Choice choose_tile(int64_t blocks, bool exact, double values, F tiles) {
   Choice best{};
@@ -104,8 +106,9 @@ inline Choice choose_tile(int64_t blocks, bool exact, double values, F tiles) {
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (splits > 1 && (values == 0 || !t.divides || splits > steps || all * (splits - 1) >= kUnits)) break;
       const int64_t per = cdiv(steps, splits), parts = cdiv(steps, per);
-      const double rounds = std::ceil(all * parts / kUnits), idle = 1.0 - std::min(1.0, all * parts / kUnits);
-      double time = rounds * (per * t.kb * t.block * (1.0 - idle * t.gain) + t.end);
+      const double full = all * parts / kUnits, whole = std::ceil(full), idle = 1.0 - std::min(1.0, full);
+      const double slow = exact || t.bm > 64 ? 1.0 : 1.0 + 0.15 * std::min(1.0, std::max(0.0, (full - 1.0) / 7));
+      double time = slow * (whole - 0.5 * (whole - full) * std::min(1.0, full / 4)) * (per * t.kb * t.block * (1.0 - idle * t.gain) + t.end);
       if (parts > 1) time += 4.0 + 0.12 * parts + parts * values * 8 / 3e6;
       if (best.bm == 0 || time < best_time) {
         best = {0, t.bm, t.bn, t.kb, (int)parts};
@@ -117,8 +120,8 @@ inline Choice choose_tile(int64_t blocks, bool exact, double values, F tiles) {
 }
 
 // Rows in E groups, whose sizes the host does not know: taken as T / E and spread around it, so that a group has a tile at
-// least and half a tile more than its rows where they are more.  Forced one at a time over 48 cases of 8 to 128
-// groups of 4 to 200 rows, 512 x 2048 to 2048 x 7168, sizes e^(0.5 normal), the tiles chosen cost 2.7% more than the best.
+// least and half a tile more than its rows where they are more.  Forced one at a time over 128 cases of 4 to 128
+// groups of 24 to 2000 rows, 512 x 2048 to 2048 x 7168, sizes e^(0.5 normal), the tiles chosen cost 2.3% more than the best.
 //
 // The kernel for few rows, 16 or 32 of a group and 16 or 32 columns to a workgroup, divides K between its waves, which is
 // the faster where there are no more workgroups than compute units (of 16 rows and for a float32 C: twice as many)
@@ -134,7 +137,7 @@ inline Choice choose_grouped(int64_t T, int64_t E, int64_t N, int64_t K, bool ex
   // pieces of `of` rows that the groups make
   const auto pieces = [&](int of) {
     const double rows = (double)T / groups / of;
-    return groups * std::max(1.0, rows + 0.5 * std::min(1.0, rows));
+    return groups * std::max(1.0, rows + 0.5);
   };
   if (T <= 32 * groups) {
     const int rows = T <= 8 * groups ? 16 : 32;
