@@ -49,7 +49,13 @@ class FeedForward(_Weights):
         super().__init__((), hidden, inner, device)
 
     def forward(self, x):
-        return _FeedForward.apply(x, self.gate, self.up, self.down, self.codes())
+        if torch.is_grad_enabled():
+            return _FeedForward.apply(x, self.gate, self.up, self.down, self.codes())
+        (g, gs, _, _), (w, ws, _, _), (d, ds, _, _) = self.codes()
+        xq, xs, _, _ = mx.block128_quantize(x)
+        h = mx.block128_linear(xq, xs, g, gs, activation="silu", gate=mx.block128_gemm(xq, xs, w, ws))
+        hq, hs, _, _ = mx.block128_quantize(h)
+        return mx.block128_linear(hq, hs, d, ds, residual=x)
 
 
 class _FeedForward(torch.autograd.Function):
@@ -88,7 +94,14 @@ class Experts(_Weights):
         super().__init__((experts,), hidden, inner, device)
 
     def forward(self, x, offsets):
-        return _Experts.apply(x, self.gate, self.up, self.down, self.codes(), offsets)
+        if torch.is_grad_enabled():
+            return _Experts.apply(x, self.gate, self.up, self.down, self.codes(), offsets)
+        (g, gs, _, _), (w, ws, _, _), (d, ds, _, _) = self.codes()
+        xq, xs, _, _ = mx.block128_quantize(x)
+        h = mx.block128_grouped_gemm(xq, xs, g, gs, offsets, activation="silu",
+                                     gate=mx.block128_grouped_gemm(xq, xs, w, ws, offsets))
+        hq, hs, _, _ = mx.block128_quantize(h)
+        return mx.block128_grouped_gemm(hq, hs, d, ds, offsets)
 
 
 class _Experts(torch.autograd.Function):
@@ -138,10 +151,13 @@ def check(hidden=512, inner=1024, tokens=300, sizes=(100, 0, 3, 260, 129), behin
     y = layer(x)
     dy = torch.randn_like(y)
     y.backward(dy)
+    with torch.no_grad():
+        served = layer(x)
     ref_in = [t.detach().float().requires_grad_() for t in (x, layer.gate, layer.up, layer.down)]
     ref = plain(*ref_in) + ref_in[0]
     ref.backward(dy.float())
     errors["dense y"] = off(y, ref)
+    errors["dense served y"] = off(served, ref)
     for name, a, b in zip(("dx", "dgate", "dup", "ddown"), (x, layer.gate, layer.up, layer.down), ref_in):
         errors["dense " + name] = off(a.grad, b.grad)
 
@@ -152,11 +168,14 @@ def check(hidden=512, inner=1024, tokens=300, sizes=(100, 0, 3, 260, 129), behin
     y = experts(x, ends.int().cuda())
     dy = torch.randn_like(y)
     y.backward(dy)
+    with torch.no_grad():
+        served = experts(x, ends.int().cuda())
     ref_in = [t.detach().float().requires_grad_() for t in (x, experts.gate, experts.up, experts.down)]
     parts = [plain(ref_in[0][a:b], *(w[e] for w in ref_in[1:])) for e, (a, b) in enumerate(zip(ends[:-1], ends[1:]))]
     ref = torch.cat(parts + [torch.zeros(behind, hidden, device="cuda")])
     ref.backward(dy.float())
     errors["experts y"] = off(y, ref)
+    errors["experts served y"] = off(served, ref)
     for name, a, b in zip(("dx", "dgate", "dup", "ddown"), (x, experts.gate, experts.up, experts.down), ref_in):
         errors["experts " + name] = off(a.grad, b.grad)
     return errors
@@ -164,4 +183,4 @@ def check(hidden=512, inner=1024, tokens=300, sizes=(100, 0, 3, 260, 129), behin
 
 if __name__ == "__main__":
     for name, e in check().items():
-        print(f"{name:14s} relative error {e:.4f}")
+        print(f"{name:16s} relative error {e:.4f}")
