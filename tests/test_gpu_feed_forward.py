@@ -263,6 +263,20 @@ def check_backward(lib, m, n, dtype, kind, gate, bias, pad=None, seed=0):
     return dz, dgate, dbias
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_bias_gradient_keeps_float32(lib, dtype):
+    """One z down each column and dy of one, so that a slope's error adds up.  gelu's slope is off by less than 2^-21 (4e-7 of
+    a tail that is at most a half, and roundings of 2^-24 of numbers below 1.13), and the sum of m of them by less than
+    m 2^-24 of it."""
+    m, n = 4, 800
+    z = torch.linspace(-4, 4, n).to(dtype)
+    dbias = lib.activation_backward(torch.ones(m, n, dtype=dtype, device="cuda"), z.expand(m, n).contiguous().cuda(), "gelu",
+                                    bias=True)[2].cpu().double()
+    want = m * torch.from_numpy(F.activation(z.double().numpy(), "gelu")[1])
+    off = (dbias - want).abs() - m * (2.0 ** -21 + 2.0 ** -24 * want.abs())
+    assert off.max() < 0, (off.max(), z[off.argmax()])
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("m,n", [(1, 1), (1, 7), (3, 8), (5, 100), (40, 2048), (333, 65), (129, 513), (700, 24), (64, 24576),
                                  (2500, 1030), (9000, 16)])
