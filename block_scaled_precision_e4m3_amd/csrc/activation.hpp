@@ -6,6 +6,9 @@
 // (of several rows where they are short), a workgroup's waves the rows of one part in turn.  Each lane adds up its
 // columns' dz over its rows, the lanes of a column meet in LDS, and a second kernel adds up the parts; a single part
 // needs none.
+//
+// 8192 x 8192 bfloat16, silu with gate and dbias: 137 us, 4.9 TB/s (a copy moves 5.1); without dbias 132.  1000 x 4096 with
+// dbias 9.3 us, of which the second kernel is 4; 40 x 2048 float32 with dbias, one part: 4.3 us.
 #pragma once
 
 #include "ends.hpp"
@@ -42,7 +45,7 @@ __global__ __launch_bounds__(kThreads) void activation_backward_kernel(Params p)
   v8f sum;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  const auto rows = [&](auto slope) {
+  ends::with_slope<DT != 0>(p.act, [&](auto slope) {
     for (int64_t m = first; m < end; m += kAhead * subs) {
       Raw8<DT> a[kAhead], b[kAhead], g[kAhead];
 #pragma unroll
@@ -75,11 +78,7 @@ __global__ __launch_bounds__(kThreads) void activation_backward_kernel(Params p)
         if constexpr (GATE) store_chunk<DT>(dgate + row * p.ld_dgate, dg, valid);
       }
     }
-  };
-  // dbias keeps float32: gelu's fast form, off by 4.7e-6 of a tail, would show in it (8192 x 8192 float16 with dbias: 97.9
-  // us, 90.9 with the fast form and 10 times the error); the others' forms are off by a few roundings
-  if (DT != 0 && p.act == MXG_ACT_GELU && p.sums) ends::with_slope<false>(MXG_ACT_GELU, rows);
-  else ends::with_slope<DT != 0>(p.act, rows);
+  });
   if (!p.sums) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) lds[tid][i] = sum[i];
