@@ -1005,6 +1005,8 @@ def activation_backward(dy, z, activation=None, gate=None, bias=False, out=None,
         dz, dgate = out
         if dz is None or (dgate is None) != (gate is None):
             _refuse(MXG_ERR_NULL, "out must hold dz, and dgate with a gate")
+        if dgate is not None and dz.data_ptr() == dgate.data_ptr() and dz.numel() > 0:
+            _refuse(MXG_ERR_SHAPE, "dz and dgate must be two tensors")
     lds = [_beside(t, shape, dy.dtype, name) for t, name in ((dy, "dy"), (z, "z"), (gate, "gate"), (dz, "dz"), (dgate, "dgate"))]
     _no_history(e, dy, z, gate, dz, dgate)
     _here(dy.get_device(), z, gate, dz, dgate, workspace)

@@ -19,11 +19,14 @@ struct Shares {
   int64_t parts, rows;
 };
 constexpr int64_t kFewRows = 256;
+// Past these columns 64 lanes to a row make a single part as well, in fewer workgroups: a launch's work items have to stay
+// below 2^32, which strips of 64 columns would not from 2^29 on.
+constexpr int64_t kFewColumns = 1 << 19;
 Shares shares(int64_t M, int64_t N) {
   Shares s;
   // Few rows: 8 lanes to a row, which still are whole lines, so that a workgroup takes 128 rows at a time and one part
   // does (40 x 2048 float32: 4.3 us on the GPU; with 64 lanes in three parts and a second kernel 8.3 us).
-  const bool few = M <= kFewRows;
+  const bool few = M <= kFewRows && N <= kFewColumns;
   s.lanes = 1;
   while (s.lanes < (few ? 8 : 64) && 8 * s.lanes < N) s.lanes *= 2;
   s.strips = (int)cdiv(N, 8 * s.lanes);

@@ -139,6 +139,7 @@ def test_refusals_say_what_is_wrong(lib):
                          (lib.MXG_ERR_FMT, lambda: lib.block128_grouped_weight_gradient(q, s, q, s, off, torch.zeros(2, 64, 64, device="cuda").bfloat16())),
                          (lib.MXG_ERR_SHAPE, lambda: lib.block128_grouped_weight_gradient(q, s, q, s, off, torch.zeros(3, 64, 64, device="cuda"))),
                          (lib.MXG_ERR_NULL, lambda: lib.activation_backward(x, x, gate=x, out=(x, None))),
+                         (lib.MXG_ERR_SHAPE, lambda: lib.activation_backward(x, x, gate=x, out=(x, x))),
                          (lib.MXG_ERR_SHAPE, lambda: lib.activation_backward(x, x[:5])),
                          (lib.MXG_ERR_ALIGN, lambda: lib.activation_backward(x[:1].expand(6, 64), x))):
         with pytest.raises(lib.MxgemmError) as e:
@@ -354,6 +355,18 @@ def test_codes_past_32_bits(lib, memory):
     for col in (0, 4095, k - 1):
         assert repeats(qt[col, :T].view(torch.uint8).view(-1, 128), want[2][col].view(torch.uint8).view(-1, 128))
         assert not qt[col, T:].view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("m", [1, 2])
+def test_few_long_rows_of_gradients(lib, memory, m):
+    """More columns than a launch's 2^32 work items take 8 at a time and 64 to a row."""
+    need(40)
+    dy = rand(1, 1 << 20).bfloat16().repeat(m, 513)
+    z = torch.ones_like(dy)
+    z[:, -5:] = -1
+    dz, _, dbias = lib.activation_backward(dy, z, "relu", bias=True)
+    assert torch.equal(dz[:, :-5], dy[:, :-5]) and not dz[:, -5:].any()
+    assert torch.equal(dbias[:-5], m * dy[0, :-5].float()) and not dbias[-5:].any()
 
 
 def test_gradients_past_32_bits(lib, memory):
