@@ -27,8 +27,11 @@
 // rows.
 //
 // The bound is memory: 8192 x 7168 bfloat16, rows and columns, 51 us (4.65
-// TB/s), 7168 x 2048 float32 squares with their transpose 14.9 us; 8 x 7168 rows
-// take 2.3 us, of which 1.95 are an empty launch.
+// TB/s; 38 where the input is partly cached), in 32 groups 59.5 us (with the
+// blocks that groups leave empty), 7168 x 2048 float32 squares with their
+// transpose 14.9 us; 8 x 7168 rows take 2.3 us, of which 1.95 are an empty
+// launch, 8 x 4096 in both directions 4.9, and 6.2 in 32 groups, whose offsets
+// come before the rows can be asked for.
 #pragma once
 
 #include <type_traits>
@@ -267,7 +270,8 @@ __global__ __launch_bounds__(kQThreads) void block128_quantize_kernel(std::condi
         }
         if constexpr (COLS) {
           // with a barrier to come, each row's scale once: lane i < 8 of the 16 makes row i's (8192 x 7168 bfloat16, both
-          // directions, replayed: 39.9 us, 43.2 with every lane making all eight; 8 x 4096: 4.9 and 5.7; the groups above: 24.7)
+          // directions, input partly cached: 39.9 us, 43.2 with every lane making all eight; 8 x 4096: 4.9 and 5.7; the
+          // groups above: 24.7)
           unsigned mine = rmax[0];
 #pragma unroll
           for (int i = 1; i < RT; ++i) mine = (c & 7) == i ? rmax[i] : mine;

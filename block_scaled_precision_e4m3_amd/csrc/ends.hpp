@@ -7,12 +7,12 @@
 //   gelu       z P(z), P the normal distribution's
 //   gelu_tanh  z s(u), u = 2 sqrt(2/pi) (z + 0.044715 z^3), which is z (1 + tanh(u/2)) / 2 without its cancellation
 //
-// P's tail, and from it P, is e^(-x^2/2) R(x), x = |z|, with R a polynomial in 1 / (1 + p x) fitted to erfcx(x / sqrt 2) / 2
-// over 0..14 for the least relative error.  FAST is for results that are rounded to 16 bits: hardware exponential and
+// P's tail, and from it P, is e^(-x^2/2) R(x), x = |z|, with R a polynomial in 1 / (1 + p x) fitted to erfcx(x / sqrt 2) /
+// 2 over 0..14 for the least relative error.  FAST is for results that are rounded to 16 bits: hardware exponential and
 // reciprocal (about 2^-22, and |u| 2^-24 for the exponential's argument), and R of degree 6, off by 4.7e-6: a fiftieth of
 // float16's rounding.  Slopes take R of degree 8 all the same, since their sums, the bias' gradient, are float32 (degree 6:
-// 1.4e-6 off over 8192 rows, degree 8: 1.5e-7, in the same time).  The others keep what the exponential's argument loses, divide, and take R of degree 8, off by 4e-7
-// of the tail with the rounding of its own sums.
+// 1.4e-6 off over 8192 rows, degree 8: 1.5e-7, in the same time).  The others keep what the exponential's argument loses,
+// divide, and take R of degree 8, off by 4e-7 of the tail with the rounding of its own sums.
 #pragma once
 
 #include "../../include/mxgemm.h"
