@@ -18,16 +18,18 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 import block_scaled_precision_e4m3_amd as mx  # noqa: E402
+from weight_codes import WeightCodes  # noqa: E402
 
 
 class AttentionInput(torch.nn.Module):
     """q (T, heads, D), k (T, kv_heads, D) and v (T, kv_heads, D) of hidden states x (T, hidden), bfloat16; norm: q and k
     are normed per head before the positions turn them.
 
-    weight ((heads + 2 kv_heads) D, hidden) is kept in bfloat16 and in codes of both directions, which follow the changes
-    that torch counts (an optimiser's step, load_state_dict); requantise() after others (through weight.data)."""
+    weight ((heads + 2 kv_heads) D, hidden) is kept in bfloat16 and in codes of both directions, kept while the weight stays
+    what it is (weight_codes.py); requantise() after changes that torch does not count (through weight.data)."""
 
     def __init__(self, hidden, heads, kv_heads, head_dim, max_positions, rot=None, norm=True, eps=1e-6,
                  device="cuda"):
@@ -38,16 +40,15 @@ class AttentionInput(torch.nn.Module):
         self.q_norm = torch.nn.Parameter(torch.ones(head_dim, device=device)) if norm else None
         self.k_norm = torch.nn.Parameter(torch.ones(head_dim, device=device)) if norm else None
         self.cos, self.sin = mx.rope_table(max_positions, rot or head_dim, device=device)
+        self.kept = WeightCodes()
         self.requantise()
 
-    @torch.no_grad()
-    def requantise(self):
-        self.codes = mx.block128_quantize(self.weight, square=True, cols=True)
-        self.codes_of = self.changes()
+    @property
+    def codes(self):
+        return self.kept(self.weight)[0]
 
-    def changes(self):
-        """torch's count of the weight's changes; inference tensors have none."""
-        return None if self.weight.is_inference() else self.weight._version
+    def requantise(self):
+        self.kept.make(self.weight)
 
     def split(self, y):
         """Views of the projection's output (T, (heads + 2 kv_heads) D)."""
@@ -69,23 +70,23 @@ class AttentionInput(torch.nn.Module):
                                         out=out)[2:]
 
     def forward(self, x, positions=None):
-        if self.codes_of != self.changes():
-            self.requantise()
         if torch.is_grad_enabled():
-            return _AttentionInput.apply(x, self.weight, self.q_norm, self.k_norm, self, positions)
+            return _AttentionInput.apply(x, self.weight, self.q_norm, self.k_norm, self, self.codes, positions)
+        w, ws, _, _ = self.codes
         xq, xs, _, _ = mx.block128_quantize(x)
-        q, k, v = self.split(mx.block128_gemm(xq, xs, self.codes[0], self.codes[1]))
+        q, k, v = self.split(mx.block128_gemm(xq, xs, w, ws))
         return *self.positioned(q, k, positions), v
 
 
 class _AttentionInput(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, q_norm, k_norm, layer, positions):
+    def forward(ctx, x, weight, q_norm, k_norm, layer, codes, positions):
+        w, ws, wt, wts = codes
         xq, xs, xqt, xst = mx.block128_quantize(x, cols=True)
-        y = mx.block128_gemm(xq, xs, layer.codes[0], layer.codes[1])
+        y = mx.block128_gemm(xq, xs, w, ws)
         q, k, v = layer.split(y)
         ctx.layer = layer
-        ctx.save_for_backward(y, xqt, xst, q_norm, k_norm, *layer.codes[2:], positions)
+        ctx.save_for_backward(y, xqt, xst, q_norm, k_norm, wt, wts, positions)
         # a view of y may not leave: y is kept as it is for the backward pass
         return *layer.positioned(q, k, positions), v.clone()
 
@@ -102,7 +103,7 @@ class _AttentionInput(torch.autograd.Function):
         g, gs, gt, gts = mx.block128_quantize(dy, cols=True)
         dx = mx.block128_gemm(g, gs, wt, wts)
         dw = mx.block128_gemm(gt, gts, xqt, xst, b_block=1, c_dtype=torch.float32)
-        return dx, dw.to(layer.weight.dtype), dqn, dkn, None, None
+        return dx, dw.to(layer.weight.dtype), dqn, dkn, None, None, None
 
 
 def plain(layer, x, weight, q_norm, k_norm, positions):

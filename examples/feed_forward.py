@@ -18,28 +18,28 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 import block_scaled_precision_e4m3_amd as mx  # noqa: E402
+from weight_codes import WeightCodes  # noqa: E402
 
 
 class _Weights(torch.nn.Module):
-    """gate, up (..., inner, hidden) and down (..., hidden, inner), bfloat16, with their codes in both directions, which
-    follow the changes that torch counts."""
+    """gate, up (..., inner, hidden) and down (..., hidden, inner), bfloat16, with their codes in both directions, kept while
+    the weights stay what they are (weight_codes.py); requantise() after changes that torch does not count (through .data)."""
 
     def __init__(self, lead, hidden, inner, device):
         super().__init__()
         self.gate, self.up = (torch.nn.Parameter((torch.randn(*lead, inner, hidden, device=device) / hidden ** 0.5).bfloat16())
                               for _ in range(2))
         self.down = torch.nn.Parameter((torch.randn(*lead, hidden, inner, device=device) / inner ** 0.5).bfloat16())
-        self.codes_of = None
+        self.kept = WeightCodes()
 
-    @torch.no_grad()
     def codes(self):
-        now = tuple(None if w.is_inference() else w._version for w in (self.gate, self.up, self.down))
-        if self.codes_of is None or now != self.codes_of:
-            self.kept = [mx.block128_quantize(w, square=True, cols=True) for w in (self.gate, self.up, self.down)]
-            self.codes_of = now
-        return self.kept
+        return self.kept(self.gate, self.up, self.down)
+
+    def requantise(self):
+        self.kept.make(self.gate, self.up, self.down)
 
 
 class FeedForward(_Weights):
