@@ -951,8 +951,8 @@ def block128_linear(a, sa, b, sb, bias=None, activation=None, gate=None, residua
     a (M, K) codes with sa (ceil(K/128), M), b (N, K) codes with sb (ceil(N/128), ceil(K/128)): blocks of 128 x 128.
     activation: None, "relu", "silu", "gelu" or "gelu_tanh"; bias (N) float32 or of c's dtype; gate and residual (M, N)
     of c's dtype, rows possibly further apart; each may be None.  c: the output, new by default; it may be residual or gate
-    itself.  c_dtype, accuracy and workspace as of block128_gemm.  Returns c, or (c, z) with preact: z in c's dtype, from
-    which activation_backward makes the gradients.
+    itself, and is refused where it lies on them or on other operands in another way.  c_dtype, accuracy and workspace as of
+    block128_gemm.  Returns c, or (c, z) with preact: z in c's dtype, from which activation_backward makes the gradients.
 
     Not differentiable (codes have no gradient): a layer defines its own, as examples/feed_forward.py does, and inputs
     that require gradients are refused outside torch.no_grad()."""
@@ -987,7 +987,8 @@ def activation_backward(dy, z, activation=None, gate=None, bias=False, out=None,
     and, with bias, dbias (N) float32, dz's sum over rows (else None).
 
     dz is the product's gradient; the residual's is dy.  dy, z and gate are (M, N) of one dtype, rows possibly further
-    apart.  out: the pair (dz, dgate), which may be any of dy, z and gate."""
+    apart.  out: the pair (dz, dgate), two of dy, z, gate and others; refused where they lie on these or on each other in
+    another way."""
     e = _env or _torch()
     if out is None and stream is None and workspace is None and e.fast is not None:
         done = e.fast.activation_backward(dy, z, activation, gate, bias)
@@ -1100,8 +1101,9 @@ def block128_grouped_gemm(a, sa, b, sb, offsets, activation=None, gate=None, pre
     kernel and need not be known on the host.  Groups may be empty.  Rows before the first group and behind the last one
     are left as they were in a given c, and zero in a new one and in z.  E is at most 1024, T at most 2^24.
 
-    activation, gate, preact, c_dtype and the refusal of inputs that require gradients as in block128_linear.  The input's
-    gradient is the same call with b's transposed codes; the weights' is block128_grouped_weight_gradient."""
+    activation, gate, preact, c_dtype, c (which may be gate) and the refusal of inputs that require gradients as in
+    block128_linear.  The input's gradient is the same call with b's transposed codes; the weights' is
+    block128_grouped_weight_gradient."""
     e = _env or _torch()
     if stream is None and e.fast is not None:
         done = e.fast.grouped(a, sa, b, sb, offsets, activation, gate, preact, c_dtype, c)

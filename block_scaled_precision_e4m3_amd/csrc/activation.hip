@@ -7,6 +7,7 @@
 #include "../../include/mxgemm.h"
 #include "activation.hpp"
 #include "host_checks.hpp"
+#include "overlap.hpp"
 
 namespace {
 
@@ -90,6 +91,17 @@ int mxgemm_activation_backward(const void* DY, const void* Z, const void* GATE, 
       if (t && !on_device(t, dev)) return MXG_ERR_DEVICE;
     if (need > 0 && !on_device(workspace, dev)) return MXG_ERR_DEVICE;
   }
+  // Workgroups would read what others have written, or write the same places.  dz and dgate may be one of what is read, the
+  // same rows of it: a lane has read what it writes.
+  RowsAt of[5];
+  for (int i = 0; i < 5; ++i) of[i] = rows_at(all[i], M, N, strides[i], mxg::elem_bytes(dtype));
+  const RowsAt sums = flat(DBIAS, 4 * N), scratch = flat(workspace, (int64_t)need);
+  for (int i = 0; i < 5; ++i) {
+    if (overlap(of[i], sums) || overlap(of[i], scratch)) return MXG_ERR_SHAPE;
+    for (int j = 3; i < 3 && j < 5; ++j)
+      if (overlap(of[i], of[j]) && !same(of[i], of[j])) return MXG_ERR_SHAPE;
+  }
+  if (overlap(of[3], of[4]) || overlap(sums, scratch)) return MXG_ERR_SHAPE;
   hipStream_t s = (hipStream_t)stream;
   if (M == 0) {
     if (DBIAS) hipLaunchKernelGGL(mxg::activation::bias_zero_kernel, dim3((unsigned)cdiv(N, 256)), dim3(256), 0, s, DBIAS, (int)N);

@@ -122,6 +122,13 @@ int product(const void* A, const float* SA, const void* B, const float* SB, void
       (need > 0 && !on_device(workspace, dev))))
     return MXG_ERR_DEVICE;
   if (ends && !trusted && !mxg::b128::ends_on_device(*ends, dev)) return MXG_ERR_DEVICE;
+  if (ends) {
+    const int64_t kb = cdiv(K, 128);
+    if (mxg::b128::outputs_overlap(rows_at(C, M, N, ldc, mxg::elem_bytes(c_dtype)), ends, c_dtype,
+                                   {flat(A, M * K), flat(SA, 4 * kb * M), flat(B, N * K), flat(SB, 4 * kb * cdiv(N, 128)),
+                                    flat(workspace, (int64_t)need)}))
+      return MXG_ERR_SHAPE;
+  }
   MoreParams p{};
   p.A = static_cast<const uint8_t*>(A);
   p.B = static_cast<const uint8_t*>(B);

@@ -1,9 +1,12 @@
 // Host side of what follows a product (ends.hpp): checks of the arguments, and which launch a choice stands for.
 #pragma once
 
+#include <initializer_list>
+
 #include "block128_choose.hpp"
 #include "block128_launch.hpp"
 #include "host_checks.hpp"
+#include "overlap.hpp"
 
 namespace mxg {
 namespace b128 {
@@ -32,6 +35,23 @@ inline bool ends_on_device(const mxgemm_ends_t& e, int dev) {
   for (const void* t : {e.bias, e.gate, e.residual, (const void*)e.preact})
     if (t && !host::on_device(t, dev)) return false;
   return true;
+}
+
+// Whether an output lies on anything that the call reads or writes besides: workgroups would read what others have written.
+// Only gate and residual may be C, the same rows of it, which the lanes that write them have read before.
+inline bool outputs_overlap(const host::RowsAt& c, const mxgemm_ends_t* e, int c_dtype, std::initializer_list<host::RowsAt> others) {
+  using namespace host;
+  for (const RowsAt& o : others)
+    if (overlap(c, o)) return true;
+  if (!e) return false;
+  const int64_t n = elem_bytes(c_dtype), N = c.bytes / n;
+  const RowsAt bias = flat(e->bias, N * elem_bytes(e->bias_dtype)), gate = rows_at(e->gate, c.rows, N, e->ldgate, n),
+               residual = rows_at(e->residual, c.rows, N, e->ldresidual, n), z = rows_at(e->preact, c.rows, N, e->ldpreact, n);
+  for (const RowsAt& o : others)
+    if (overlap(z, o)) return true;
+  for (const RowsAt& o : {gate, residual})
+    if (overlap(z, o) || (overlap(c, o) && !same(c, o))) return true;
+  return overlap(c, bias) || overlap(z, bias) || overlap(c, z);
 }
 
 // Whether rows of all tensors beside C are whole 16-byte chunks, `per` elements each.

@@ -36,6 +36,8 @@ bool offsets_aligned(const void* offsets, unsigned flags) {
   return aligned_to(offsets, (flags & MXG_GROUP_OFFSETS64) ? 8 : 4);
 }
 
+int64_t offsets_bytes(int64_t E, unsigned flags) { return (E + 1) * ((flags & MXG_GROUP_OFFSETS64) ? 8 : 4); }
+
 mxg::groups::Groups groups_of(const void* offsets, int64_t T, int64_t E, unsigned flags) {
   return {offsets, (int)E, (int)T, (flags & MXG_GROUP_OFFSETS64) != 0};
 }
@@ -150,6 +152,10 @@ int mxgemm_block128_grouped(const void* A, const float* SA, const void* B, const
       if (t && !on_device(t, dev)) return MXG_ERR_DEVICE;
     if (ends && !ends_on_device(*ends, dev)) return MXG_ERR_DEVICE;
   }
+  if (outputs_overlap(rows_at(C, T, N, ldc, mxg::elem_bytes(c_dtype)), ends, c_dtype,
+                      {flat(A, T * K), flat(SA, 4 * cdiv(K, 128) * T), flat(B, E * N * K), flat(SB, 4 * E * cdiv(N, 128) * cdiv(K, 128)),
+                       flat(offsets, offsets_bytes(E, flags))}))
+    return MXG_ERR_SHAPE;
   MoreParams p{};
   p.A = static_cast<const uint8_t*>(A);
   p.B = static_cast<const uint8_t*>(B);
@@ -234,6 +240,10 @@ int mxgemm_block128_grouped_weight_gradient(const void* A, const float* SA, cons
   if (!trusted)
     for (const void* t : {A, (const void*)SA, B, (const void*)SB, offsets, (const void*)C, need > 0 ? (const void*)workspace : nullptr})
       if (t && !on_device(t, dev)) return MXG_ERR_DEVICE;
+  if (outputs_overlap(rows_at(C, E * M, N, ldc, 4), nullptr, MXG_DT_F32,
+                      {flat(A, 128 * blocks * M), flat(SA, 4 * blocks * M), flat(B, 128 * blocks * N), flat(SB, 4 * blocks * N),
+                       flat(offsets, offsets_bytes(E, flags)), flat(workspace, (int64_t)need)}))
+    return MXG_ERR_SHAPE;
   MoreParams p{};
   p.A = static_cast<const uint8_t*>(A);
   p.B = static_cast<const uint8_t*>(B);

@@ -717,7 +717,7 @@ const char* mxgemm_strerror(int status) {
   switch (status) {
     case MXG_OK: return "success";
     case MXG_ERR_NULL: return "a required pointer is NULL";
-    case MXG_ERR_SHAPE: return "invalid size (negative, or offsets overflow)";
+    case MXG_ERR_SHAPE: return "invalid size (negative, or offsets overflow), or an output that lies on another tensor";
     case MXG_ERR_ALIGN: return "misaligned buffer (16 bytes), K not a multiple of 16, or N not a multiple of 4";
     case MXG_ERR_SFVEC: return "sf_vec_size must be 16 or 32";
     case MXG_ERR_FMT: return "element format must be MXG_FMT_E4M3 or MXG_FMT_E5M2 (or MXG_FMT_E2M1 for both A and B)";

@@ -567,8 +567,8 @@ enum {
  *              apart.  Either may be C itself with C's row distance.
  *   preact   : (M, N) of C's type, rows ldpreact >= N apart: receives z, from
  *              which mxgemm_activation_backward makes the gradients.
- * No row distance exceeds 2^21.  Other overlaps of outputs with anything are
- * not allowed.
+ * No row distance exceeds 2^21.  Other overlaps of C and preact with each other
+ * or with what the call reads are refused (MXG_ERR_SHAPE).
  */
 typedef struct {
   const void* bias;
@@ -603,7 +603,8 @@ int mxgemm_block128_linear(const void* A, const float* SA, const void* B, const 
  * (dp is dz, and the residual's gradient is dy.)
  *   DY, Z, GATE, DZ, DGATE : (M, N) of `dtype`, rows strides[0..4] >= N elements
  *            apart.  GATE and DGATE may both be NULL (no gate).  DZ and DGATE may each
- *            be one of DY, Z, GATE with the same row distance; no other overlap.
+ *            be one of DY, Z, GATE with the same row distance; other overlaps
+ *            of what is written are refused (MXG_ERR_SHAPE).
  *   DBIAS : (N) float32, overwritten, or NULL.  Summed in a fixed order: equal
  *            calls give equal bits.
  *   workspace : device memory of at least
@@ -688,7 +689,8 @@ int mxgemm_block128_grouped(const void* A, const float* SA, const void* B, const
  *   A  : (M, 128 blocks) codes (QT), SA: (blocks, M) (ST); B: (N, 128 blocks), SB:
  *        (blocks, N); blocks = mxgemm_group_blocks(T, E) < 2^16.
  *   C  : (E, M, N) float32, rows ldc >= N apart, groups M * ldc apart; zero for
- *        a group without rows.  MXG_B128_ACCUMULATE: C += product.
+ *        a group without rows.  MXG_B128_ACCUMULATE: C += product.  It must not
+ *        lie on what the call reads (MXG_ERR_SHAPE).
  * Products and sums as in a float32 C of mxgemm_block128.
  *   workspace : device memory of at least
  *        mxgemm_block128_grouped_weight_gradient_workspace_bytes, 16-byte aligned,
