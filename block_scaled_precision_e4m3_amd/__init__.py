@@ -635,9 +635,19 @@ def _changed(e, *tensors):
             e.torch.autograd.graph.increment_version(t)
 
 
+def _followed(e, tensors):
+    """Whether autograd follows any of the tensors: backward, or forward by a tangent (which no_grad does not end)."""
+    if e.torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    forward = e.torch.autograd.forward_ad
+    if forward._current_level < 0 or not e.torch._C._is_fwd_grad_enabled():
+        return False
+    return any(t is not None and forward.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def _history(e, out, *tensors):
     """Whether a call's result needs a history; one that goes into `out` cannot have any."""
-    if not e.torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (*tensors, *(out or ()))):
+    if not _followed(e, (*tensors, *(out or ()))):
         return False
     if out is not None:
         _refuse(MXG_ERR_FLAGS, "out has no gradient: call without out, or under torch.no_grad()")
@@ -868,10 +878,10 @@ def _activation(name):
 
 
 def _no_history(e, *tensors):
-    """Refuses tensors whose gradient would be lost without a word."""
-    if e.torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        _refuse(MXG_ERR_FLAGS, "the call has no history for autograd: call under torch.no_grad(), and define the layer's "
-                               "gradients with activation_backward")
+    """Refuses tensors whose gradient or tangent would be lost without a word."""
+    if _followed(e, tensors):
+        _refuse(MXG_ERR_FLAGS, "the call has no history for autograd: call under torch.no_grad() and without tangents, and "
+                               "define the layer's gradients with activation_backward")
 
 
 def _beside(t, shape, dtype, name):
@@ -955,7 +965,7 @@ def block128_linear(a, sa, b, sb, bias=None, activation=None, gate=None, residua
     block128_gemm.  Returns c, or (c, z) with preact: z in c's dtype, from which activation_backward makes the gradients.
 
     Not differentiable (codes have no gradient): a layer defines its own, as examples/feed_forward.py does, and inputs
-    that require gradients are refused outside torch.no_grad()."""
+    that require gradients are refused outside torch.no_grad(), those with a tangent everywhere."""
     e = _env or _torch()
     if stream is None and workspace is None and e.fast is not None:
         done = e.fast.linear(a, sa, b, sb, bias, activation, gate, residual, preact, c_dtype, c)
@@ -963,7 +973,7 @@ def block128_linear(a, sa, b, sb, bias=None, activation=None, gate=None, residua
             return done
     m, k, n, fa, fb = _operands(e, a, sa, b, sb, ())
     act = _activation(activation)
-    _no_history(e, bias, gate, residual, c)
+    _no_history(e, a, sa, b, sb, bias, gate, residual, c)
     _here(a.get_device(), sa, b, sb, bias, gate, residual, c, workspace)
     given = 0 if workspace is None else _workspace_bytes(workspace)
     c, ldc, own, z, ct = _product_out(e, m, n, c, c_dtype, preact, a.device, stream)
@@ -1112,7 +1122,7 @@ def block128_grouped_gemm(a, sa, b, sb, offsets, activation=None, gate=None, pre
     groups, flags = _groups(e, offsets)
     m, k, n, fa, fb = _operands(e, a, sa, b, sb, (groups,))
     act = _activation(activation)
-    _no_history(e, gate, c)
+    _no_history(e, a, sa, b, sb, gate, c)
     _here(a.get_device(), sa, b, sb, offsets, gate, c)
     c, ldc, own, z, ct = _product_out(e, m, n, c, c_dtype, preact, a.device, stream)
     ends = _ends(e, act, None, gate, None, z, m, n, c.dtype)
@@ -1153,9 +1163,9 @@ def block128_grouped_weight_gradient(a, sa, b, sb, offsets, c=None, accumulate=F
         _refuse(MXG_ERR_ALIGN, "a and b must be contiguous")
     if accumulate and c is None:
         _refuse(MXG_ERR_NULL, "accumulate needs c")
+    _no_history(e, a, sa, b, sb, c)
     own, ldc = c is None, n
     if not own:
-        _no_history(e, c)
         if c.shape != (groups, m, n):
             _refuse(MXG_ERR_SHAPE, f"c must have shape {(groups, m, n)}, got {tuple(c.shape)}")
         if c.dtype != e.f32:

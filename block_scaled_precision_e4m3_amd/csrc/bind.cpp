@@ -13,7 +13,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <ATen/core/grad_mode.h>
+#include <c10/core/AutogradState.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <hip/hip_runtime_api.h>
@@ -69,11 +69,12 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
 
 PyObject* none() { Py_RETURN_NONE; }
 
-// Whether the call's result needs a history, which the wrapper gives it.
+// Whether the call's result needs a history, backward or forward (a tangent, which no_grad does not end): the wrapper gives it
+// one or refuses.
 bool history(std::initializer_list<const Tensor*> all) {
-  if (!at::GradMode::is_enabled()) return false;
+  const c10::AutogradState& mode = c10::AutogradState::get_tls_state();
   for (const Tensor* t : all)
-    if (t && t->requires_grad()) return true;
+    if (t && ((mode.get_grad_mode() && t->requires_grad()) || (mode.get_fw_grad_mode() && t->_fw_grad(0).defined()))) return true;
   return false;
 }
 
@@ -289,7 +290,7 @@ bool product(PyObject* a, PyObject* sa, PyObject* b, PyObject* sb, PyObject* bia
   if (B.size(nd - 1) != p->k) return false;
   const int64_t kb = cdiv(p->k, 128), want[3] = {groups, cdiv(p->n, 128), kb};
   if (!floats(*p->sa, {kb, p->m}, p->dev) || !floats(*p->sb, {want + 3 - nd, (size_t)nd}, p->dev)) return false;
-  if (history({tb, tg, tr, p->given})) return false;
+  if (history({p->a, p->sa, p->b, p->sb, tb, tg, tr, p->given})) return false;
   at::ScalarType type = p->given ? p->given->scalar_type() : at::kBFloat16;
   if (c_dtype != Py_None) {
     if (!THPDtype_Check(c_dtype)) return false;
@@ -379,7 +380,7 @@ PyObject* grouped_weight_gradient(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const Tensor *a = tensor(v[0], &other), *sa = tensor(v[1], &other), *b = tensor(v[2], &other), *sb = tensor(v[3], &other),
                *offsets = tensor(v[4], &other), *given = tensor(v[5], &other);
   const bool accumulate = truth(v[6]);
-  if (other || !a || !sa || !b || !sb || (accumulate && !given) || history({given})) return none();
+  if (other || !a || !sa || !b || !sb || (accumulate && !given) || history({a, sa, b, sb, given})) return none();
   const int fa = fmt_of(a->scalar_type()), fb = fmt_of(b->scalar_type()), dev = a->is_cuda() ? a->get_device() : -1;
   int64_t groups = 0;
   unsigned flags = kTrusted | (accumulate ? MXG_B128_ACCUMULATE : 0u);
