@@ -18,7 +18,7 @@
 // What the forms cost beside the plain product: 8192 x 24576 x 1536 bfloat16
 // 292 us plain; with bias 315, silu 333, gelu or a gate 391, z kept 355, silu,
 // gate and z kept 459, all of them 539 (three more tensors of 403 MB).  Rows in
-// groups: 16384 of 32, 4096 x 7168, silu and gate, 590 to 610 us (1.6 PFLOP/s: a
+// groups: 16384 of 32, 4096 x 7168, silu and gate, 560 to 590 us (1.7 PFLOP/s: a
 // fifth of the tiles' rows are empty).  Along K: 8192 tokens of 16, 4096 x 2048,
 // 187 to 197 us, of which storing 537 MB costs 37 and the exchange before it 6
 // (builds without them); stored under the next tile's first MFMAs, with a third
